@@ -162,7 +162,7 @@ def _prepare_tables(case, rng, gen):
                 positions=torch.empty(rows, dtype=torch.int32, device=DEVICE),
                 new_seq_lens=torch.empty(n, dtype=torch.int32, device=DEVICE),
                 new_pool_state=torch.empty(2, dtype=torch.int32, device=DEVICE),
-                workspace=torch.empty(4 * n + 64, dtype=torch.int32, device=DEVICE))
+                done_counter=torch.zeros(1, dtype=torch.int32, device=DEVICE))
 
 
 def _cache_shapes(blocks, k_heads, k_size, v_heads, v_size, layout, width):
@@ -259,7 +259,7 @@ def _own_tables(s):
     pa.pa_build_tables(s["block_tables"], s["seq_lens"], s["free_ring"], s["pool_state"], s["slots"],
                        max_seq_len=s["max_seq_len"], keep_lens=s["keep_lens"], query_start=s["query_start"],
                        positions=s["positions"], new_seq_lens=s["new_seq_lens"], new_pool_state=s["new_pool_state"],
-                       workspace=s["workspace"])
+                       done_counter=s["done_counter"])
     return _tables_outputs(s)
 
 

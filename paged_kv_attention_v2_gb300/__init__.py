@@ -1,8 +1,9 @@
 """Paged-KV decode attention for GB300 (sm_103a): Python binding of libpa_decode.so.
 
 This module only marshals torch tensors (device memory and the current CUDA
-stream) into the C ABI of include/pa_decode.h; every step of the computation
-runs in the library's CUDA kernels.  It raises if the library is missing.
+stream) into the C ABI of include/pa_decode.h and include/pa_cache.h (cache.py);
+every step of the computation runs in the library's CUDA kernels.  It raises if
+the library is missing.
 
     out = torch.empty_like(query)
     ws = alloc_workspace(num_seqs, num_heads, head_size, max_seq_len, query.device)
@@ -14,13 +15,14 @@ from __future__ import annotations
 import ctypes
 
 from . import _abi
-from ._abi import (PA_BLOCK_SIZE, PA_DEVERR_BLOCK_ID, PA_DEVERR_SEQ_LEN, PA_DEVERR_TIMEOUT,
-                   PA_PARTITION_SIZE, LibraryMissing)
+from ._abi import (PA_BLOCK_SIZE, PA_DEVERR_BLOCK_ID, PA_DEVERR_POOL, PA_DEVERR_SEQ_LEN, PA_DEVERR_SLOT,
+                   PA_DEVERR_TIMEOUT, PA_PARTITION_SIZE, LibraryMissing)
 
 __all__ = ["pa_decode", "pa_decode_static_workspace", "alloc_workspace", "max_num_partitions", "choose_mode",
            "plan", "plan_for", "status_str",
            "PaDecodeError", "PA_PARTITION_SIZE", "PA_BLOCK_SIZE", "PA_DEVERR_BLOCK_ID",
-           "PA_DEVERR_SEQ_LEN", "PA_DEVERR_TIMEOUT", "LibraryMissing", "library"]
+           "PA_DEVERR_SEQ_LEN", "PA_DEVERR_TIMEOUT", "LibraryMissing", "library",
+           "pa_build_tables", "pa_append_kv", "PA_DEVERR_POOL", "PA_DEVERR_SLOT"]
 
 _LAYOUTS = {"split": _abi.PA_LAYOUT_SPLIT, "nhd": _abi.PA_LAYOUT_NHD}
 _MODES = {"auto": _abi.PA_MODE_AUTO, "v1": _abi.PA_MODE_V1, "v2": _abi.PA_MODE_V2}
@@ -28,8 +30,8 @@ _KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP
 
 
 class PaDecodeError(RuntimeError):
-    def __init__(self, status: int):
-        super().__init__(f"pa_decode failed: {status_str(status)} (status {status})")
+    def __init__(self, status: int, call: str = "pa_decode"):
+        super().__init__(f"{call} failed: {status_str(status)} (status {status})")
         self.status = status
 
 
@@ -247,3 +249,6 @@ def pa_decode_static_workspace(out, query, key_cache, value_cache, block_tables,
         st = library().pa_decode_static_workspace(ctypes.byref(args), ctypes.c_void_p(handle))
     if st != _abi.PA_OK:
         raise PaDecodeError(st)
+
+
+from .cache import pa_append_kv, pa_build_tables  # noqa: E402  (uses the helpers above)

@@ -1,4 +1,4 @@
-"""ctypes view of include/pa_decode.h and loading of libpa_decode.so.
+"""ctypes view of include/pa_decode.h and include/pa_cache.h, and loading of libpa_decode.so.
 
 Loading fails loudly when the library has not been built: there is no other
 implementation behind this package.
@@ -28,14 +28,17 @@ PA_DEVERR_BLOCK_ID = 1
 PA_DEVERR_SEQ_LEN = 2
 PA_DEVERR_TIMEOUT = 4
 PA_DEVERR_QUERY_RANGE = 8
+PA_DEVERR_POOL = 16
+PA_DEVERR_SLOT = 32
 
 PA_PARTITION_SIZE = 512
 PA_BLOCK_SIZE = 16
 
-# every function include/pa_decode.h declares
+# every function include/pa_decode.h and include/pa_cache.h declare
 EXPORTED = ("pa_decode", "pa_max_num_partitions", "pa_workspace_elems", "pa_choose_mode",
             "pa_choose_mode_for_lengths", "pa_workspace_bytes", "pa_partition_size", "pa_plan",
-            "pa_status_str", "pa_version", "pa_decode_static_workspace", "pa_debug_withhold_page")
+            "pa_status_str", "pa_version", "pa_decode_static_workspace", "pa_debug_withhold_page",
+            "pa_build_tables", "pa_append_kv")
 
 PA_STATIC_WORKSPACE_FLOATS = 4 * 1024 * 1024
 PA_FUSED_MAX_PARTITIONS = 8
@@ -96,6 +99,56 @@ class PaLaunchPlan(ctypes.Structure):
     ]
 
 
+class PaTablesArgs(ctypes.Structure):
+    _fields_ = [
+        ("block_tables", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("keep_lens", ctypes.c_void_p),
+        ("query_start", ctypes.c_void_p),
+        ("free_ring", ctypes.c_void_p),
+        ("pool_state", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("new_seq_lens", ctypes.c_void_p),
+        ("new_pool_state", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("dev_error", ctypes.c_void_p),
+        ("done_counter", ctypes.c_void_p),
+    ]
+
+
+class PaAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("key", ctypes.c_void_p),
+        ("value", ctypes.c_void_p),
+        ("key_cache", ctypes.c_void_p),
+        ("value_cache", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("key_stride", ctypes.c_int64),
+        ("key_head_stride", ctypes.c_int64),
+        ("value_stride", ctypes.c_int64),
+        ("value_head_stride", ctypes.c_int64),
+        ("num_tokens", ctypes.c_int32),
+        ("num_key_heads", ctypes.c_int32),
+        ("key_head_size", ctypes.c_int32),
+        ("num_value_heads", ctypes.c_int32),
+        ("value_head_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("dev_error", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -137,6 +190,10 @@ def load(path: Path | None = None):
     lib.pa_plan.restype = ctypes.c_int
     lib.pa_debug_withhold_page.argtypes = [ctypes.c_int32, ctypes.c_int64]
     lib.pa_debug_withhold_page.restype = ctypes.c_int
+    lib.pa_build_tables.argtypes = [ctypes.POINTER(PaTablesArgs), ctypes.c_void_p]
+    lib.pa_build_tables.restype = ctypes.c_int
+    lib.pa_append_kv.argtypes = [ctypes.POINTER(PaAppendArgs), ctypes.c_void_p]
+    lib.pa_append_kv.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib

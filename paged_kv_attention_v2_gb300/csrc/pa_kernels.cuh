@@ -86,6 +86,7 @@ struct Params {
     int kv_evict_first;      // KV page copies marked evict_first (partition outputs small against L2)
     int32_t* tile_ctr;       // [2] dynamic schedule: tiles claimed, CTAs done (NULL: static schedule)
     int metadata_ready;      // block tables / lengths / query_start final: read before the grid wait
+    uint32_t zero;           // 0 (mbar_arrive_after)
 };
 
 struct TileDesc {
@@ -917,7 +918,8 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm.td_empty + slot * 8);  // Q and descriptor are in registers
+        // Q and descriptor are in registers (lane 0 takes part in the last read)
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qb[NTW - 1][KT - 1][1], p.zero);
 
         float sl[NTW][2];
 #pragma unroll
@@ -1028,7 +1030,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
                                       vf[mt][3]);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sm.empty + st * 8);
+                if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vf[KT - 1][3], p.zero);
             }
 
             // logits, online softmax, P as B fragments of P.V
@@ -1070,6 +1072,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
             }
 
             // acc^T[head dim][head] += V^T . P^T
+            uint32_t vlast = 0;  // the page's last read
 #pragma unroll
             for (int mt = 0; mt < KT; ++mt) {
                 uint32_t a0, a1, a2, a3;
@@ -1083,6 +1086,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
                 } else {
                     ldsm_x4_trans(vp + v_frag_off<LAYOUT>(lane, mt), a0, a1, a2, a3);
                 }
+                vlast = a3;
 #pragma unroll
                 for (int nt = 0; nt < NTW; ++nt) {
                     mma_16816<BF>(acc[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
@@ -1091,7 +1095,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
             }
             if constexpr (!kEarlyV) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sm.empty + st * 8);
+                if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vlast, p.zero);
             }
         }
 
@@ -1272,7 +1276,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
         }
         if (q_clamped) report(p, PA_DEVERR_QUERY_RANGE);
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm.td_empty + slot * 8);
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qb[NT - 1][KT - 1][1], p.zero);
 
         float sl[NT][2];
 #pragma unroll
@@ -1384,7 +1388,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                     ldsm_x4(vp + v8_frag_off<LAYOUT, HEAD>(lane, mt), vw[mt / 2][0], vw[mt / 2][1],
                             vw[mt / 2][2], vw[mt / 2][3]);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sm.empty + st * 8);
+                if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vw[KT / 2 - 1][3], p.zero);
             }
 
             uint32_t pb[NT][2];
@@ -1419,6 +1423,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
             // turns each 8 x 8 block (tokens x head dims 16mt + 4cq + {0,1} or
             // {2,3}) into the A fragment, whose rows are then head dims 16mt +
             // tau(r) (rows r) and 16mt + tau(r) + 2 (rows r + 8).
+            uint32_t vlast = 0;  // the page's last read
 #pragma unroll
             for (int mt = 0; mt < KT; mt += 2) {
                 // words of rows r and r + 8 (head dims, or tokens for NHD) of
@@ -1432,6 +1437,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                 } else {
                     ldsm_x4(vp + v8_frag_off<LAYOUT, HEAD>(lane, mt), w[0], w[1], w[2], w[3]);
                 }
+                vlast = w[3];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t a0, a1, a2, a3;
@@ -1454,7 +1460,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
             }
             if constexpr (!kEarlyV) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sm.empty + st * 8);
+                if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vlast, p.zero);
             }
         }
 
@@ -1565,7 +1571,8 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                     }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm.td_empty + slot * 8);  // Q and descriptor are in registers
+        // Q and descriptor are in registers (lane 0 takes part in the last read)
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qa[NT - 1][KT - 1][1], p.zero);
 
         float sl[NT][2];
         int klo[NT][2], khi[NT][2];  // key range of this lane's rows within the tile
@@ -1721,6 +1728,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 
             // acc^T[head dim][row] += V^T . P^T; A fragment of (m-tile mt,
             // k-step ks): head dims 16mt + r / + 8 by k-indices cq / cq + 4
+            uint32_t vlast = 0;  // the page's last read
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -1743,6 +1751,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a[e]) : "r"(va));
                         }
                     }
+                    vlast = a[3];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
 #pragma unroll
@@ -1757,7 +1766,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(sm.empty + st * 8);
+            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vlast, p.zero);
         }
 
         float* mw = sm.merge + warp * C::kMergeRows * C::kMergeStride;

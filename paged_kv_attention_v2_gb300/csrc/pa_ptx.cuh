@@ -29,6 +29,19 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
                  : "memory");
 }
 
+// One lane's arrival for its warp, once the warp's last read of the buffer that
+// the barrier guards has returned: `read` is a register that this read filled,
+// and the barrier's address depends on it (`zero` is 0, but not to the
+// compiler).  Program order alone does not do: the arrival may overtake
+// ldmatrix / ld.shared still queued behind other warps' shared-memory accesses,
+// and the next bulk copy into the buffer then overwrites what they are yet to
+// read (measured: with neighbours zeroing page tails, one fp32 call in a
+// hundred).  Shared-memory reads of a warp return in order, so the last one
+// stands for all.
+__device__ __forceinline__ void mbar_arrive_after(uint32_t bar, uint32_t read, uint32_t zero) {
+    mbar_arrive(bar + (read & zero));
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile(
         "{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),

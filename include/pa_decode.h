@@ -348,6 +348,51 @@ typedef struct pa_launch_plan {
 pa_status pa_plan(const pa_decode_args* args, pa_launch_plan* plan);
 
 /*
+ * Differential attention over the paged cache: each head is the difference of
+ * two softmax maps over one value head twice as wide, with a learned weight
+ * lambda, then an RMS norm of its own:
+ *     o = sum_t (softmax_t(z1) - lambda * softmax_t(z2)) V_g(t)
+ *     z1_t = scale * <query[row][h][0], K_g[0](t)>,  z2_t = scale * <query[row][h][1], K_g[1](t)>
+ *     out[row][h] = out_scale * norm_weight * o / sqrt(mean(o^2) + norm_eps)     with norm
+ *     out[row][h] = out_scale * o                                                without
+ * with softcap, alibi_slopes, sliding_window, fp8 caches and query_start as in
+ * pa_decode, applied to both maps' logits.  Sums, statistics and the norm are
+ * fp32; the output is rounded once.  A row that sees no key gets zeros.
+ * (The pages have no counterpart.)
+ *
+ * `decode` describes the call as for pa_decode, with these differences, where
+ * num_heads and num_kv_heads count differential heads and head_size (64 or 128)
+ * is that of a query or key of one map:
+ *   query        [rows][num_heads][2][head_size]
+ *   out          [rows][num_heads][2 * head_size]
+ *   key_cache    the layouts of pa_layout with 2 * num_kv_heads heads of
+ *                head_size: heads 2g and 2g + 1 hold the keys of the two maps of kv head g
+ *   value_cache  num_kv_heads heads of 2 * head_size
+ *   exp_sums, max_logits [rows][num_heads][2][P], tmp_out [rows][num_heads][2][P][2 * head_size]:
+ *                Phase 1 statistics per map, before lambda and norm (pa_workspace_elems
+ *                with 2 * num_heads heads of 2 * head_size)
+ *   max_query_len * (num_heads / num_kv_heads) <= 8  (one tile holds both maps' rows)
+ */
+typedef struct pa_diff_args {
+    pa_decode_args decode;
+    /* lambda of (row, head) at lambdas[row * lambda_row_stride + head], fp32: [num_heads]
+     * with stride 0, or one per row (a lambda that depends on the token).  Usually
+     * exp(<q1, k1>) - exp(<q2, k2>) + lambda_init of the layer's learned vectors. */
+    const float* lambdas;
+    int64_t lambda_row_stride;   /* >= 0 */
+    const float* norm_weight;    /* [2 * head_size] fp32, or NULL (ones); used with norm */
+    float norm_eps;              /* > 0 with norm */
+    float out_scale;             /* e.g. 1 - lambda_init */
+    int32_t norm;                /* non-zero: RMS norm of each head's output */
+} pa_diff_args;
+
+/* Enqueue one differential decode; statuses and errors as pa_decode. */
+pa_status pa_diff_decode(const pa_diff_args* args, void* stream);
+
+/* What pa_diff_decode would launch (as pa_plan). */
+pa_status pa_diff_plan(const pa_diff_args* args, pa_launch_plan* plan);
+
+/*
  * Test hook for the bounded waits of the kernels (failure detection without a
  * GPU fault).  While `enable` is non-zero, every later pa_decode call of this
  * process withholds the copy of the first page of one CTA, so the consumer

@@ -22,7 +22,8 @@ __all__ = ["pa_decode", "pa_decode_static_workspace", "alloc_workspace", "max_nu
            "plan", "plan_for", "status_str",
            "PaDecodeError", "PA_PARTITION_SIZE", "PA_BLOCK_SIZE", "PA_DEVERR_BLOCK_ID",
            "PA_DEVERR_SEQ_LEN", "PA_DEVERR_TIMEOUT", "LibraryMissing", "library",
-           "pa_build_tables", "pa_append_kv", "PA_DEVERR_POOL", "PA_DEVERR_SLOT"]
+           "pa_build_tables", "pa_append_kv", "pa_diff_decode", "alloc_diff_workspace", "diff_plan",
+           "PA_DEVERR_POOL", "PA_DEVERR_SLOT"]
 
 _LAYOUTS = {"split": _abi.PA_LAYOUT_SPLIT, "nhd": _abi.PA_LAYOUT_NHD}
 _MODES = {"auto": _abi.PA_MODE_AUTO, "v1": _abi.PA_MODE_V1, "v2": _abi.PA_MODE_V2}
@@ -251,4 +252,5 @@ def pa_decode_static_workspace(out, query, key_cache, value_cache, block_tables,
         raise PaDecodeError(st)
 
 
-from .cache import pa_append_kv, pa_build_tables  # noqa: E402  (uses the helpers above)
+from .cache import pa_append_kv, pa_build_tables  # noqa: E402
+from .diff import alloc_diff_workspace, diff_plan, pa_diff_decode  # noqa: E402

@@ -38,7 +38,7 @@ PA_BLOCK_SIZE = 16
 EXPORTED = ("pa_decode", "pa_max_num_partitions", "pa_workspace_elems", "pa_choose_mode",
             "pa_choose_mode_for_lengths", "pa_workspace_bytes", "pa_partition_size", "pa_plan",
             "pa_status_str", "pa_version", "pa_decode_static_workspace", "pa_debug_withhold_page",
-            "pa_build_tables", "pa_append_kv")
+            "pa_build_tables", "pa_append_kv", "pa_diff_decode", "pa_diff_plan")
 
 PA_STATIC_WORKSPACE_FLOATS = 4 * 1024 * 1024
 PA_FUSED_MAX_PARTITIONS = 8
@@ -96,6 +96,18 @@ class PaLaunchPlan(ctypes.Structure):
         ("dynamic_schedule", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
         ("tiles", ctypes.c_int64),
+    ]
+
+
+class PaDiffArgs(ctypes.Structure):
+    _fields_ = [
+        ("decode", PaDecodeArgs),
+        ("lambdas", ctypes.c_void_p),
+        ("lambda_row_stride", ctypes.c_int64),
+        ("norm_weight", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float),
+        ("out_scale", ctypes.c_float),
+        ("norm", ctypes.c_int32),
     ]
 
 
@@ -190,6 +202,10 @@ def load(path: Path | None = None):
     lib.pa_plan.restype = ctypes.c_int
     lib.pa_debug_withhold_page.argtypes = [ctypes.c_int32, ctypes.c_int64]
     lib.pa_debug_withhold_page.restype = ctypes.c_int
+    lib.pa_diff_decode.argtypes = [ctypes.POINTER(PaDiffArgs), ctypes.c_void_p]
+    lib.pa_diff_decode.restype = ctypes.c_int
+    lib.pa_diff_plan.argtypes = [ctypes.POINTER(PaDiffArgs), ctypes.POINTER(PaLaunchPlan)]
+    lib.pa_diff_plan.restype = ctypes.c_int
     lib.pa_build_tables.argtypes = [ctypes.POINTER(PaTablesArgs), ctypes.c_void_p]
     lib.pa_build_tables.restype = ctypes.c_int
     lib.pa_append_kv.argtypes = [ctypes.POINTER(PaAppendArgs), ctypes.c_void_p]

@@ -94,6 +94,41 @@ bool make_nhd_map(CUtensorMap* map, const void* base, int64_t rows, int head_siz
     return r == CUDA_SUCCESS;
 }
 
+// Pair of adjacent key heads of a differential cache in the NHD layout: 4-D view
+// (chunk of at most 128 bytes of a row, token, chunk index, page of one head),
+// box = both heads' pages.  In shared memory it lands map by map, each as blocks
+// of 16 rows x 128 bytes (fp8 heads of 64: 64 bytes) with the swizzle of that
+// width, which is the layout of a page of a head twice as wide where a row has
+// whole 128-byte chunks.
+bool make_nhd_pair_map(CUtensorMap* map, const void* base, int64_t pages, int head_size, int elem,
+                       CUtensorMapDataType t) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int row = head_size * elem, chunk = row < 128 ? row : 128;
+    cuuint64_t dims[4] = {(cuuint64_t)(chunk / elem), PA_BLOCK_SIZE, (cuuint64_t)(row / chunk), (cuuint64_t)pages};
+    cuuint64_t strides[3] = {(cuuint64_t)row, (cuuint64_t)chunk, (cuuint64_t)row * PA_BLOCK_SIZE};
+    cuuint32_t box[4] = {(cuuint32_t)(chunk / elem), PA_BLOCK_SIZE, (cuuint32_t)(row / chunk), 2};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, t, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    chunk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// fp8 NHD value page of 256 bytes a row: two blocks of 16 rows x 128 bytes.
+bool make_nhd_map_fp8_wide(CUtensorMap* map, const void* base, int64_t rows, int head_size) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {128, (cuuint64_t)rows, (cuuint64_t)(head_size / 128)};
+    cuuint64_t strides[2] = {(cuuint64_t)head_size, 128};
+    cuuint32_t box[3] = {128, PA_BLOCK_SIZE, (cuuint32_t)(head_size / 128)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // fp8 NHD page of one kv head = 16 rows of head_size bytes: one box of the
 // whole page, swizzled by 128 bytes (head_size 128) or 64 bytes (64) so the
 // kernel's four-byte reads of eight token rows fall in distinct banks.
@@ -171,6 +206,7 @@ struct Prepared {
     int kv = PA_KV_SAME;
     int ctas_per_sm = 0;
     bool empty = false;  // num_seqs == 0: nothing to launch
+    bool diff = false;   // differential attention
 };
 
 // The kernels of the (query type, cache type) pair: launch them, or with
@@ -179,6 +215,15 @@ pa_status dispatch(Prepared& pr, pa::LaunchOut* out) {
     pr.la.query = out;
     const int kvk = pr.kv == PA_KV_FP8_E4M3 ? pa::kKvE4M3 : pa::kKvE5M2;
     cudaError_t e;
+    if (pr.diff) {
+        const bool same = pr.kv == PA_KV_SAME;
+        switch (pr.la.dtype) {
+        case PA_DTYPE_F32: e = pa::launch_diff_f32(pr.p, pr.la); break;
+        case PA_DTYPE_F16: e = same ? pa::launch_diff_f16(pr.p, pr.la) : pa::launch_diff_f16_fp8(pr.p, pr.la, kvk); break;
+        default: e = same ? pa::launch_diff_bf16(pr.p, pr.la) : pa::launch_diff_bf16_fp8(pr.p, pr.la, kvk); break;
+        }
+        return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    }
     switch (pr.la.dtype) {
     case PA_DTYPE_F32: e = pa::launch_f32(pr.p, pr.la); break;
     case PA_DTYPE_F16: e = pr.kv == PA_KV_SAME ? pa::launch_f16(pr.p, pr.la) : pa::launch_f16_fp8(pr.p, pr.la, kvk); break;
@@ -188,8 +233,10 @@ pa_status dispatch(Prepared& pr, pa::LaunchOut* out) {
 }
 
 // Host-visible checks of pa_decode (every error returned before any launch),
-// then the kernel parameters, the v1 / v2 choice and the tile order.
-pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr) {
+// then the kernel parameters, the v1 / v2 choice and the tile order.  With `df`
+// (whose decode member `a` is) the call is a differential one: num_heads and
+// num_kv_heads count differential heads, head_size is that of the keys.
+pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_diff_args* df = nullptr) {
     if (!a) return PA_ERR_INVALID_ARG;
     if (a->num_seqs < 0 || a->num_heads <= 0 || a->num_kv_heads <= 0 || a->max_seq_len < 0 ||
         a->num_blocks < 0 || a->max_blocks_per_seq < 0)
@@ -209,20 +256,26 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr) {
     if (a->block_size != PA_BLOCK_SIZE) return PA_ERR_UNSUPPORTED;
     if (a->head_size != 64 && a->head_size != 128) return PA_ERR_UNSUPPORTED;
     const int group = a->num_heads / a->num_kv_heads;
-    if (group > 16) return PA_ERR_UNSUPPORTED;
+    // MMA columns of a tile: 16, two per row (one per map) in a differential call
+    const int max_rows = df ? 8 : 16;
+    if (group > max_rows) return PA_ERR_UNSUPPORTED;
     // several query tokens per sequence: all tokens of a (sequence, kv head)
     // share one tile, their group rows side by side (at most 16)
     const bool multi = a->query_start != nullptr;
     const int max_q = multi ? a->max_query_len : 1;
     if (multi && (a->max_query_len < 1 || a->num_query_tokens < 0 || !aligned(a->query_start, 4)))
         return PA_ERR_INVALID_ARG;
-    if ((int64_t)max_q * group > 16) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)max_q * group > max_rows) return PA_ERR_UNSUPPORTED;
+    if (df && (!std::isfinite(df->norm_eps) || !std::isfinite(df->out_scale) || (df->norm != 0 && df->norm_eps <= 0.f) ||
+               df->lambda_row_stride < 0))
+        return PA_ERR_INVALID_ARG;
     if (a->num_seqs == 0) {
         pr.empty = true;
         return PA_OK;
     }
     if (!a->out || !a->query || !a->key_cache || !a->value_cache || !a->block_tables || !a->seq_lens)
         return PA_ERR_INVALID_ARG;
+    if (df && (!df->lambdas || !aligned(df->lambdas, 4) || !aligned(df->norm_weight, 4))) return PA_ERR_INVALID_ARG;
     if (a->num_blocks == 0) return PA_ERR_INVALID_ARG;
     if ((int64_t)a->max_blocks_per_seq * PA_BLOCK_SIZE < (int64_t)a->max_seq_len)
         return PA_ERR_INVALID_ARG;
@@ -280,6 +333,14 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr) {
     p.withhold_page = g_withhold_page.load();
     p.tile_ctr = nullptr;  // set below once the mode is known
     p.metadata_ready = a->metadata_ready ? 1 : 0;
+    if (df) {
+        p.lambdas = df->lambdas;
+        p.lambda_stride = df->lambda_row_stride;
+        p.norm_weight = df->norm_weight;
+        p.norm_eps = df->norm_eps;
+        p.out_scale = df->out_scale;
+        p.norm = df->norm != 0;
+    }
 
     pa::LaunchArgs& la = pr.la;
     std::memset(&la, 0, sizeof la);
@@ -289,9 +350,10 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr) {
     std::memset(&pr.tmk, 0, sizeof pr.tmk);
     std::memset(&pr.tmv, 0, sizeof pr.tmv);
     la.sm_count = sm;
-    la.group_tiles = max_q * group > 8 ? 2 : 1;
+    la.group_tiles = max_q * group > max_rows / 2 ? 2 : 1;
     la.layout = a->layout;
-    la.head_size = a->head_size;
+    la.head_size = df ? 2 * a->head_size : a->head_size;  // of the values
+    pr.diff = df != nullptr;
     la.dtype = a->dtype;
     la.ev_begin = a->event_main_begin;
     la.ev_end = a->event_main_end;
@@ -336,9 +398,29 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr) {
         int l2 = 0;
         if (l2_bytes_for_current_device(&l2) != 0) return PA_ERR_LAUNCH;
         const int64_t rows = multi ? a->num_query_tokens : a->num_seqs;
-        const int64_t tmp_bytes = v1 ? 0 : rows * a->num_heads * (int64_t)max_parts * a->head_size * 4;
+        const int64_t heads = df ? 2 * (int64_t)a->num_heads : a->num_heads;  // rows of tmp_out
+        const int64_t tmp_bytes = v1 ? 0 : rows * heads * max_parts * la.head_size * 4;
         p.kv_evict_first = tmp_bytes <= (int64_t)l2 / 2 ? 1 : 0;
     }
+    return PA_OK;
+}
+
+// What a call would launch (pa_plan, pa_diff_plan).
+pa_status plan_of(const pa_decode_args* a, const pa_diff_args* df, Prepared& pr, pa_launch_plan* plan) {
+    if (!plan) return PA_ERR_INVALID_ARG;
+    std::memset(plan, 0, sizeof *plan);
+    const pa_status st = prepare(a, nullptr, pr, df);
+    if (st != PA_OK || pr.empty) return st;
+    pa::LaunchOut lo;
+    const pa_status q = dispatch(pr, &lo);
+    if (q != PA_OK) return q;
+    plan->mode = pr.p.v1 ? PA_MODE_V1 : PA_MODE_V2;
+    plan->merge_in_kernel = lo.fused ? 1 : 0;
+    plan->kernels = (pr.p.v1 || lo.fused) ? 1 : 2;
+    plan->ctas_per_sm = pr.ctas_per_sm;
+    plan->grid = (int32_t)lo.grid;
+    plan->dynamic_schedule = pr.p.tile_ctr ? 1 : 0;
+    plan->tiles = pr.la.tiles_upper;
     return PA_OK;
 }
 
@@ -407,22 +489,13 @@ pa_status pa_debug_withhold_page(int32_t enable, int64_t wait_limit_ns) {
 }
 
 pa_status pa_plan(const pa_decode_args* a, pa_launch_plan* plan) {
-    if (!plan) return PA_ERR_INVALID_ARG;
-    std::memset(plan, 0, sizeof *plan);
     Prepared pr;
-    const pa_status st = prepare(a, nullptr, pr);
-    if (st != PA_OK || pr.empty) return st;
-    pa::LaunchOut lo;
-    const pa_status q = dispatch(pr, &lo);
-    if (q != PA_OK) return q;
-    plan->mode = pr.p.v1 ? PA_MODE_V1 : PA_MODE_V2;
-    plan->merge_in_kernel = lo.fused ? 1 : 0;
-    plan->kernels = (pr.p.v1 || lo.fused) ? 1 : 2;
-    plan->ctas_per_sm = pr.ctas_per_sm;
-    plan->grid = (int32_t)lo.grid;
-    plan->dynamic_schedule = pr.p.tile_ctr ? 1 : 0;
-    plan->tiles = pr.la.tiles_upper;
-    return PA_OK;
+    return plan_of(a, nullptr, pr, plan);
+}
+
+pa_status pa_diff_plan(const pa_diff_args* a, pa_launch_plan* plan) {
+    Prepared pr;
+    return plan_of(a ? &a->decode : nullptr, a, pr, plan);
 }
 
 pa_status pa_decode(const pa_decode_args* a, void* stream) {
@@ -438,6 +511,34 @@ pa_status pa_decode(const pa_decode_args* a, void* stream) {
                                   make_nhd_map_fp8(&pr.tmv, a->value_cache, rows, a->head_size)
                             : make_nhd_map(&pr.tmk, a->key_cache, rows, a->head_size, (pa_dtype)a->dtype) &&
                                   make_nhd_map(&pr.tmv, a->value_cache, rows, a->head_size, (pa_dtype)a->dtype);
+        if (!ok) return PA_ERR_LAUNCH;
+    }
+    return dispatch(pr, nullptr);
+}
+
+pa_status pa_diff_decode(const pa_diff_args* args, void* stream) {
+    if (!args) return PA_ERR_INVALID_ARG;
+    const pa_decode_args* a = &args->decode;
+    Prepared pr;
+    const pa_status st = prepare(a, stream, pr, args);
+    if (st != PA_OK || pr.empty) return st;
+    if (a->layout == PA_LAYOUT_NHD) {
+        const int64_t rows = (int64_t)a->num_blocks * a->num_kv_heads * PA_BLOCK_SIZE;  // of the value cache
+        if (rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;  // tensor-map row coordinate is int32
+        const int64_t key_pages = 2 * (int64_t)a->num_blocks * a->num_kv_heads;
+        const int vs = 2 * a->head_size;
+        bool ok;
+        if (pr.kv != PA_KV_SAME) {
+            ok = make_nhd_pair_map(&pr.tmk, a->key_cache, key_pages, a->head_size, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8) &&
+                 (vs > 128 ? make_nhd_map_fp8_wide(&pr.tmv, a->value_cache, rows, vs)
+                           : make_nhd_map_fp8(&pr.tmv, a->value_cache, rows, vs));
+        } else {
+            const CUtensorMapDataType t = a->dtype == PA_DTYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                          : a->dtype == PA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+            ok = make_nhd_pair_map(&pr.tmk, a->key_cache, key_pages, a->head_size, a->dtype == PA_DTYPE_F32 ? 4 : 2, t) &&
+                 make_nhd_map(&pr.tmv, a->value_cache, rows, vs, (pa_dtype)a->dtype);
+        }
         if (!ok) return PA_ERR_LAUNCH;
     }
     return dispatch(pr, nullptr);

@@ -54,6 +54,12 @@ constexpr int kStagesF32x2 = 8;    // fp32 caches, two n-tiles (one CTA per SM)
 constexpr int kConsumerWarps = 4;  // consumer warps per CTA
 constexpr int kConsumerWarps5 = 5; // consumer warps per CTA, 16-bit or fp32 caches with one n-tile
 constexpr int kPrefetchPages = 16; // pages of the first tile prefetched into L2 before the grid wait
+// Value heads of 256 (differential attention with keys of 128): stages twice as
+// large, one CTA per SM.
+constexpr int kStages16Wide = 8;   // 16-bit caches: 16 KB each, eight consumer warps
+constexpr int kStagesFp8Wide = 16; // fp8 caches: 8 KB each, eight consumer warps
+constexpr int kStagesF32Wide = 4;  // fp32 caches: 32 KB each, four consumer warps
+constexpr int kConsumerWarpsWide = 8;
 constexpr int kReduceWarpMaxParts = 64;  // warp-per-row reduce up to this many partitions per row
 
 constexpr int kReduceWarpsPerCta = 8;  // warp-per-row reduce: rows per CTA
@@ -87,6 +93,13 @@ struct Params {
     int32_t* tile_ctr;       // [2] dynamic schedule: tiles claimed, CTAs done (NULL: static schedule)
     int metadata_ready;      // block tables / lengths / query_start final: read before the grid wait
     uint32_t zero;           // 0 (mbar_arrive_after)
+    // differential attention (the DIFF kernels): num_heads and group count
+    // differential heads; statistics and tmp_out have two rows per head, one per map
+    const float* lambdas;    // lambda of (row, head) at row * lambda_stride + head
+    int64_t lambda_stride;
+    const float* norm_weight;  // [value head size], or NULL (ones)
+    float norm_eps, out_scale;
+    int norm;                // RMS norm of each head's output
 };
 
 struct TileDesc {
@@ -145,9 +158,19 @@ __device__ __forceinline__ int tile_pages(int tb, int te) {
 // ------------------------------------------------------------------ config
 
 template <typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV = kKvSame,
-          bool MQ = false>
+          bool MQ = false, bool DIFF = false>
 struct Cfg {
     static constexpr bool kMQ = MQ;  // several query tokens per sequence (query_start given)
+    // Differential attention: HEAD is the value head size 2d.  A pair of adjacent
+    // key heads of d is one page of HEAD, [q1 | q2] one query row of HEAD, so
+    // pages and queries move as they do for HEAD.  MMA column v (of NT * 8) is
+    // map v / kRows of query row v % kRows: one n-tile holds both maps of up to
+    // four rows, its B fragments zero where a column meets the other map's
+    // keys; with two n-tiles each is one map of up to eight rows, and a warp of a
+    // pair reads only its map's half of the key page.
+    static constexpr bool kDiff = DIFF;
+    static constexpr int kRows = DIFF ? NT * 4 : NT * 8;  // query rows (heads x query tokens)
+    static constexpr int row_of(int v) { return DIFF ? v % kRows : v; }
     static constexpr bool kF32 = std::is_same<T, float>::value;
     static constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
     static constexpr int kElem = sizeof(T);                // query / output element
@@ -159,13 +182,14 @@ struct Cfg {
     // stages: measured, long100k_fp8 NHD 83.1 -> 75.9 µs and gqa4k_fp8 NHD
     // 34.2 -> 32.7 µs for the one-page stages.)
     static constexpr int kStageBytes = 2 * kPageBytes;  // K page, then V page
-    static constexpr int kMaxG = NT * 8;                   // rows (heads x query tokens) handled
-    // 16-bit caches with two n-tiles: warps in pairs of page streams, one
-    // n-tile each (consumer_mma); every page is consumed by two warps.
-    static constexpr bool kPairs = NT == 2 && KV == kKvSame && !kF32;
+    static constexpr int kMaxG = NT * 8;                   // MMA columns: rows (heads x query tokens) handled
+    // 16-bit caches with two n-tiles, and every differential kernel with two:
+    // warps in pairs of page streams, one n-tile each; every page is consumed by
+    // two warps.
+    static constexpr bool kPairs = NT == 2 && (DIFF || (KV == kKvSame && !kF32));
     static constexpr int kMergeRows = kPairs ? 8 : kMaxG;  // merge-buffer rows per warp
     static constexpr int kPageWarps = kPairs ? 2 : 1;      // warps that release each page
-    static constexpr int kQBytes = kMaxG * HEAD * kElem;
+    static constexpr int kQBytes = kRows * HEAD * kElem;
     static constexpr int kTD = 2;                          // tile descriptor ring depth
     static constexpr int kMergeStride = HEAD + 4;          // floats; +4 breaks bank conflicts
     static constexpr int kThreads = (NC + 1) * 32;
@@ -481,14 +505,24 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
                         if constexpr (C::kTensorMap && C::kKvElem == 1) {
                             // fp8 NHD: one box of 16 token rows x HEAD bytes per page
                             const int y = (int)(page * kBS);
-                            tensor2d_g2s_hint(dk, tmk, 0, y, fb, kvpol);
-                            tensor2d_g2s_hint(dv, tmv, 0, y, fb, kvpol);
+                            if constexpr (C::kDiff)
+                                tensor4d_g2s_hint(dk, tmk, 0, 0, 0, (int)(2 * page), fb, kvpol);
+                            else
+                                tensor2d_g2s_hint(dk, tmk, 0, y, fb, kvpol);
+                            if constexpr (HEAD > 128)  // two boxes of 128 bytes a row
+                                tensor3d_g2s_hint(dv, tmv, 0, y, 0, fb, kvpol);
+                            else
+                                tensor2d_g2s_hint(dv, tmv, 0, y, fb, kvpol);
                         } else if constexpr (C::kTensorMap) {
                             // 16-bit / fp32 NHD: the whole page in one box of the
                             // 3-D view (128-byte chunk of a row, row, chunk index),
                             // staged as HEAD * elem / 128 blocks of 16 rows x 128 bytes
+                            // (a pair of key heads: the same blocks, map by map)
                             const int y = (int)(page * kBS);
-                            tensor3d_g2s_hint(dk, tmk, 0, y, 0, fb, kvpol);
+                            if constexpr (C::kDiff)
+                                tensor4d_g2s_hint(dk, tmk, 0, 0, 0, (int)(2 * page), fb, kvpol);
+                            else
+                                tensor3d_g2s_hint(dk, tmk, 0, y, 0, fb, kvpol);
                             tensor3d_g2s_hint(dv, tmv, 0, y, 0, fb, kvpol);
                         } else {
                             bulk_g2s_hint(dk, kbase + page * C::kPageBytes, C::kPageBytes, fb, kvpol);
@@ -550,6 +584,101 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
 
 // ------------------------------------------------------------------ epilogue
 
+// Columns of an output row that a lane of a warp holds: VEC = HEAD / 32, in
+// groups of at most four successive ones.
+template <int HEAD>
+__device__ __forceinline__ int lane_col(int lane, int v) {
+    constexpr int VEC = HEAD / 32;
+    return VEC <= 4 ? lane * VEC + v : (v >> 2) * 128 + lane * 4 + (v & 3);
+}
+
+// Write row `o` of an output of type T, VEC columns per lane (lane_col).
+template <typename T, int HEAD>
+__device__ __forceinline__ void store_row(T* row, const float (&o)[HEAD / 32], int lane) {
+    constexpr int VEC = HEAD / 32;
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+#pragma unroll
+    for (int v = 0; v < VEC; v += (VEC < 4 ? VEC : 4)) {
+        T* dst = row + lane_col<HEAD>(lane, v);
+        if constexpr (std::is_same<T, float>::value) {
+            if constexpr (VEC >= 4)
+                *reinterpret_cast<float4*>(dst) = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
+            else
+                *reinterpret_cast<float2*>(dst) = make_float2(o[v], o[v + 1]);
+        } else if constexpr (VEC >= 4) {
+            uint2 w;
+            w.x = pack2<BF>(o[v], o[v + 1]);
+            w.y = pack2<BF>(o[v + 2], o[v + 3]);
+            *reinterpret_cast<uint2*>(dst) = w;
+        } else {
+            *reinterpret_cast<uint32_t*>(dst) = pack2<BF>(o[v], o[v + 1]);
+        }
+    }
+}
+
+// The output row of a differential head from its two maps' outputs, by one warp:
+//     o = o1 - lambda o2,  y = out_scale * weight * o / sqrt(mean(o^2) + eps)
+// (without the norm y = out_scale * o).  All in fp32; one rounding at the store.
+template <typename T, int HEAD>
+__device__ __forceinline__ void diff_row(const Params& p, int64_t row, int h, float (&o1)[HEAD / 32],
+                                         const float (&o2)[HEAD / 32], int lane) {
+    constexpr int VEC = HEAD / 32;
+    const float lambda = __ldg(p.lambdas + row * p.lambda_stride + h);
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        o1[v] = fmaf(-lambda, o2[v], o1[v]);
+        ss = fmaf(o1[v], o1[v], ss);
+    }
+    float sc = p.out_scale;
+    if (p.norm) {
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+        sc *= rsqrtf(ss * (1.f / HEAD) + p.norm_eps);
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        o1[v] *= sc;
+        if (p.norm && p.norm_weight) o1[v] *= __ldg(p.norm_weight + lane_col<HEAD>(lane, v));
+    }
+    store_row<T, HEAD>(static_cast<T*>(p.out) + (row * p.num_heads + h) * HEAD, o1, lane);
+}
+
+// v1 output of a differential tile: one query row per consumer warp at a time,
+// both maps merged over the warps that hold them.
+template <class C, typename T, int HEAD, int NC>
+__device__ void diff_tile_output(const Params& p, const TileDesc& d, const Smem& sm, int warp, int lane) {
+    constexpr int VEC = HEAD / 32;
+    constexpr int WR = NC / C::kPageWarps;
+    const int G = p.group, n = (C::kMQ ? d.qn : 1) * G;
+    for (int r = warp; r < n; r += NC) {
+        float o[2][VEC];
+#pragma unroll
+        for (int map = 0; map < 2; ++map) {
+            const int w0 = C::kPairs ? map * WR : 0, hl = C::kPairs ? r : map * C::kRows + r;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < WR; ++w) M = fmaxf(M, sm.ml[(w0 + w) * C::kMergeRows + hl].x);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) o[map][v] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WR; ++w) {
+                const float2 e = sm.ml[(w0 + w) * C::kMergeRows + hl];
+                const float c = e.x == -INFINITY ? 0.f : exp2f((e.x - M) * kLog2e);
+                L = fmaf(c, e.y, L);
+                const float* a = sm.merge + ((w0 + w) * C::kMergeRows + hl) * C::kMergeStride;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) o[map][v] = fmaf(c, a[lane_col<HEAD>(lane, v)], o[map][v]);
+            }
+            const float inv = L > 0.f ? p.v_scale / L : 0.f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) o[map][v] *= inv;
+        }
+        const int qi = C::kMQ ? r / G : 0;
+        diff_row<T, HEAD>(p, (int64_t)d.q0 + qi, d.kvh * G + (r - qi * G), o[0], o[1], lane);
+    }
+}
+
 // Merge the NC consumer warps' partial states of one tile and write either the
 // partition statistics (v2) or the final output row (v1).  Each thread owns up
 // to ITEMS (row, 4-column) items; all their shared-memory loads are issued
@@ -560,8 +689,21 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
     constexpr int ITEMS = (C::kMaxG * D4 + NC * 32 - 1) / (NC * 32);
     const int G = p.group;
     // row v of the merge buffers: query token v / G, head kvh * G + v % G
+    // (differential: that of v % kRows, map v / kRows, both maps side by side)
     const int qn = C::kMQ ? d.qn : 1;
-    const int n = qn * G * D4;
+    const int GE = qn * G;
+    const int n = (C::kDiff ? 2 * GE : GE) * D4;
+    if constexpr (C::kDiff) {
+        if (p.v1) {
+            diff_tile_output<C, T, HEAD, NC>(p, d, sm, tid >> 5, tid & 31);
+            return;
+        }
+    }
+    auto column = [&](int idx) {  // item -> merge row
+        const int v = idx / D4;
+        if constexpr (C::kDiff) return v < GE ? v : C::kRows + v - GE;
+        return v;
+    };
     // warps holding a partial state of row h: all of them, or with paired page
     // streams the WR warps of the row's n-tile (its rows at h % 8 of their buffers)
     constexpr int WR = NC / C::kPageWarps;
@@ -570,7 +712,7 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
         const int idx = tid + it * NC * 32;
-        const int h = idx / D4, d4 = idx - h * D4;
+        const int h = column(idx), d4 = idx % D4;
         const int w0 = C::kPairs ? (h >> 3) * WR : 0, hl = C::kPairs ? (h & 7) : h;
 #pragma unroll
         for (int w = 0; w < WR; ++w) {
@@ -588,7 +730,7 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
     for (int it = 0; it < ITEMS; ++it) {
         const int idx = tid + it * NC * 32;
         if (idx >= n) break;
-        const int h = idx / D4, d4 = idx - h * D4;
+        const int col = column(idx), h = C::row_of(col), d4 = idx % D4;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WR; ++w) M = fmaxf(M, e[it][w].x);
@@ -610,8 +752,9 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
         o.w *= inv;
         const int qi = C::kMQ ? h / G : 0;
         const int head = d.kvh * G + (h - qi * G);
-        const int64_t sh = (int64_t)(d.q0 + qi) * p.num_heads + head;
-        if (p.v1) {
+        int64_t sh = (int64_t)(d.q0 + qi) * p.num_heads + head;
+        if constexpr (C::kDiff) sh = 2 * sh + col / C::kRows;  // statistics row of the map
+        if (!C::kDiff && p.v1) {
             T* dst = static_cast<T*>(p.out) + sh * HEAD + 4 * d4;
             if constexpr (C::kF32) {
                 *reinterpret_cast<float4*>(dst) = o;
@@ -642,17 +785,30 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
 template <typename T, int HEAD, bool L2ONLY>
 __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int h, int len, int qn, int qi,
                                                int lane);
+template <int HEAD, bool L2ONLY>
+__device__ __forceinline__ void merge_stats_row(const Params& p, int64_t srow, int h, int len, int qn, int qi,
+                                                int lane, float (&acc)[HEAD / 32]);
 
 // The rows of one (sequence, kv head), one per consumer warp at a time.  Not
 // inlined: its loads then never share a register allocation with the page
 // loop (three fp8 CTAs per SM need the kernel within 128 registers).
-template <typename T, int HEAD, int NC, bool MQ>
+template <typename T, int HEAD, int NC, bool MQ, bool DIFF>
 __device__ __noinline__ void merge_group(const Params& p, int seq_kvh_base, int q0, int qn, int len, int warp,
                                          int lane) {
     const int G = p.group;
     for (int r = warp; r < qn * G; r += NC) {
         const int qi = MQ ? r / G : 0;
-        merge_row_warp<T, HEAD, true>(p, (int64_t)q0 + qi, seq_kvh_base + (r - qi * G), len, qn, qi, lane);
+        if constexpr (DIFF) {
+            const int64_t row = (int64_t)q0 + qi;
+            const int h = seq_kvh_base + (r - qi * G);
+            float o[2][HEAD / 32];
+#pragma unroll
+            for (int map = 0; map < 2; ++map)
+                merge_stats_row<HEAD, true>(p, 2 * (row * p.num_heads + h) + map, h, len, qn, qi, lane, o[map]);
+            diff_row<T, HEAD>(p, row, h, o[0], o[1], lane);
+        } else {
+            merge_row_warp<T, HEAD, true>(p, (int64_t)q0 + qi, seq_kvh_base + (r - qi * G), len, qn, qi, lane);
+        }
     }
 }
 
@@ -680,7 +836,7 @@ __device__ bool tile_finish(const Params& p, const TileDesc& d, const Smem& sm, 
     }
     if (!consumer_sync(sm, mphase, lane)) return false;
     if (sm.abort[2])
-        merge_group<T, HEAD, NC, C::kMQ>(p, d.kvh * p.group, d.q0, C::kMQ ? d.qn : 1, d.len, warp, lane);
+        merge_group<T, HEAD, NC, C::kMQ, C::kDiff>(p, d.kvh * p.group, d.q0, C::kMQ ? d.qn : 1, d.len, warp, lane);
     return true;
 }
 
@@ -787,6 +943,17 @@ __device__ __forceinline__ void settle_max(float (&m)[NT][2], float (&mx)[NT][2]
 
 // ------------------------------------------------------------------ consumers
 
+// What lane 0 hands the query slot back with: its last word, or where one n-tile
+// holds both maps, which lanes 0-15 and 16-31 read one after the other, a
+// combination of both halves' last ones.
+template <class C, int KQ>
+__device__ __forceinline__ uint32_t last_query_word(const uint32_t (&q)[KQ][2]) {
+    if constexpr (C::kDiff && !C::kPairs)
+        return q[KQ / 2 - 1][1] | __shfl_xor_sync(0xffffffffu, q[KQ - 1][1], 16);
+    else
+        return q[KQ - 1][1];
+}
+
 // Byte offset of this lane's ldmatrix row address inside a K page for k-step kk
 // (A operand of Q.K^T: rows = 16 tokens, columns = head dims 16kk..16kk+15).
 template <int LAYOUT>
@@ -880,6 +1047,9 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
     constexpr int NTW = kPairs ? 1 : NT;          // n-tiles per warp
     constexpr int PSTRIDE = kPairs ? NC / 2 : NC; // warps per page stream
     const int nt0 = kPairs ? warp / PSTRIDE : 0;
+    // k-steps of Q.K^T: a warp of a differential pair takes its own map's half
+    constexpr int KQ = C::kDiff && kPairs ? KT / 2 : KT;
+    const uint32_t khalf = C::kDiff && kPairs ? (uint32_t)nt0 * (C::kPageBytes / 2) : 0u;
     const int pfirst = kPairs ? warp % PSTRIDE : warp;
     const int G = p.group;
     const int r = lane >> 2, cq = lane & 3;
@@ -900,16 +1070,18 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
         const int GE = qn * G;  // rows of N: query token v / G, head kvh * G + v % G
 
         // Q as B fragments: B[k = head dim][n = row], rows >= GE are zero.
-        uint32_t qb[NTW][KT][2];
+        uint32_t qb[NTW][KQ][2];
         const uint32_t qs = sm.q + slot * C::kQBytes;
 #pragma unroll
         for (int nt = 0; nt < NTW; ++nt) {
-            const int h = (nt0 + nt) * 8 + r;
+            const int v = (nt0 + nt) * 8 + r, h = C::row_of(v);
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
+            for (int kk = 0; kk < KQ; ++kk) {
                 uint32_t b0 = 0, b1 = 0;
-                if (h < GE) {
-                    const uint32_t a = qs + (uint32_t)((h * HEAD + kk * 16 + 2 * cq) * 2);
+                // (one n-tile of both maps: zero against the other map's keys)
+                if (h < GE && (!C::kDiff || kPairs || kk / (KT / 2) == v / C::kRows)) {
+                    const int k0 = C::kDiff && kPairs ? nt0 * (HEAD / 2) + kk * 16 : kk * 16;
+                    const uint32_t a = qs + (uint32_t)((h * HEAD + k0 + 2 * cq) * 2);
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b0) : "r"(a));
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b1) : "r"(a + 16));
                 }
@@ -917,16 +1089,17 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
                 qb[nt][kk][1] = b1;
             }
         }
+        const uint32_t qlast = last_query_word<C, KQ>(qb[NTW - 1]);
         __syncwarp();
         // Q and descriptor are in registers (lane 0 takes part in the last read)
-        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qb[NTW - 1][KT - 1][1], p.zero);
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);
 
         float sl[NTW][2];
 #pragma unroll
         for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int h = (nt0 + nt) * 8 + 2 * cq + e;
+                const int h = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
                 sl[nt][e] = (has_alibi && h < GE) ? __ldg(p.alibi + d.kvh * G + h % G) : 0.f;
             }
         // key range of each of this lane's rows: its query token's position and
@@ -936,7 +1109,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
         for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int v = (nt0 + nt) * 8 + 2 * cq + e;
+                const int v = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
                 int lo = d.tok_begin, hi = d.tok_end - 1;
                 if (C::kMQ && v < GE) {
                     const int pos = d.len - qn + v / G;
@@ -998,9 +1171,9 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
+            for (int kk = 0; kk < KQ; ++kk) {
                 uint32_t a0, a1, a2, a3;
-                ldsm_x4(kp + k_frag_off<LAYOUT>(lane, kk), a0, a1, a2, a3);
+                ldsm_x4(kp + khalf + k_frag_off<LAYOUT>(lane, kk), a0, a1, a2, a3);
 #pragma unroll
                 for (int nt = 0; nt < NTW; ++nt) {
                     if (kk & 1)
@@ -1160,8 +1333,10 @@ __device__ __forceinline__ void fp8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t&
 // tensor copy leaves it: rows of HEAD bytes, chunks swizzled (128-byte swizzle:
 // chunk ^ (t mod 8); 64-byte swizzle: chunk ^ ((t / 2) mod 4)), so the eight
 // rows a warp reads at once fall in distinct banks.
+// Value rows of 256 bytes are two such blocks of 128-byte rows, one after the other.
 template <int HEAD>
 __device__ __forceinline__ uint32_t nhd8_off(int t, int c) {
+    if constexpr (HEAD > 128) return (uint32_t)((c >> 3) * 2048) + nhd8_off<128>(t, c & 7);
     const int sw = HEAD == 128 ? (t & 7) : ((t >> 1) & 3);
     return (uint32_t)(t * HEAD + ((c ^ sw) << 4));
 }
@@ -1170,11 +1345,15 @@ __device__ __forceinline__ uint32_t nhd8_off(int t, int c) {
 // kk + 1.  Matrix j = lane / 8 holds the 16-byte rows of the eight tokens of
 // S^T rows 0-7 (j even) or 8-15 (j odd) in k-step kk + j / 2, so register j of
 // lane (r, cq) is the word (token of row r or r + 8, head dims 16k + 4cq..+3).
-template <int LAYOUT, int HEAD>
+// A differential page (DIFF) is two pages of HEAD / 2, map by map.
+template <int LAYOUT, int HEAD, bool DIFF>
 __device__ __forceinline__ uint32_t k8_frag_off(int lane, int kk) {
     const int j = lane >> 3, i = lane & 7;
     const int c = kk + (j >> 1);
-    if constexpr (LAYOUT == kNHD) {
+    if constexpr (LAYOUT == kNHD && DIFF) {
+        constexpr int CM = HEAD / 32;  // chunks of one map's row
+        return (uint32_t)(c / CM * (kBS * HEAD / 2)) + nhd8_off<HEAD / 2>(i + ((j & 1) << 3), c % CM);
+    } else if constexpr (LAYOUT == kNHD) {
         return nhd8_off<HEAD>(i + ((j & 1) << 3), c);  // natural token order
     } else {
         const int tok = ((i >> 1) << 2) + (i & 1) + ((j & 1) << 1);  // tau(i), tau(i) + 2
@@ -1200,9 +1379,13 @@ __device__ __forceinline__ uint32_t v8_frag_off(int lane, int mt) {
 // swizzle only permutes chunks inside a row).
 template <int HEAD>
 __device__ __forceinline__ void zero_v_tail8_nhd(uint32_t vpage, int valid, int lane) {
-    for (int i = lane; i < (kBS - valid) * HEAD / 4; i += 32)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(vpage + (uint32_t)(valid * HEAD + 4 * i)), "r"(0u)
-                     : "memory");
+    constexpr int ROW = HEAD > 128 ? 128 : HEAD;  // bytes of a row of a block
+#pragma unroll
+    for (int b = 0; b < HEAD / ROW; ++b)
+        for (int i = lane; i < (kBS - valid) * ROW / 4; i += 32)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vpage + (uint32_t)(b * kBS * ROW + valid * ROW + 4 * i)),
+                         "r"(0u)
+                         : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -1225,6 +1408,14 @@ template <class C, typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC,
 __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int lane) {
     constexpr bool QBF = C::kBF16;
     constexpr int KT = HEAD / 16;
+    // differential, two n-tiles: warps in pairs, one map each (see consumer_mma)
+    constexpr bool kPairs = C::kPairs;
+    constexpr int NTW = kPairs ? 1 : NT;
+    constexpr int PSTRIDE = kPairs ? NC / 2 : NC;
+    constexpr int KQ = kPairs ? KT / 2 : KT;
+    const int nt0 = kPairs ? warp / PSTRIDE : 0;
+    const int pfirst = kPairs ? warp % PSTRIDE : warp;
+    const uint32_t khalf = kPairs ? (uint32_t)nt0 * (C::kPageBytes / 2) : 0u;
     const int G = p.group;
     const int r = lane >> 2, cq = lane & 3;
     // page token of S^T rows r and r + 8: permuted for the split layout (see
@@ -1249,17 +1440,18 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
         const int GE = qn * G;  // rows of N: query token v / G, head kvh * G + v % G
 
         // Q as fp16 B fragments in the permuted head-dim order.
-        uint32_t qb[NT][KT][2];
+        uint32_t qb[NTW][KQ][2];
         bool q_clamped = false;
         const uint32_t qs = sm.q + slot * C::kQBytes;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + r;
+        for (int nt = 0; nt < NTW; ++nt) {
+            const int v = (nt0 + nt) * 8 + r, h = C::row_of(v);
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
+            for (int kk = 0; kk < KQ; ++kk) {
                 uint32_t w0 = 0, w1 = 0;
-                if (h < GE) {
-                    const uint32_t a = qs + (uint32_t)((h * HEAD + kk * 16 + 4 * cq) * 2);
+                if (h < GE && (!C::kDiff || kPairs || kk / (KT / 2) == v / C::kRows)) {
+                    const int k0 = kPairs ? nt0 * (HEAD / 2) + kk * 16 : kk * 16;
+                    const uint32_t a = qs + (uint32_t)((h * HEAD + k0 + 4 * cq) * 2);
                     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(a));
                     if constexpr (QBF) {
                         float2 f0 = unpack2<true>(w0), f1 = unpack2<true>(w1);
@@ -1275,25 +1467,26 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
             }
         }
         if (q_clamped) report(p, PA_DEVERR_QUERY_RANGE);
+        const uint32_t qlast = last_query_word<C, KQ>(qb[NTW - 1]);
         __syncwarp();
-        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qb[NT - 1][KT - 1][1], p.zero);
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);
 
-        float sl[NT][2];
+        float sl[NTW][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int h = nt * 8 + 2 * cq + e;
+                const int h = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
                 sl[nt][e] = (has_alibi && h < GE) ? __ldg(p.alibi + d.kvh * G + h % G) : 0.f;
             }
         // key range of each of this lane's rows: its query token's position and
         // window, within the tile (padded rows get the tile's range)
-        int klo[NT][2], khi[NT][2];
+        int klo[NTW][2], khi[NTW][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int v = nt * 8 + 2 * cq + e;
+                const int v = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
                 int lo = d.tok_begin, hi = d.tok_end - 1;
                 if (C::kMQ && v < GE) {
                     const int pos = d.len - qn + v / G;
@@ -1309,10 +1502,10 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
         const int lo_all = C::kMQ ? max(d.tok_begin, window_lo_at(p, d.len - 1)) : d.tok_begin;
         const int origin = d.tok_end - 1;
 
-        float m[NT][2], l[NT][2], mx[NT][2];  // reference max, sum, this lane's running max
-        float acc[KT][NT][4];
+        float m[NTW][2], l[NTW][2], mx[NTW][2];  // reference max, sum, this lane's running max
+        float acc[KT][NTW][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NTW; ++nt) {
             m[nt][0] = m[nt][1] = mx[nt][0] = mx[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
@@ -1325,9 +1518,9 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
         const int page0 = d.tok_begin / kBS * kBS;
         // stage and phase of page j: advanced per page with one n-tile, computed
         // per page with two (whose registers are all taken)
-        uint32_t st = (gbase + (uint32_t)warp) % STAGES, ph = ((gbase + (uint32_t)warp) / STAGES) & 1;
-        for (int j = warp; j < npages; j += NC, advance_stage<STAGES, NC>(st, ph)) {
-            if constexpr (NT > 1) {
+        uint32_t st = (gbase + (uint32_t)pfirst) % STAGES, ph = ((gbase + (uint32_t)pfirst) / STAGES) & 1;
+        for (int j = pfirst; j < npages; j += PSTRIDE, advance_stage<STAGES, PSTRIDE>(st, ph)) {
+            if constexpr (NTW > 1) {
                 st = (gbase + (uint32_t)j) % STAGES;
                 ph = ((gbase + (uint32_t)j) / STAGES) & 1;
             }
@@ -1352,24 +1545,24 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
 
             // S^T[row][head]: key page [d/16][token][16 bytes] (split) or [token][d]
             // with swizzled 16-byte chunks (NHD)
-            float s[NT][4], s2[NT][4];
+            float s[NTW][4], s2[NTW][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
             // one ldmatrix.x4 fetches the four 32-bit words (tokens tlo / thi,
             // k-steps kk / kk + 1) that four separate loads would
 #pragma unroll
-            for (int kk = 0; kk < KT; kk += 2) {
+            for (int kk = 0; kk < KQ; kk += 2) {
                 uint32_t w[4];
-                ldsm_x4(kp + k8_frag_off<LAYOUT, HEAD>(lane, kk), w[0], w[1], w[2], w[3]);
+                ldsm_x4(kp + khalf + k8_frag_off<LAYOUT, HEAD, C::kDiff>(lane, kk), w[0], w[1], w[2], w[3]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t a0, a1, a2, a3;
                     fp8x4_to_f16<KV>(w[2 * u], a0, a2);
                     fp8x4_to_f16<KV>(w[2 * u + 1], a1, a3);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < NTW; ++nt) {
                         if (u)
                             mma_16816<false>(s2[nt], a0, a1, a2, a3, qb[nt][kk + u][0], qb[nt][kk + u][1]);
                         else
@@ -1380,7 +1573,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
 
             // One n-tile: the page's V words go to registers here and the stage
             // back to the producer, before the softmax, the conversion and P.V.
-            constexpr bool kEarlyV = NT == 1;
+            constexpr bool kEarlyV = NTW == 1;
             uint32_t vw[kEarlyV ? KT / 2 : 1][4];
             if constexpr (kEarlyV) {
 #pragma unroll
@@ -1391,10 +1584,10 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                 if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vw[KT / 2 - 1][3], p.zero);
             }
 
-            uint32_t pb[NT][2];
-            float z[NT][4];
+            uint32_t pb[NTW][2];
+            float z[NTW][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NTW; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = (s[nt][e] + s2[nt][e]) * p.scale;
@@ -1410,9 +1603,9 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                     if (t1 < klo[nt][1] || t1 > khi[nt][1]) z[nt][3] = -INFINITY;
                 }
             }
-            softmax_page<NT, KT, C::kMQ>(z, m, mx, l, acc, edge);
+            softmax_page<NTW, KT, C::kMQ>(z, m, mx, l, acc, edge);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NTW; ++nt) {
                 pb[nt][0] = movmatrix_trans(pack2<false>(z[nt][0], z[nt][1]));  // k-index 2cq.. = tokens tlo
                 pb[nt][1] = movmatrix_trans(pack2<false>(z[nt][2], z[nt][3]));
             }
@@ -1454,7 +1647,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                         fp8x4_to_f16<KV>(w[2 * u + 1], a1, a3);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NTW; ++nt)
                         mma_16816<false>(acc[mt + u][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                 }
             }
@@ -1464,9 +1657,9 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
             }
         }
 
-        settle_max<NT, KT>(m, mx, l, acc);
+        settle_max<NTW, KT>(m, mx, l, acc);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NTW; ++nt) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], o);
@@ -1475,7 +1668,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
         }
         float* mw = sm.merge + warp * C::kMergeRows * C::kMergeStride;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NTW; ++nt) {
             const int h0 = nt * 8 + 2 * cq;
 #pragma unroll
             for (int mt = 0; mt < KT; ++mt) {
@@ -1529,7 +1722,15 @@ template <class C, int HEAD, int NT, int LAYOUT, int STAGES, int NC>
 __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lane) {
     constexpr int KT = HEAD / 8;   // k-steps of Q.K^T (8 head dims each)
     constexpr int MT = HEAD / 16;  // m-tiles of P.V (16 head dims each)
-    constexpr bool QSPLIT = NT == 1;  // Q held split for the whole tile
+    // differential, two n-tiles: warps in pairs, one map each (see consumer_mma)
+    constexpr bool kPairs = C::kPairs;
+    constexpr int NTW = kPairs ? 1 : NT;
+    constexpr int PSTRIDE = kPairs ? NC / 2 : NC;
+    constexpr int KQ = kPairs ? KT / 2 : KT;
+    const int nt0 = kPairs ? warp / PSTRIDE : 0;
+    const int pfirst = kPairs ? warp % PSTRIDE : warp;
+    const uint32_t khalf = kPairs ? (uint32_t)nt0 * (C::kPageBytes / 2) : 0u;
+    constexpr bool QSPLIT = NTW == 1 && KQ <= 16;  // Q held split for the whole tile
     const int G = p.group;
     const int r = lane >> 2, cq = lane & 3;
     const bool has_alibi = p.alibi != nullptr;
@@ -1550,37 +1751,39 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 
         // Q as B fragments (k = head dim 8kk + cq / + 4, n = row nt * 8 + r):
         // hi and lo terms (one n-tile) or the raw words (two)
-        uint32_t qa[NT][KT][2];
-        uint32_t qlo[QSPLIT ? KT : 1][2];
+        uint32_t qa[NTW][KQ][2];
+        uint32_t qlo[QSPLIT ? KQ : 1][2];
         {
             const float* q = reinterpret_cast<const float*>(
                 __cvta_shared_to_generic(sm.q + slot * C::kQBytes));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
-                for (int kk = 0; kk < KT; ++kk)
+                for (int kk = 0; kk < KQ; ++kk)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int row = nt * 8 + r;
-                        const uint32_t x =
-                            row < GE ? __float_as_uint(q[row * HEAD + kk * 8 + cq + 4 * e]) : 0u;
+                        const int v = (nt0 + nt) * 8 + r, row = C::row_of(v);
+                        const int k0 = kPairs ? nt0 * (HEAD / 2) + kk * 8 : kk * 8;
+                        const bool mine = row < GE && (!C::kDiff || kPairs || kk / (KT / 2) == v / C::kRows);
+                        const uint32_t x = mine ? __float_as_uint(q[row * HEAD + k0 + cq + 4 * e]) : 0u;
                         if constexpr (QSPLIT)
                             split_tf32(x, qa[nt][kk][e], qlo[kk][e]);
                         else
                             qa[nt][kk][e] = x;
                     }
         }
+        const uint32_t qlast = last_query_word<C, KQ>(qa[NTW - 1]);
         __syncwarp();
         // Q and descriptor are in registers (lane 0 takes part in the last read)
-        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qa[NT - 1][KT - 1][1], p.zero);
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);
 
-        float sl[NT][2];
-        int klo[NT][2], khi[NT][2];  // key range of this lane's rows within the tile
+        float sl[NTW][2];
+        int klo[NTW][2], khi[NTW][2];  // key range of this lane's rows within the tile
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int v = nt * 8 + 2 * cq + e;
+                const int v = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
                 sl[nt][e] = (has_alibi && v < GE) ? __ldg(p.alibi + d.kvh * G + v % G) : 0.f;
                 int lo = d.tok_begin, hi = d.tok_end - 1;
                 if (C::kMQ && v < GE) {
@@ -1595,10 +1798,10 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
         const int lo_all = C::kMQ ? max(d.tok_begin, window_lo_at(p, d.len - 1)) : d.tok_begin;
         const int origin = d.tok_end - 1;
 
-        float m[NT][2], l[NT][2], mx[NT][2];  // reference max, sum, this lane's running max
-        float acc[MT][NT][4];
+        float m[NTW][2], l[NTW][2], mx[NTW][2];  // reference max, sum, this lane's running max
+        float acc[MT][NTW][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NTW; ++nt) {
             m[nt][0] = m[nt][1] = mx[nt][0] = mx[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
@@ -1616,9 +1819,9 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
         const int src0 = 4 * tk0 + (r >> 1), src1 = 4 * tk1 + (r >> 1);
         // stage and phase of page j: advanced per page with one n-tile, computed
         // per page with two (whose registers are all taken)
-        uint32_t st = (gbase + (uint32_t)warp) % STAGES, ph = ((gbase + (uint32_t)warp) / STAGES) & 1;
-        for (int j = warp; j < npages; j += NC, advance_stage<STAGES, NC>(st, ph)) {
-            if constexpr (NT > 1) {
+        uint32_t st = (gbase + (uint32_t)pfirst) % STAGES, ph = ((gbase + (uint32_t)pfirst) / STAGES) & 1;
+        for (int j = pfirst; j < npages; j += PSTRIDE, advance_stage<STAGES, PSTRIDE>(st, ph)) {
+            if constexpr (NTW > 1) {
                 st = (gbase + (uint32_t)j) % STAGES;
                 ph = ((gbase + (uint32_t)j) / STAGES) & 1;
             }
@@ -1647,25 +1850,25 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             // sum across the k-steps of a page or, for P.V below, the pages of
             // a tile: without it a 24-head, group-12 fp32 case missed the 1e-5
             // tolerance even with the rounded split.
-            float s[NT][4], s2[NT][4];
+            float s[NTW][4], s2[NTW][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NTW; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
+            for (int kk = 0; kk < KQ; ++kk) {
                 uint32_t a[4], ah[4], al[4];
                 const int cg = 2 * kk + (lj >> 1);  // 16-byte chunk of the head dims
                 const uint32_t ka =
                     LAYOUT == kSplit
-                        ? kp + (uint32_t)((cg * kBS + li + ((lj & 1) << 3)) * 16)
-                        : kp + (uint32_t)((cg >> 3) * 2048 + (li + ((lj & 1) << 3)) * 128 +
+                        ? kp + khalf + (uint32_t)((cg * kBS + li + ((lj & 1) << 3)) * 16)
+                        : kp + khalf + (uint32_t)((cg >> 3) * 2048 + (li + ((lj & 1) << 3)) * 128 +
                                           (((cg & 7) ^ li) << 4));
                 ldsm_x4(ka, a[0], a[1], a[2], a[3]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < NTW; ++nt) {
                     uint32_t bh[2], bl[2];
                     if constexpr (QSPLIT) {
                         bh[0] = qa[nt][kk][0];
@@ -1687,10 +1890,10 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             }
 
             // logits, online softmax, P^T as B fragments (hi and lo) per n-tile
-            uint32_t pbh[NT][2][2], pbl[NT][2][2];
-            float z[NT][4];
+            uint32_t pbh[NTW][2][2], pbl[NTW][2][2];
+            float z[NTW][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NTW; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = (s[nt][e] + s2[nt][e]) * p.scale;
@@ -1706,9 +1909,9 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                     if (t1 < klo[nt][1] || t1 > khi[nt][1]) z[nt][3] = -INFINITY;
                 }
             }
-            softmax_page<NT, MT, C::kMQ>(z, m, mx, l, acc, edge);
+            softmax_page<NTW, MT, C::kMQ>(z, m, mx, l, acc, edge);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NTW; ++nt) {
                 // z[nt]: p of (token r, row 2cq), (token r, row 2cq + 1),
                 // (token r + 8, row 2cq), (token r + 8, row 2cq + 1)
                 const float* pv = z[nt];
@@ -1755,7 +1958,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 #pragma unroll
                     for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < NTW; ++nt) {
                         float t[4] = {0.f, 0.f, 0.f, 0.f};
                         mma_1688_tf32(t, al[0], al[1], al[2], al[3], pbh[nt][ks][0], pbh[nt][ks][1]);
                         mma_1688_tf32(t, ah[0], ah[1], ah[2], ah[3], pbl[nt][ks][0], pbl[nt][ks][1]);
@@ -1770,9 +1973,9 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
         }
 
         float* mw = sm.merge + warp * C::kMergeRows * C::kMergeStride;
-        settle_max<NT, MT>(m, mx, l, acc);
+        settle_max<NTW, MT>(m, mx, l, acc);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NTW; ++nt) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], o);
@@ -1814,14 +2017,15 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 // two n-tiles fills an SM's shared memory with one CTA (16 KB stages): no cap.
 // fp8 with one n-tile: capped for three CTAs per SM (128 registers: fifteen
 // warps put four on some SM sub-partition, whose register file is 16 K).
-template <typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV, bool MQ>
+// Value heads of 256 hold one CTA per SM.
+template <typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV, bool MQ, bool DIFF>
 __global__ void __launch_bounds__((NC + 1) * 32,
-                                  (std::is_same<T, float>::value && NT > 1)
+                                  (HEAD > 128 || (std::is_same<T, float>::value && NT > 1))
                                       ? 1
                                       : ((NT > 1 || std::is_same<T, float>::value) ? 2 : (KV != kKvSame ? 3 : 1)))
     pa_partition_kernel(const Params p, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {
-    using C = Cfg<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ>;
+    using C = Cfg<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ, DIFF>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -2029,26 +2233,31 @@ __global__ void __launch_bounds__(WARPS * 32) pa_reduce_kernel(const Params p) {
 // L2ONLY: every load through L2 only (the merge inside the partition kernel
 // reads what other CTAs of the same grid wrote); otherwise the partition
 // outputs are read with an evict_first hint (their last use).
-template <typename T, int HEAD, bool L2ONLY>
-__device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int h, int len, int qn, int qi,
-                                               int lane) {
-    constexpr int VEC = HEAD / 32;  // columns per lane: 4 (HEAD 128) or 2 (HEAD 64)
+// merge_stats_row does this for one row `srow` of the statistics, leaving the
+// merged output row in acc (columns lane_col).
+template <int HEAD, bool L2ONLY>
+__device__ __forceinline__ void merge_stats_row(const Params& p, int64_t srow, int h, int len, int qn, int qi,
+                                                int lane, float (&acc)[HEAD / 32]) {
+    constexpr int VEC = HEAD / 32;  // columns per lane: 8 (HEAD 256), 4 (HEAD 128) or 2 (HEAD 64)
     constexpr int PRE = 8;          // partition outputs loaded before the weights are known
     const int hi = len - qn + qi;                      // the query token's position
     const int P = hi >= 0 ? (hi + kPart) / kPart : 0;  // partitions holding its keys
     const int p0 = window_lo_at(p, hi) / kPart;        // partitions before p0: outside the window
-    const int64_t sb = (row * p.num_heads + h) * p.max_parts;
+    const int64_t sb = srow * p.max_parts;
     float* ml = p.max_logits + sb;
     float* es = p.exp_sums + sb;
-    const float* tmp = p.tmp_out + sb * HEAD + lane * VEC;
+    const float* tmp = p.tmp_out + sb * HEAD + lane_col<HEAD>(lane, 0);
 
     // partition outputs p0 .. p0 + 7 and this lane's first statistics, all in flight
     const uint64_t pol = l2_policy_evict_first();  // partition outputs: last use
     auto load_out = [&](int q, float (&t)[VEC]) {
-        if constexpr (VEC == 4) {
-            const float4 v = L2ONLY ? __ldcg(reinterpret_cast<const float4*>(tmp + (int64_t)q * HEAD))
-                                    : ld_global_v4_hint(tmp + (int64_t)q * HEAD, pol);
-            t[0] = v.x; t[1] = v.y; t[2] = v.z; t[3] = v.w;
+        if constexpr (VEC >= 4) {
+#pragma unroll
+            for (int c = 0; c < VEC; c += 4) {
+                const float* at = tmp + (int64_t)q * HEAD + c * 32;
+                const float4 v = L2ONLY ? __ldcg(reinterpret_cast<const float4*>(at)) : ld_global_v4_hint(at, pol);
+                t[c] = v.x; t[c + 1] = v.y; t[c + 2] = v.z; t[c + 3] = v.w;
+            }
         } else {
             const float2 v = L2ONLY ? __ldcg(reinterpret_cast<const float2*>(tmp + (int64_t)q * HEAD))
                                     : ld_global_v2_hint(tmp + (int64_t)q * HEAD, pol);
@@ -2092,7 +2301,6 @@ __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int
 
     // weighted sum of the partition outputs; lane i holds the weight of
     // partition p0 + 32j + i for the current group j of 32
-    float acc[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
     float c = m1 == -INFINITY ? 0.f : expf(m1 - M) * e1 * invW;
@@ -2129,23 +2337,6 @@ __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int
         }
     }
 
-    T* dst = static_cast<T*>(p.out) + (row * p.num_heads + h) * HEAD + lane * VEC;
-    if constexpr (std::is_same<T, float>::value) {
-        if constexpr (VEC == 4)
-            *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        else
-            *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
-    } else {
-        constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
-        if constexpr (VEC == 4) {
-            uint2 v;
-            v.x = pack2<BF>(acc[0], acc[1]);
-            v.y = pack2<BF>(acc[2], acc[3]);
-            *reinterpret_cast<uint2*>(dst) = v;
-        } else {
-            *reinterpret_cast<uint32_t*>(dst) = pack2<BF>(acc[0], acc[1]);
-        }
-    }
     // statistics: sequence frame -> absolute ALiBi positions; unused partitions
     // padded (every read of this row's statistics is above, in this warp)
     __syncwarp();
@@ -2158,6 +2349,14 @@ __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int
             es[q] = 0.f;
         }
     }
+}
+
+template <typename T, int HEAD, bool L2ONLY>
+__device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int h, int len, int qn, int qi,
+                                               int lane) {
+    float acc[HEAD / 32];
+    merge_stats_row<HEAD, L2ONLY>(p, row * p.num_heads + h, h, len, qn, qi, lane, acc);
+    store_row<T, HEAD>(static_cast<T*>(p.out) + (row * p.num_heads + h) * HEAD, acc, lane);
 }
 
 // Phase 2 with one warp per (sequence, query token, head) row, for batches of
@@ -2181,6 +2380,161 @@ __global__ void __launch_bounds__(kReduceWarpsPerCta * 32) pa_reduce_warp_kernel
     }
     const int len = clamp_len(p, p.seq_lens[s]);
     merge_row_warp<T, HEAD, false>(p, (int64_t)q0 + qi, h, len, qn, qi, lane);
+}
+
+// Phase 2 of differential rows, few partitions: two warps per (sequence, query
+// token, head), one map each (the two merges' round trips overlap); the second
+// hands its row to the first through shared memory.
+template <typename T, int HEAD, bool MQ>
+__global__ void __launch_bounds__(kReduceWarpsPerCta * 32) pa_diff_reduce_warp_kernel(const Params p) {
+    constexpr int VEC = HEAD / 32, ROWS = kReduceWarpsPerCta / 2;
+    __shared__ float second[ROWS][HEAD];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, map = warp & 1;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    const int64_t rid = (int64_t)blockIdx.x * ROWS + (warp >> 1);
+    const int64_t nrows = (int64_t)p.num_seqs * (MQ ? p.max_q_len : 1) * p.num_heads;
+    const int sq = (int)(rid / p.num_heads), h = (int)(rid - (int64_t)sq * p.num_heads);
+    const int s = MQ ? sq / p.max_q_len : sq, qi = MQ ? sq - s * p.max_q_len : 0;
+    int q0 = s, qn = 1;
+    bool mine = rid < nrows;
+    if (MQ && mine) {
+        query_rows(p, s, q0, qn);
+        mine = qi < qn;
+    }
+    const int64_t row = (int64_t)q0 + qi;
+    float o[VEC];
+    if (mine) {
+        merge_stats_row<HEAD, false>(p, 2 * (row * p.num_heads + h) + map, h, clamp_len(p, p.seq_lens[s]), qn, qi,
+                                     lane, o);
+        if (map)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) second[warp >> 1][lane_col<HEAD>(lane, v)] = o[v];
+    }
+    __syncthreads();
+    if (!mine || map) return;
+    float o2[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) o2[v] = second[warp >> 1][lane_col<HEAD>(lane, v)];
+    diff_row<T, HEAD>(p, row, h, o, o2, lane);
+}
+
+// Phase 2 of differential rows, many partitions: one CTA per (sequence, query
+// token, head), half of its warps per map; each thread owns a float4 column of a
+// partition row and keeps U of them in flight with its own running max, as
+// pa_reduce_kernel does.  The first warp combines them and writes the row.
+template <typename T, int HEAD, int WARPS, int U, bool MQ>
+__global__ void __launch_bounds__(WARPS * 32) pa_diff_reduce_kernel(const Params p) {
+    constexpr int D4 = HEAD / 4;
+    constexpr int HALF = WARPS * 16;     // threads of a map
+    constexpr int RSTEP = HALF / D4;     // partition rows per round
+    constexpr int VEC = HEAD / 32;
+    static_assert(HALF % D4 == 0, "whole partition rows");
+    __shared__ __align__(16) float part[2][RSTEP][HEAD];
+    __shared__ float rowm[2][RSTEP], roww[2][RSTEP];
+
+    const int bid = blockIdx.x;
+    const int sq = bid / p.num_heads, h = bid - sq * p.num_heads;
+    const int s = MQ ? sq / p.max_q_len : sq, qi = MQ ? sq - s * p.max_q_len : 0;
+    const int map = threadIdx.x / HALF, tid = threadIdx.x % HALF, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    int q0 = s, qn = 1;
+    if constexpr (MQ) {
+        query_rows(p, s, q0, qn);
+        if (qi >= qn) return;
+    }
+    const int len = clamp_len(p, p.seq_lens[s]);
+    const int hi = len - qn + qi;                      // the query token's position
+    const int P = hi >= 0 ? (hi + kPart) / kPart : 0;  // partitions holding its keys
+    const int p0 = window_lo_at(p, hi) / kPart;        // partitions before p0: outside the window
+    const int64_t row = (int64_t)q0 + qi;
+    const int64_t sb = (2 * (row * p.num_heads + h) + map) * p.max_parts;
+    float* ml = p.max_logits + sb;
+    float* es = p.exp_sums + sb;
+    const float* tmp = p.tmp_out + sb * HEAD;
+    const uint64_t pol = l2_policy_evict_first();  // partition outputs: last use
+
+    const int prow = tid / D4, d4 = tid % D4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, W = 0.f;
+    for (int qb = p0 + prow; qb < P; qb += RSTEP * U) {
+        float mq[U], eq[U];
+        float4 t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = qb + u * RSTEP;
+            if (q < P) {
+                mq[u] = ml[q];
+                eq[u] = es[q];
+                t[u] = ld_global_v4_hint(tmp + (int64_t)q * HEAD + 4 * d4, pol);
+            } else {
+                mq[u] = -INFINITY;
+                eq[u] = 0.f;
+                t[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (mq[u] == -INFINITY) continue;
+            if (mq[u] > M) {
+                const float sc = (M == -INFINITY) ? 0.f : expf(M - mq[u]);
+                a.x *= sc;
+                a.y *= sc;
+                a.z *= sc;
+                a.w *= sc;
+                W *= sc;
+                M = mq[u];
+            }
+            const float c = expf(mq[u] - M) * eq[u];
+            a.x += c * t[u].x;
+            a.y += c * t[u].y;
+            a.z += c * t[u].z;
+            a.w += c * t[u].w;
+            W += c;
+        }
+    }
+    *reinterpret_cast<float4*>(&part[map][prow][4 * d4]) = a;
+    if (d4 == 0) {
+        rowm[map][prow] = M;
+        roww[map][prow] = W;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        float o[2][VEC];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float Mg = -INFINITY, Wg = 0.f;
+#pragma unroll
+            for (int i = 0; i < RSTEP; ++i) Mg = fmaxf(Mg, rowm[k][i]);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) o[k][v] = 0.f;
+#pragma unroll
+            for (int i = 0; i < RSTEP; ++i) {
+                const float c = rowm[k][i] == -INFINITY ? 0.f : expf(rowm[k][i] - Mg);
+                Wg = fmaf(c, roww[k][i], Wg);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) o[k][v] = fmaf(c, part[k][i][lane_col<HEAD>(lane, v)], o[k][v]);
+            }
+            const float inv = Wg > 0.f ? 1.f / Wg : 0.f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) o[k][v] *= inv;
+        }
+        diff_row<T, HEAD>(p, row, h, o[0], o[1], lane);
+    }
+    // statistics: sequence frame -> absolute ALiBi positions, unused partitions
+    // padded (every read of them above happened before the barrier)
+    const float shift = p.alibi ? __ldg(p.alibi + h) * (float)(len - 1) : 0.f;
+    for (int q = tid; q < p.max_parts; q += HALF) {
+        if (q >= p0 && q < P) {
+            if (p.alibi) ml[q] += shift;
+        } else {
+            ml[q] = -INFINITY;
+            es[q] = 0.f;
+        }
+    }
 }
 
 }  // namespace pa

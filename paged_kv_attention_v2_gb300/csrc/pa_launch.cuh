@@ -42,13 +42,16 @@ constexpr int kMaxDevices = 64;
 // (a short merge).  With several rounds the CTA that merges falls behind and
 // becomes the last arriver of the next group too, so merges pile up on a few
 // CTAs; the separate reduce kernel spreads them over the whole GPU instead.
-template <typename T, int HEAD, int NT, int LAYOUT, int KV, bool MQ>
+template <typename T, int HEAD, int NT, int LAYOUT, int KV, bool MQ, bool DIFF = false>
 cudaError_t launch_main(const Params& p_in, const LaunchArgs& la, bool* fused) {
-    constexpr int STAGES = std::is_same<T, float>::value ? (NT == 1 ? kStagesF32 : kStagesF32x2)
-                           : (KV == kKvSame ? (NT == 1 ? kStages16 : kStages16x2) : kStagesFp8);
-    constexpr int NC = (KV == kKvSame && NT == 1) ? kConsumerWarps5 : kConsumerWarps;
-    using C = Cfg<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ>;
-    auto kern = pa_partition_kernel<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ>;
+    constexpr bool F32 = std::is_same<T, float>::value, WIDE = HEAD > 128;
+    constexpr int STAGES = WIDE ? (F32 ? kStagesF32Wide : (KV == kKvSame ? kStages16Wide : kStagesFp8Wide))
+                           : F32 ? (NT == 1 ? kStagesF32 : kStagesF32x2)
+                                 : (KV == kKvSame ? (NT == 1 ? kStages16 : kStages16x2) : kStagesFp8);
+    constexpr int NC = WIDE ? (F32 ? kConsumerWarps : kConsumerWarpsWide)
+                            : ((KV == kKvSame && NT == 1) ? kConsumerWarps5 : kConsumerWarps);
+    using C = Cfg<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ, DIFF>;
+    auto kern = pa_partition_kernel<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ, DIFF>;
 
     static std::atomic<int> occ_cache[kMaxDevices];
     int dev = 0;
@@ -185,6 +188,59 @@ cudaError_t launch_family(const Params& p, const LaunchArgs& la) {
         return la.head_size == 128 ? launch_reduce<T, 128, true>(p, la) : launch_reduce<T, 64, true>(p, la);
     return la.head_size == 128 ? launch_reduce<T, 128, false>(p, la) : launch_reduce<T, 64, false>(p, la);
 }
+
+// ---------------------------------------------------------------- differential
+
+template <typename T, int HEAD, bool MQ>
+cudaError_t launch_diff_reduce(const Params& p, const LaunchArgs& la) {
+    const int64_t rows = (int64_t)p.num_seqs * p.max_q_len * p.num_heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = la.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // few rows of many partitions, or more partitions than a warp should walk: a
+    // CTA per row (as launch_reduce)
+    if ((p.max_parts > 32 && rows <= 2 * (int64_t)la.sm_count) || p.max_parts > kReduceWarpMaxParts) {
+        cfg.gridDim = dim3((unsigned)rows);
+        cfg.blockDim = dim3(16 * 32);
+        return cudaLaunchKernelEx(&cfg, pa_diff_reduce_kernel<T, HEAD, 16, HEAD == 128 ? 8 : 4, MQ>, p);
+    }
+    cfg.gridDim = dim3((unsigned)((rows + kReduceWarpsPerCta / 2 - 1) / (kReduceWarpsPerCta / 2)));
+    cfg.blockDim = dim3(kReduceWarpsPerCta * 32);
+    return cudaLaunchKernelEx(&cfg, pa_diff_reduce_warp_kernel<T, HEAD, MQ>, p);
+}
+
+template <typename T, int HEAD, int NT, int KV, bool MQ>
+cudaError_t launch_diff_layout(const Params& p, const LaunchArgs& la, bool* fused) {
+    return la.layout == kNHD ? launch_main<T, HEAD, NT, kNHD, KV, MQ, true>(p, la, fused)
+                             : launch_main<T, HEAD, NT, kSplit, KV, MQ, true>(p, la, fused);
+}
+
+template <typename T, int HEAD, int KV, bool MQ>
+cudaError_t launch_diff_head(const Params& p, const LaunchArgs& la) {
+    bool fused = false;
+    const cudaError_t e = la.group_tiles == 2 ? launch_diff_layout<T, HEAD, 2, KV, MQ>(p, la, &fused)
+                                              : launch_diff_layout<T, HEAD, 1, KV, MQ>(p, la, &fused);
+    if (e != cudaSuccess || p.v1 || fused || la.query) return e;
+    return launch_diff_reduce<T, HEAD, MQ>(p, la);
+}
+
+// Differential attention for one (query type, cache type) pair; la.head_size is
+// the value head size, 128 or 256.
+template <typename T, int KV, int HEAD>
+cudaError_t launch_diff_family(const Params& p, const LaunchArgs& la) {
+    return p.query_start ? launch_diff_head<T, HEAD, KV, true>(p, la) : launch_diff_head<T, HEAD, KV, false>(p, la);
+}
+
+// One translation unit per (query type, cache kind); kv: kKvSame / kKvE4M3 / kKvE5M2
+cudaError_t launch_diff_f32(const Params& p, const LaunchArgs& la);
+cudaError_t launch_diff_f16(const Params& p, const LaunchArgs& la);
+cudaError_t launch_diff_bf16(const Params& p, const LaunchArgs& la);
+cudaError_t launch_diff_f16_fp8(const Params& p, const LaunchArgs& la, int kv);
+cudaError_t launch_diff_bf16_fp8(const Params& p, const LaunchArgs& la, int kv);
 
 cudaError_t launch_f32(const Params& p, const LaunchArgs& la);
 cudaError_t launch_f16(const Params& p, const LaunchArgs& la);

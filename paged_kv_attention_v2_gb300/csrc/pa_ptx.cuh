@@ -128,6 +128,17 @@ __device__ __forceinline__ void tensor3d_g2s_hint(uint32_t dst, const CUtensorMa
         : "memory");
 }
 
+// 4-D tiled tensor copy global -> shared, completing on an mbarrier, with an
+// L2 cache policy.
+__device__ __forceinline__ void tensor4d_g2s_hint(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                                  int w, uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(pol)
+        : "memory");
+}
+
 // Bulk prefetch of global memory into L2 (a hint: no completion, no data
 // returned).  src 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {

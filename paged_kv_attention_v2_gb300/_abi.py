@@ -6,6 +6,7 @@ implementation behind this package.
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -161,6 +162,19 @@ class PaAppendArgs(ctypes.Structure):
     ]
 
 
+_CODES = {ctypes.c_void_p: "P", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f"}
+
+
+def packer(cls) -> struct.Struct:
+    """struct.Struct with the layout of an argument struct (nested ones field by
+    field), the same as the C compiler's: packing the fields' values into bytes
+    takes a fraction of the time that filling a ctypes structure does."""
+    def codes(c):
+        for _, t in c._fields_:
+            yield from codes(t) if issubclass(t, ctypes.Structure) else _CODES[t]
+    return struct.Struct("@" + "".join(codes(cls)) + "0P")  # padded at the end like the struct
+
+
 _lib = None
 
 
@@ -202,13 +216,14 @@ def load(path: Path | None = None):
     lib.pa_plan.restype = ctypes.c_int
     lib.pa_debug_withhold_page.argtypes = [ctypes.c_int32, ctypes.c_int64]
     lib.pa_debug_withhold_page.restype = ctypes.c_int
-    lib.pa_diff_decode.argtypes = [ctypes.POINTER(PaDiffArgs), ctypes.c_void_p]
+    # argument structs of these come as structures (byref) or as packed bytes
+    lib.pa_diff_decode.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.pa_diff_decode.restype = ctypes.c_int
     lib.pa_diff_plan.argtypes = [ctypes.POINTER(PaDiffArgs), ctypes.POINTER(PaLaunchPlan)]
     lib.pa_diff_plan.restype = ctypes.c_int
-    lib.pa_build_tables.argtypes = [ctypes.POINTER(PaTablesArgs), ctypes.c_void_p]
+    lib.pa_build_tables.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.pa_build_tables.restype = ctypes.c_int
-    lib.pa_append_kv.argtypes = [ctypes.POINTER(PaAppendArgs), ctypes.c_void_p]
+    lib.pa_append_kv.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.pa_append_kv.restype = ctypes.c_int
     if path is None:
         _lib = lib

@@ -8,8 +8,6 @@ is one step of serving: the lengths, the tables and the pool move on in place.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _abi
@@ -18,58 +16,73 @@ _LAYOUT = {"split": _abi.PA_LAYOUT_SPLIT, "nhd": _abi.PA_LAYOUT_NHD}
 _KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP8_E5M2}
 _DTYPE = {torch.float32: _abi.PA_DTYPE_F32, torch.float16: _abi.PA_DTYPE_F16,
           torch.bfloat16: _abi.PA_DTYPE_BF16}
+_BYTES = {torch.float32: 4, torch.float16: 2, torch.bfloat16: 2}
+_TABLES = _abi.packer(_abi.PaTablesArgs)
+_APPEND = _abi.packer(_abi.PaAppendArgs)
+_PAGE = _abi.PA_BLOCK_SIZE
 
 
-def _stream_handle(stream, device) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _call(name: str, args, stream, device) -> None:
-    """The entry point `name` on `stream` (default: torch's current one), with the
-    tensors' device current."""
+def _call(name: str, args: bytes, stream, device: int) -> None:
+    """The entry point `name` with packed arguments on `stream` (default: torch's
+    current one), with the tensors' device current."""
+    if device < 0:
+        raise ValueError(f"{name} needs CUDA tensors")
     fn = getattr(_abi.load(), name)
-    handle = _stream_handle(stream, device)
-    if torch.cuda.current_device() == device.index:
-        st = fn(ctypes.byref(args), handle)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == device:
+        st = fn(args, handle)
     else:
         with torch.cuda.device(device):
-            st = fn(ctypes.byref(args), handle)
+            st = fn(args, handle)
     if st != _abi.PA_OK:
         from . import PaDecodeError
         raise PaDecodeError(st, name)
 
 
-def _ints(name: str, t, device, numel: int | None = None) -> int | None:
-    """Data pointer of a contiguous int32 tensor on `device` (None: no tensor)."""
+def _pointer(name: str, t, dtype, device: int, numel: int = -1) -> int:
+    """Address of a contiguous tensor of `dtype` on `device` (None: 0), of `numel` elements if given."""
     if t is None:
-        return None
-    if t.dtype is not torch.int32 or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-    if numel is not None and t.numel() != numel:
+        return 0
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the call's device")
+    if numel >= 0 and t.numel() != numel:
         raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
     return t.data_ptr()
+
+
+def _ints(name: str, t, device: int, numel: int = -1) -> int:
+    return _pointer(name, t, torch.int32, device, numel)
+
+
+def _pack_tables(block_tables, seq_lens, free_ring, pool_state, slots, max_seq_len, keep_lens, query_start,
+                 positions, new_seq_lens, new_pool_state, done_counter, dev_error) -> bytes:
+    device = seq_lens.get_device()
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    n, width = block_tables.shape
+    rows = slots.numel()
+    lens = _ints("seq_lens", seq_lens, device, n)
+    state = _ints("pool_state", pool_state, device, 2)
+    return _TABLES.pack(
+        _ints("block_tables", block_tables, device), lens, _ints("keep_lens", keep_lens, device, n),
+        _ints("query_start", query_start, device, n + 1), _ints("free_ring", free_ring, device), state,
+        _ints("slots", slots, device), _ints("positions", positions, device, rows),
+        lens if new_seq_lens is None else _ints("new_seq_lens", new_seq_lens, device, n),
+        state if new_pool_state is None else _ints("new_pool_state", new_pool_state, device, 2),
+        n, rows, free_ring.numel(), _PAGE, max_seq_len, width, _ints("dev_error", dev_error, device, 1),
+        _ints("done_counter", done_counter, device, 1))
 
 
 def make_tables_args(block_tables, seq_lens, free_ring, pool_state, slots, *, max_seq_len: int,
                      keep_lens=None, query_start=None, positions=None, new_seq_lens=None,
                      new_pool_state=None, done_counter=None, dev_error=None) -> _abi.PaTablesArgs:
     """Build the C argument struct of pa_build_tables (arguments as there)."""
-    device = seq_lens.device
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    n, width = block_tables.shape
-    rows = slots.numel()
-    return _abi.PaTablesArgs(
-        _ints("block_tables", block_tables, device), _ints("seq_lens", seq_lens, device, n),
-        _ints("keep_lens", keep_lens, device, n), _ints("query_start", query_start, device, n + 1),
-        _ints("free_ring", free_ring, device), _ints("pool_state", pool_state, device, 2),
-        _ints("slots", slots, device), _ints("positions", positions, device, rows),
-        _ints("new_seq_lens", seq_lens if new_seq_lens is None else new_seq_lens, device, n),
-        _ints("new_pool_state", pool_state if new_pool_state is None else new_pool_state, device, 2),
-        n, rows, free_ring.numel(), _abi.PA_BLOCK_SIZE, int(max_seq_len), width,
-        _ints("dev_error", dev_error, device, 1), _ints("done_counter", done_counter, device, 1))
+    return _abi.PaTablesArgs.from_buffer_copy(
+        _pack_tables(block_tables, seq_lens, free_ring, pool_state, slots, max_seq_len, keep_lens, query_start,
+                     positions, new_seq_lens, new_pool_state, done_counter, dev_error))
 
 
 def pa_build_tables(block_tables, seq_lens, free_ring, pool_state, slots, *, max_seq_len: int,
@@ -88,51 +101,52 @@ def pa_build_tables(block_tables, seq_lens, free_ring, pool_state, slots, *, max
     lets a call of many rows use the whole GPU.  Everything else, and what happens
     when the pool runs short, is in include/pa_cache.h.
     """
-    device = seq_lens.device
-    args = make_tables_args(block_tables, seq_lens, free_ring, pool_state, slots, max_seq_len=max_seq_len,
-                            keep_lens=keep_lens, query_start=query_start, positions=positions,
-                            new_seq_lens=new_seq_lens, new_pool_state=new_pool_state,
-                            done_counter=done_counter, dev_error=dev_error)
-    if not seq_lens.is_cuda:
-        raise ValueError("pa_build_tables needs CUDA tensors")
-    _call("pa_build_tables", args, stream, device)
+    args = _pack_tables(block_tables, seq_lens, free_ring, pool_state, slots, max_seq_len, keep_lens, query_start,
+                        positions, new_seq_lens, new_pool_state, done_counter, dev_error)
+    _call("pa_build_tables", args, stream, seq_lens.get_device())
+
+
+def _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_scale, v_scale, dev_error) -> bytes:
+    device, dtype = key.get_device(), key.dtype
+    tokens, k_heads, k_size = key.shape
+    v_tokens, v_heads, v_size = value.shape
+    if v_tokens != tokens:
+        raise ValueError(f"{tokens} keys and {v_tokens} values")
+    if value.dtype is not dtype or dtype not in _DTYPE:
+        raise ValueError("key and value must both be float32, float16 or bfloat16")
+    kv_bytes = _BYTES[dtype] if kv_dtype is None else 1
+    blocks = key_cache.shape[0]
+    if value_cache.shape[0] != blocks:
+        raise ValueError(f"{blocks} key pages and {value_cache.shape[0]} value pages")
+    ks, kh, kd = key.stride()
+    vs, vh, vd = value.stride()
+    if kd != 1 or vd != 1:
+        raise ValueError("the head dims of key and value must be contiguous")
+    if value.get_device() != device:
+        raise ValueError("key and value must be on one device")
+    for name, cache, page in (("key_cache", key_cache, k_heads * k_size * _PAGE),
+                              ("value_cache", value_cache, v_heads * v_size * _PAGE)):
+        if cache.element_size() != kv_bytes:
+            raise ValueError(f"{name} has {cache.element_size()}-byte elements, kv_dtype "
+                             f"{kv_dtype or 'same as key'} needs {kv_bytes}")
+        if cache.numel() != blocks * page or not cache.is_contiguous() or cache.get_device() != device:
+            raise ValueError(f"{name} must be contiguous, {blocks} pages of {page} elements, on the call's device")
+    # the stride of a dimension of one is never used
+    if tokens <= 1:
+        ks = vs = 0
+    return _APPEND.pack(
+        key.data_ptr(), value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+        _ints("slots", slots, device, tokens), ks, kh if k_heads > 1 else 0, vs, vh if v_heads > 1 else 0, tokens,
+        k_heads, k_size, v_heads, v_size, blocks, _PAGE, _DTYPE[dtype], _LAYOUT[layout], _KV[kv_dtype], k_scale,
+        v_scale, _ints("dev_error", dev_error, device, 1))
 
 
 def make_append_args(key, value, key_cache, value_cache, slots, *, layout: str = "split",
                      kv_dtype: str | None = None, k_scale: float = 1.0, v_scale: float = 1.0,
                      dev_error=None) -> _abi.PaAppendArgs:
     """Build the C argument struct of pa_append_kv (arguments as there)."""
-    device = key.device
-    tokens, k_heads, k_size = key.shape
-    v_tokens, v_heads, v_size = value.shape
-    if v_tokens != tokens:
-        raise ValueError(f"{tokens} keys and {v_tokens} values")
-    if value.dtype is not key.dtype or key.dtype not in _DTYPE:
-        raise ValueError("key and value must both be float32, float16 or bfloat16")
-    elem = key.element_size()
-    kv_bytes = 1 if kv_dtype is not None else elem
-    blocks = key_cache.shape[0]
-    if value_cache.shape[0] != blocks:
-        raise ValueError(f"{blocks} key pages and {value_cache.shape[0]} value pages")
-    for name, x, cache, page in (("key", key, key_cache, k_heads * k_size), ("value", value, value_cache, v_heads * v_size)):
-        if cache.element_size() != kv_bytes:
-            raise ValueError(f"{name}_cache has {cache.element_size()}-byte elements, kv_dtype "
-                             f"{kv_dtype or 'same as key'} needs {kv_bytes}")
-        if cache.numel() != blocks * page * _abi.PA_BLOCK_SIZE or not cache.is_contiguous():
-            raise ValueError(f"{name}_cache must be contiguous, {blocks} pages of {page * _abi.PA_BLOCK_SIZE} elements")
-        if x.device != device or cache.device != device:
-            raise ValueError("pa_append_kv needs its tensors on one device")
-        if x.stride(2) != 1:
-            raise ValueError(f"the head dims of {name} must be contiguous")
-    # the stride of a dimension of one is never used
-    ks, vs = (key.stride(0), value.stride(0)) if tokens > 1 else (0, 0)
-    kh = key.stride(1) if k_heads > 1 else 0
-    vh = value.stride(1) if v_heads > 1 else 0
-    return _abi.PaAppendArgs(
-        key.data_ptr(), value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-        _ints("slots", slots, device, tokens), ks, kh, vs, vh, tokens, k_heads, k_size, v_heads, v_size, blocks,
-        _abi.PA_BLOCK_SIZE, _DTYPE[key.dtype], _LAYOUT[layout], _KV[kv_dtype], k_scale, v_scale,
-        _ints("dev_error", dev_error, device, 1))
+    return _abi.PaAppendArgs.from_buffer_copy(
+        _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_scale, v_scale, dev_error))
 
 
 def pa_append_kv(key, value, key_cache, value_cache, slots, *, layout: str = "split",
@@ -147,8 +161,5 @@ def pa_append_kv(key, value, key_cache, value_cache, slots, *, layout: str = "sp
     layout; kv_dtype "e4m3" / "e5m2" quantises to fp8 caches holding K / k_scale
     and V / v_scale.
     """
-    args = make_append_args(key, value, key_cache, value_cache, slots, layout=layout, kv_dtype=kv_dtype,
-                            k_scale=k_scale, v_scale=v_scale, dev_error=dev_error)
-    if not key.is_cuda:
-        raise ValueError("pa_append_kv needs CUDA tensors")
-    _call("pa_append_kv", args, stream, key.device)
+    args = _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_scale, v_scale, dev_error)
+    _call("pa_append_kv", args, stream, key.get_device())

@@ -11,8 +11,9 @@ import ctypes
 import torch
 
 from . import _abi
-from .cache import _DTYPE, _KV, _LAYOUT, _call, _ints
+from .cache import _BYTES, _DTYPE, _KV, _LAYOUT, _PAGE, _call, _ints, _pointer
 
+_DIFF = _abi.packer(_abi.PaDiffArgs)
 _MODE = {"auto": _abi.PA_MODE_AUTO, "v1": _abi.PA_MODE_V1, "v2": _abi.PA_MODE_V2}
 
 
@@ -35,91 +36,85 @@ def alloc_diff_workspace(rows: int, num_heads: int, head_size: int, max_seq_len:
     return ws
 
 
-def _floats(name: str, t, device, numel: int | None = None):
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous float32 tensor on {device}")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
-    return t.data_ptr()
+def _floats(name: str, t, device: int, numel: int = -1) -> int:
+    return _pointer(name, t, torch.float32, device, numel)
 
 
-def make_diff_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, lambdas, num_kv_heads: int,
-                   scale: float, max_seq_len: int, norm: bool = True, norm_weight=None, norm_eps: float = 1e-5,
-                   out_scale: float = 1.0, alibi_slopes=None, softcap: float = 0.0, layout: str = "split",
-                   mode: str = "auto", exp_sums=None, max_logits=None, tmp_out=None, dev_error=None,
-                   event_begin=None, event_end=None, partition_counters=None, window_left: int = -1,
-                   kv_dtype: str | None = None, k_scale: float = 1.0, v_scale: float = 1.0, query_start=None,
-                   max_query_len: int | None = None, seq_lens_host=None, tile_counters=None,
-                   metadata_ready: bool = False) -> _abi.PaDiffArgs:
-    """Build the C argument struct of pa_diff_decode (arguments as there)."""
-    device = query.device
+def _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambdas, num_kv_heads, scale, max_seq_len,
+               norm=True, norm_weight=None, norm_eps=1e-5, out_scale=1.0, alibi_slopes=None, softcap=0.0,
+               layout="split", mode="auto", exp_sums=None, max_logits=None, tmp_out=None, dev_error=None,
+               event_begin=None, event_end=None, partition_counters=None, window_left=-1, kv_dtype=None, k_scale=1.0,
+               v_scale=1.0, query_start=None, max_query_len=None, seq_lens_host=None, tile_counters=None,
+               metadata_ready=False):
+    """The packed arguments, and what has to live until the call has been made."""
+    device, dtype = query.get_device(), query.dtype
     if query.dim() != 4 or query.shape[2] != 2:
         raise ValueError("query must be [rows, num_heads, 2, head_size]")
     rows, heads, _, size = query.shape
     n = seq_lens.shape[0]
-    if tuple(out.shape) != (rows, heads, 2 * size) or out.dtype is not query.dtype:
-        raise ValueError(f"out must be {(rows, heads, 2 * size)} of the query's type")
-    if query.dtype not in _DTYPE:
+    if out.shape != (rows, heads, 2 * size):
+        raise ValueError(f"out must be {(rows, heads, 2 * size)}")
+    if dtype not in _DTYPE:
         raise ValueError("query must be float32, float16 or bfloat16")
     if query_start is None:
         if rows != n:
             raise ValueError(f"query has {rows} rows for {n} sequences")
-    elif max_query_len is None:
-        raise ValueError("max_query_len is required with query_start")
+        tokens = most = 0
+    else:
+        if max_query_len is None:
+            raise ValueError("max_query_len is required with query_start")
+        tokens, most = rows, max_query_len
     if block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
     blocks = key_cache.shape[0]
-    elem = 1 if kv_dtype is not None else query.element_size()
-    numel = blocks * 2 * num_kv_heads * _abi.PA_BLOCK_SIZE * size
-    for name, t in (("out", out), ("query", query), ("key_cache", key_cache), ("value_cache", value_cache)):
-        if not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be contiguous and on {device}")
+    elem = _BYTES[dtype] if kv_dtype is None else 1
+    numel = blocks * 2 * num_kv_heads * _PAGE * size
     for name, c in (("key_cache", key_cache), ("value_cache", value_cache)):
         if c.element_size() != elem:
             raise ValueError(f"{name} has {c.element_size()}-byte elements, kv_dtype "
                              f"{kv_dtype or 'same as query'} needs {elem}")
-        if c.shape[0] != blocks or c.numel() != numel:
-            raise ValueError(f"{name} holds {c.numel()} elements in {c.shape[0]} pages, expected {numel} in {blocks}")
-    parts = max(1, -(-int(max_seq_len) // _abi.PA_PARTITION_SIZE))
+        if c.shape[0] != blocks or c.numel() != numel or not c.is_contiguous() or c.get_device() != device:
+            raise ValueError(f"{name} must be contiguous on the call's device, {numel} elements in {blocks} pages "
+                             f"(it holds {c.numel()} in {c.shape[0]})")
+    stats = rows * heads * 2 * max(1, -(-max_seq_len // _abi.PA_PARTITION_SIZE))
     stride = 0
     if lambdas.dim() == 2:
-        if lambdas.shape != (rows, heads):
-            raise ValueError("lambdas must be [num_heads] or [rows, num_heads]")
-        if lambdas.stride(1) != 1 and heads > 1:
-            raise ValueError("the heads of lambdas must be contiguous")
+        if lambdas.shape != (rows, heads) or (lambdas.stride(1) != 1 and heads > 1):
+            raise ValueError("lambdas must be [num_heads] or [rows, num_heads], its heads contiguous")
+        if lambdas.dtype is not torch.float32 or lambdas.get_device() != device:
+            raise ValueError("lambdas must be float32 on the call's device")
         stride = lambdas.stride(0) if rows > 1 else 0
-        if lambdas.dtype is not torch.float32 or lambdas.device != device:
-            raise ValueError(f"lambdas must be float32 on {device}")
         lam = lambdas.data_ptr()
     else:
         lam = _floats("lambdas", lambdas, device, heads)
     host = None
     if seq_lens_host is not None:
         import numpy as np
-        src = seq_lens_host.numpy() if hasattr(seq_lens_host, "numpy") else seq_lens_host
-        host = np.ascontiguousarray(src, dtype=np.int32)
+        host = np.ascontiguousarray(seq_lens_host.numpy() if isinstance(seq_lens_host, torch.Tensor) else seq_lens_host,
+                                    dtype=np.int32)
         if host.shape != (n,):
             raise ValueError("seq_lens_host must hold num_seqs lengths")
-    decode = _abi.PaDecodeArgs(
-        out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-        _ints("block_tables", block_tables, device), _ints("seq_lens", seq_lens, device, n),
-        n, heads, num_kv_heads, size, blocks, _abi.PA_BLOCK_SIZE, int(max_seq_len), block_tables.shape[1],
-        scale, softcap, _floats("alibi_slopes", alibi_slopes, device, heads), _DTYPE[query.dtype], _LAYOUT[layout],
-        _MODE[mode], _floats("exp_sums", exp_sums, device, rows * heads * 2 * parts),
-        _floats("max_logits", max_logits, device, rows * heads * 2 * parts),
-        _floats("tmp_out", tmp_out, device, rows * heads * 4 * parts * size),
-        _ints("dev_error", dev_error, device, 1), None if event_begin is None else event_begin.cuda_event,
-        None if event_end is None else event_end.cuda_event,
+    return _DIFF.pack(
+        _pointer("out", out, dtype, device), _pointer("query", query, dtype, device), key_cache.data_ptr(),
+        value_cache.data_ptr(), _ints("block_tables", block_tables, device), _ints("seq_lens", seq_lens, device, n),
+        n, heads, num_kv_heads, size, blocks, _PAGE, max_seq_len, block_tables.shape[1], scale, softcap,
+        _floats("alibi_slopes", alibi_slopes, device, heads), _DTYPE[dtype], _LAYOUT[layout], _MODE[mode],
+        _floats("exp_sums", exp_sums, device, stats), _floats("max_logits", max_logits, device, stats),
+        _floats("tmp_out", tmp_out, device, stats * 2 * size), _ints("dev_error", dev_error, device, 1),
+        0 if event_begin is None else event_begin.cuda_event, 0 if event_end is None else event_end.cuda_event,
         _ints("partition_counters", partition_counters, device, n * num_kv_heads),
-        int(window_left) + 1 if window_left >= 0 else 0, _KV[kv_dtype], k_scale, v_scale,
-        _ints("query_start", query_start, device, n + 1), 0 if query_start is None else rows,
-        0 if query_start is None else int(max_query_len), None if host is None else host.ctypes.data,
-        _ints("tile_counters", tile_counters, device, 2), 1 if metadata_ready else 0)
-    args = _abi.PaDiffArgs(decode, lam, stride, _floats("norm_weight", norm_weight, device, 2 * size), norm_eps,
-                           out_scale, 1 if norm else 0)
-    args._keep_host_lens = host  # the pointer above stays valid as long as the struct lives
+        window_left + 1 if window_left >= 0 else 0, _KV[kv_dtype], k_scale, v_scale,
+        _ints("query_start", query_start, device, n + 1), tokens, most,
+        0 if host is None else host.__array_interface__["data"][0], _ints("tile_counters", tile_counters, device, 2),
+        1 if metadata_ready else 0,
+        lam, stride, _floats("norm_weight", norm_weight, device, 2 * size), norm_eps, out_scale, 1 if norm else 0), host
+
+
+def make_diff_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, lambdas, **kw) -> _abi.PaDiffArgs:
+    """Build the C argument struct of pa_diff_decode (arguments as there)."""
+    packed, host = _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambdas, **kw)
+    args = _abi.PaDiffArgs.from_buffer_copy(packed)
+    args._keep_host_lens = host  # the pointer inside stays valid as long as the struct lives
     return args
 
 
@@ -148,7 +143,5 @@ def pa_diff_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *
     with the workspace of alloc_diff_workspace.  At most 8 query tokens x heads
     per kv head.  Raises PaDecodeError with the library's status on failure.
     """
-    args = make_diff_args(out, query, key_cache, value_cache, block_tables, seq_lens, lambdas=lambdas, **kw)
-    if not query.is_cuda:
-        raise ValueError("pa_diff_decode needs CUDA tensors")
-    _call("pa_diff_decode", args, stream, query.device)
+    packed, _host = _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambdas, **kw)
+    _call("pa_diff_decode", packed, stream, query.get_device())

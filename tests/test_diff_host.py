@@ -138,3 +138,21 @@ def test_statement_in_64_bits_against_a_loop():
                 y = 0.4 * c["norm_weight"].double() * x / torch.sqrt((x * x).mean() + 1e-5)
                 assert np.allclose(out[r0 + i, h], y.numpy(), rtol=1e-12, atol=1e-12)
     assert np.isfinite(tol).all() and (tol > 0).all()
+
+
+@pytest.mark.parametrize("cls", [_abi.PaDiffArgs, _abi.PaTablesArgs, _abi.PaAppendArgs])
+def test_packed_arguments_are_the_struct(cls):
+    """The packed bytes have the struct's size and every field in its place."""
+    def leaves(c, base=0):
+        for name, t in c._fields_:
+            at = base + getattr(c, name).offset
+            if issubclass(t, ctypes.Structure):
+                yield from leaves(t, at)
+            else:
+                yield at, t
+    fields = list(leaves(cls))
+    pack = _abi.packer(cls)
+    assert pack.size == ctypes.sizeof(cls)
+    data = pack.pack(*range(1, len(fields) + 1))
+    for i, (at, t) in enumerate(fields):
+        assert t.from_buffer_copy(data, at).value == i + 1

@@ -68,114 +68,154 @@ __device__ __forceinline__ uint4 load_chunk(const T* src, float scale) {
     }
 }
 
-template <typename T, int KV, int LAYOUT>
-__global__ void __launch_bounds__(kThreads) pa_append_kernel(const AppendParams p) {
+// One head of a CTA's rows: `src` its row t0, `cache` its page of block 0 (pages
+// of one head `block_bytes` apart), SIZE its head size.
+template <typename T, int KV, int LAYOUT, int SIZE, bool KEY>
+__device__ __forceinline__ void append_head(const AppendParams& p, const T* src, int64_t stride, uint8_t* cache,
+                                            int64_t block_bytes, float scale, int t0, int n, uint8_t* tile) {
     constexpr int E = KV == kSame ? (int)sizeof(T) : 1;  // bytes of a cache element
     constexpr int X = 16 / E;                            // elements of a 16-byte chunk
-    extern __shared__ __align__(16) uint8_t tile[];      // split values: [token][head size + pad] elements
-    __shared__ int slot_of[kTokens];
-    __shared__ int unit_first[kTokens], unit_count[kTokens], units;
-
-    const bool is_key = (int)blockIdx.y < p.num_key_heads;
-    const int head = is_key ? blockIdx.y : (int)blockIdx.y - p.num_key_heads;
-    const int heads = is_key ? p.num_key_heads : p.num_value_heads;
-    const int size = is_key ? p.key_head_size : p.value_head_size;
-    const float scale = is_key ? p.k_scale : p.v_scale;
-    const int64_t stride = is_key ? p.key_stride : p.value_stride;
-    const T* src = static_cast<const T*>(is_key ? p.key : p.value) +
-                   head * (is_key ? p.key_head_stride : p.value_head_stride);
-    uint8_t* cache = static_cast<uint8_t*>(is_key ? p.key_cache : p.value_cache);
-    const int64_t page_bytes = (int64_t)kBS * size * E;
-    const int t0 = blockIdx.x * kTokens, n = min(kTokens, p.num_tokens - t0);
-    const int chunks = size / X;  // 16-byte chunks of a token's head
+    constexpr int CH = SIZE / X;                         // chunks of a token's head
+    constexpr bool SPLIT = LAYOUT == PA_LAYOUT_SPLIT;
+    constexpr int ITEMS = kTokens * CH, PER = (ITEMS + kThreads - 1) / kThreads;
+    __shared__ int64_t base_of[kTokens];  // byte offset of token t's first element in the cache, < 0: no slot
     const int tid = threadIdx.x;
+
+    // The rows do not wait for the slots: both are loaded at once.  Chunk (token,
+    // c) of a thread's item k: 8 tokens x 4 chunks per warp where the cache is
+    // [chunk][token] (split keys: whole sectors are read and written), rows of
+    // chunks elsewhere.
+    int slot = -1;
+    if (tid < n) slot = __ldg(p.slots + t0 + tid);  // n <= kTokens
+    auto place = [&](int k, int& t, int& c) {
+        const int i = k * kThreads + tid;
+        if constexpr (SPLIT && KEY) {
+            t = (i >> 5) % (kTokens / 8) * 8 + (i & 7);
+            c = (i >> 5) / (kTokens / 8) * 4 + (i >> 3 & 3);
+        } else {
+            t = i / CH;
+            c = i % CH;
+        }
+        return ITEMS % kThreads == 0 || i < ITEMS;
+    };
+    uint4 v[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        int t, c;
+        if (place(k, t, c) && t < n) v[k] = load_chunk<T, KV>(src + t * stride + c * X, scale);
+    }
+    if (tid < kTokens) {
+        if (slot >= p.num_blocks * kBS) {
+            if (blockIdx.y == 0 && p.dev_error) atomicOr(p.dev_error, PA_DEVERR_SLOT);
+            slot = -1;
+        }
+        constexpr int STEP = SPLIT ? (KEY ? 16 : E) : SIZE * E;  // bytes from a token to the next
+        base_of[tid] = slot < 0 ? -1 : (int64_t)(slot >> 4) * block_bytes + (slot & 15) * STEP;
+    }
+    if constexpr (!SPLIT || KEY) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            int t, c;
+            if (!place(k, t, c)) break;
+            const int64_t at = base_of[t];
+            if (at >= 0) *reinterpret_cast<uint4*>(cache + at + c * (SPLIT ? 256 : 16)) = v[k];
+        }
+    } else {
+        // values [head dim][16 tokens]: transposed through shared memory, rows in
+        // the cache's type with a pitch of one chunk more than a row
+        constexpr int PITCH = SIZE * E + 16;
+        __shared__ int unit_first[kTokens], unit_count[kTokens], unit_total;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            int t, c;
+            if (place(k, t, c) && t < n) *reinterpret_cast<uint4*>(tile + t * PITCH + c * 16) = v[k];
+        }
+        // units: maximal runs of successive slots inside one 16-byte unit of a page row
+        if (tid < kTokens) {
+            const int before = __shfl_up_sync(0xffffffffu, slot, 1);
+            const bool begins = slot >= 0 && (tid == 0 || slot % X == 0 || before != slot - 1);
+            const unsigned b = __ballot_sync(0xffffffffu, begins), skipped = __ballot_sync(0xffffffffu, slot < 0);
+            if (begins) {
+                const int k = __popc(b & ((1u << tid) - 1));
+                const unsigned stop = (b | skipped) & ~((2u << tid) - 1);  // first token that is not this unit's
+                unit_first[k] = tid;
+                unit_count[k] = (stop ? __ffs(stop) - 1 : 32) - tid;
+            }
+            if (tid == 0) unit_total = __popc(b);
+        }
+        __syncthreads();
+        // item -> (unit, head dim): the E units that make up a page row (16 tokens)
+        // of a full page lie side by side, so a warp writes whole sectors
+        const int units = unit_total;
+        for (int i = tid; i < (units + E - 1) / E * (E * SIZE); i += kThreads) {
+            const int u = i / (E * SIZE) * E + i % E, d = i / E % SIZE;
+            if (u >= units) continue;
+            const int t = unit_first[u], m = unit_count[u];
+            uint8_t* dst = cache + base_of[t] + d * (kBS * E);
+            const uint8_t* col = tile + t * PITCH + d * E;
+            if (m == X) {
+                uint32_t w[4];
+                if constexpr (E == 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint32_t*>(col + k * PITCH);
+                } else if constexpr (E == 2) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = *reinterpret_cast<const uint16_t*>(col + 2 * k * PITCH) |
+                               (uint32_t) * reinterpret_cast<const uint16_t*>(col + (2 * k + 1) * PITCH) << 16;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = col[4 * k * PITCH] | (uint32_t)col[(4 * k + 1) * PITCH] << 8 |
+                               (uint32_t)col[(4 * k + 2) * PITCH] << 16 | (uint32_t)col[(4 * k + 3) * PITCH] << 24;
+                }
+                *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                for (int k = 0; k < m; ++k) {
+                    if constexpr (E == 4)
+                        *reinterpret_cast<uint32_t*>(dst + 4 * k) = *reinterpret_cast<const uint32_t*>(col + k * PITCH);
+                    else if constexpr (E == 2)
+                        *reinterpret_cast<uint16_t*>(dst + 2 * k) = *reinterpret_cast<const uint16_t*>(col + k * PITCH);
+                    else
+                        dst[k] = col[k * PITCH];
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int KV, int LAYOUT>
+__global__ void __launch_bounds__(kThreads) pa_append_kernel(const AppendParams p) {
+    constexpr int E = KV == kSame ? (int)sizeof(T) : 1;
+    extern __shared__ __align__(16) uint8_t tile[];
+    const bool key = (int)blockIdx.y < p.num_key_heads;
+    const int head = key ? blockIdx.y : (int)blockIdx.y - p.num_key_heads;
+    const int heads = key ? p.num_key_heads : p.num_value_heads, size = key ? p.key_head_size : p.value_head_size;
+    const int t0 = blockIdx.x * kTokens, n = min(kTokens, p.num_tokens - t0);
+    const int64_t stride = key ? p.key_stride : p.value_stride;
+    const T* src = static_cast<const T*>(key ? p.key : p.value) + t0 * stride +
+                   head * (key ? p.key_head_stride : p.value_head_stride);
+    const int64_t page = (int64_t)kBS * size * E;
+    uint8_t* cache = static_cast<uint8_t*>(key ? p.key_cache : p.value_cache) + head * page;
 
     pa::pdl_launch_dependents();
     pa::pdl_wait_primary();
 
-    if (tid < kTokens) {
-        int s = tid < n ? __ldg(p.slots + t0 + tid) : -1;
-        if (s >= p.num_blocks * kBS) {
-            if (blockIdx.y == 0 && p.dev_error) atomicOr(p.dev_error, PA_DEVERR_SLOT);
-            s = -1;
-        }
-        slot_of[tid] = s < 0 ? -1 : s;
-    }
-    __syncthreads();
-
-    const bool transposed = LAYOUT == PA_LAYOUT_SPLIT && !is_key;
-    if (!transposed) {
-        // chunk (token, c): NHD a row of chunks per token, split [chunk][token].
-        // 8 tokens x 4 chunks per warp
-        for (int i = tid; i < kTokens * chunks; i += kThreads) {
-            const int quad = i >> 5, lane = i & 31;
-            const int t = (quad % (kTokens / 8)) * 8 + (lane & 7), c = quad / (kTokens / 8) * 4 + (lane >> 3);
-            const int s = slot_of[t];
-            if (s < 0) continue;
-            const uint4 v = load_chunk<T, KV>(src + (t0 + t) * stride + c * X, scale);
-            uint8_t* page = cache + ((int64_t)(s / kBS) * heads + head) * page_bytes;
-            const int off = s % kBS;
-            uint8_t* dst = LAYOUT == PA_LAYOUT_SPLIT ? page + (c * kBS + off) * 16 : page + (off * chunks + c) * 16;
-            *reinterpret_cast<uint4*>(dst) = v;
-        }
-        return;
-    }
-
-    // split values: rows to shared memory in the cache's type (row pitch padded
-    // by one chunk, so that a column's reads do not fall in one bank)
-    const int pitch = size * E + 16;
-    for (int i = tid; i < kTokens * chunks; i += kThreads) {
-        const int t = i / chunks, c = i % chunks;
-        if (slot_of[t] < 0) continue;
-        *reinterpret_cast<uint4*>(tile + t * pitch + c * 16) =
-            load_chunk<T, KV>(src + (t0 + t) * stride + c * X, scale);
-    }
-    // units: maximal runs of successive slots inside one 16-byte unit of a page row
-    if (tid < 32) {
-        const int s = slot_of[tid], before = tid > 0 ? slot_of[tid - 1] : -2;
-        const bool begins = s >= 0 && (s % X == 0 || before != s - 1);
-        const unsigned b = __ballot_sync(0xffffffffu, begins), skipped = __ballot_sync(0xffffffffu, s < 0);
-        if (begins) {
-            const int k = __popc(b & ((1u << tid) - 1));
-            const unsigned stop = (b | skipped) & ~((2u << tid) - 1);  // first token that is not this unit's
-            unit_first[k] = tid;
-            unit_count[k] = (stop ? __ffs(stop) - 1 : 32) - tid;
-        }
-        if (tid == 0) units = __popc(b);
-    }
-    __syncthreads();
-    for (int i = tid; i < units * size; i += kThreads) {
-        const int u = i / size, d = i % size;
-        const int t = unit_first[u], m = unit_count[u], s = slot_of[t];
-        uint8_t* dst = cache + ((int64_t)(s / kBS) * heads + head) * page_bytes + (int64_t)(d * kBS + s % kBS) * E;
-        const uint8_t* col = tile + t * pitch + d * E;
-        if (m == X) {
-            uint32_t w[4];
-            if constexpr (E == 4) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint32_t*>(col + k * pitch);
-            } else if constexpr (E == 2) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = *reinterpret_cast<const uint16_t*>(col + 2 * k * pitch) |
-                           (uint32_t) * reinterpret_cast<const uint16_t*>(col + (2 * k + 1) * pitch) << 16;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = col[4 * k * pitch] | (uint32_t)col[(4 * k + 1) * pitch] << 8 |
-                           (uint32_t)col[(4 * k + 2) * pitch] << 16 | (uint32_t)col[(4 * k + 3) * pitch] << 24;
-            }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            for (int k = 0; k < m; ++k) {
-                if constexpr (E == 4)
-                    *reinterpret_cast<uint32_t*>(dst + 4 * k) = *reinterpret_cast<const uint32_t*>(col + k * pitch);
-                else if constexpr (E == 2)
-                    *reinterpret_cast<uint16_t*>(dst + 2 * k) = *reinterpret_cast<const uint16_t*>(col + k * pitch);
-                else
-                    dst[k] = col[k * pitch];
-            }
-        }
+    if (key) {
+        if (size == 64)
+            append_head<T, KV, LAYOUT, 64, true>(p, src, stride, cache, heads * page, p.k_scale, t0, n, tile);
+        else if (size == 128)
+            append_head<T, KV, LAYOUT, 128, true>(p, src, stride, cache, heads * page, p.k_scale, t0, n, tile);
+        else
+            append_head<T, KV, LAYOUT, 256, true>(p, src, stride, cache, heads * page, p.k_scale, t0, n, tile);
+    } else {
+        if (size == 64)
+            append_head<T, KV, LAYOUT, 64, false>(p, src, stride, cache, heads * page, p.v_scale, t0, n, tile);
+        else if (size == 128)
+            append_head<T, KV, LAYOUT, 128, false>(p, src, stride, cache, heads * page, p.v_scale, t0, n, tile);
+        else
+            append_head<T, KV, LAYOUT, 256, false>(p, src, stride, cache, heads * page, p.v_scale, t0, n, tile);
     }
 }
 

@@ -44,7 +44,7 @@ struct TablesParams {
 };
 
 struct Seq {
-    int keep, start, own, want;  // tokens kept, first row, pages before and after
+    int keep, start, n, own, want;  // tokens kept, first row, new tokens, pages before and after
     bool bad;
 };
 
@@ -56,11 +56,12 @@ __device__ __forceinline__ Seq load_seq(const TablesParams& p, int s) {
     q.start = p.query_start ? p.query_start[s] : s;
     q.bad = len < 0 || len > p.max_seq_len || q.keep < 0 || q.keep > len || q.start < 0 || end < q.start ||
             end > p.num_tokens || (s == 0 && q.start != 0) || end - q.start > p.max_seq_len - q.keep;
+    q.n = end - q.start;
     if (q.bad) {
-        q.keep = q.own = q.want = 0;
+        q.keep = q.n = q.own = q.want = 0;
     } else {
         q.own = (int)(((int64_t)len + kBS - 1) / kBS);
-        q.want = (int)(((int64_t)q.keep + (end - q.start) + kBS - 1) / kBS);
+        q.want = (int)(((int64_t)q.keep + q.n + kBS - 1) / kBS);
     }
     return q;
 }
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
     // of the chunk's sequences: first row, tokens kept, pages before, pages
     // after, ring entries taken / filled before it
     int* start = sm;
-    int* keep = start + chunk;
+    int* keep = start + chunk + 4;  // start[n]: the row behind the chunk's last
     int* own = keep + chunk;
     int* want = own + chunk;
     int* pop0 = want + chunk;
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
                 push0[j] = (int)(at & 0xffffffffu);
                 const int d = q[i].want - q[i].own;
                 at += d > 0 ? (uint64_t)d << 32 : (uint64_t)(-d);
+                if (s == S - 1 || j == chunk - 1) start[j + 1] = q[i].start + q[i].n;
             }
         }
         return carry + total;
@@ -168,7 +170,8 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
     if (!ok && blockIdx.x == 0 && tid == 0 && p.dev_error)
         atomicOr(p.dev_error, bad ? PA_DEVERR_SEQ_LEN : PA_DEVERR_POOL);
 
-    const int rows = !ok || S == 0 ? 0 : (p.query_start ? p.query_start[S] : S);  // rows with a token
+    const bool one_chunk = S <= chunk;
+    const int rows = !ok || S == 0 ? 0 : (one_chunk ? start[S] : (p.query_start ? p.query_start[S] : S));  // with a token
     const int step = (int)(gridDim.x * blockDim.x) * kRowsPerThread;
     const int first = (int)(blockIdx.x * blockDim.x + tid) * kRowsPerThread;
 
@@ -177,58 +180,51 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
         uint64_t carry = 0;
         for (int base = 0; base < S; base += chunk) {
             const int n = min(chunk, S - base);
-            if (S > chunk) {  // a further chunk: its sums again
+            if (!one_chunk) {  // a further chunk: its sums again
                 bool ignored = false;
                 __syncthreads();
                 carry = sum_chunk(base, carry, ignored);
                 __syncthreads();
             }
             const int row0 = start[0];
-            const int row1 = base + n < S ? (p.query_start ? p.query_start[base + n] : base + n) : rows;
+            const int row1 = start[n];
             // rows [row0, row1): four successive rows per thread
-            for (int64_t t0 = first; t0 < row1; t0 += step) {
-                if (t0 + kRowsPerThread <= row0) continue;
-                int slot[kRowsPerThread], pos[kRowsPerThread];
-                int j = -1;
+            auto page_id = [&](int j, int page, bool first_token) {
+                int32_t* entry = p.block_tables + (int64_t)(base + j) * p.max_blocks_per_seq + page;
+                if (page < own[j]) return *entry;
+                int64_t k = (int64_t)head + pop0[j] + (page - own[j]);
+                if (k >= N) k -= N;
+                const int id = p.free_ring[k];
+                if (first_token) *entry = id;  // of a new page: always one of this call's
+                return id;
+            };
+            auto slot_at = [&](int id, int off) {
+                if ((unsigned)id < (unsigned)N) return id * kBS + off;
+                bad_id = true;
+                return -1;
+            };
+            for (int64_t q = first; q < row1; q += step) {
+                if (q + kRowsPerThread <= row0) continue;
+                const int t = max((int)q, row0);
+                int j = p.query_start ? last_at_most(start, n, t) : t - base;
+                if (p.vec && t == q && t + kRowsPerThread <= start[j + 1]) {  // four tokens of one sequence
+                    const int pos = keep[j] + t - start[j], page = pos >> 4, off = pos & 15;
+                    const int id = page_id(j, page, off == 0);
+                    const int next = off > kBS - kRowsPerThread ? page_id(j, page + 1, true) : id;
+                    int slot[kRowsPerThread];
 #pragma unroll
-                for (int i = 0; i < kRowsPerThread; ++i) {
-                    const int t = (int)t0 + i;
-                    slot[i] = -1;
-                    pos[i] = 0;
-                    if (t < row0 || t >= row1) continue;
-                    if (j < 0) {
-                        j = p.query_start ? last_at_most(start, n, t) : t - base;
-                    } else {
-                        while (j + 1 < n && start[j + 1] <= t) ++j;
-                    }
-                    pos[i] = keep[j] + t - start[j];
-                    const int page = pos[i] / kBS, off = pos[i] % kBS;
-                    int32_t* entry = p.block_tables + (int64_t)(base + j) * p.max_blocks_per_seq + page;
-                    int id;
-                    if (page < own[j]) {
-                        id = *entry;
-                    } else {
-                        // the first token of a new page always is one of this call's
-                        int64_t k = (int64_t)head + pop0[j] + (page - own[j]);
-                        if (k >= N) k -= N;
-                        id = p.free_ring[k];
-                        if (off == 0) *entry = id;
-                    }
-                    if ((unsigned)id >= (unsigned)N)
-                        bad_id = true;
-                    else
-                        slot[i] = id * kBS + off;
-                }
-                if (p.vec && t0 >= row0 && t0 + kRowsPerThread <= row1) {
-                    *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                    for (int i = 0; i < kRowsPerThread; ++i)
+                        slot[i] = off + i < kBS ? slot_at(id, off + i) : slot_at(next, off + i - kBS);
+                    *reinterpret_cast<int4*>(p.slots + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
                     if (p.positions)
-                        *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-                } else {
-                    for (int i = 0; i < kRowsPerThread; ++i) {
-                        if (t0 + i < row0 || t0 + i >= row1) continue;
-                        p.slots[t0 + i] = slot[i];
-                        if (p.positions) p.positions[t0 + i] = pos[i];
-                    }
+                        *reinterpret_cast<int4*>(p.positions + t) = make_int4(pos, pos + 1, pos + 2, pos + 3);
+                    continue;
+                }
+                for (int r = t; r < q + kRowsPerThread && r < row1; ++r) {
+                    while (start[j + 1] <= r) ++j;  // ends: start[n] = row1
+                    const int pos = keep[j] + r - start[j], off = pos & 15;
+                    p.slots[r] = slot_at(page_id(j, pos >> 4, off == 0), off);
+                    if (p.positions) p.positions[r] = pos;
                 }
             }
             // pages put back by the chunk's sequences: one entry per thread
@@ -245,12 +241,10 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
         if (bad_id && p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
     }
     // padding
-    for (int64_t t0 = first; t0 < p.num_tokens; t0 += step)
-        for (int i = 0; i < kRowsPerThread; ++i) {
-            if (t0 + i < rows || t0 + i >= p.num_tokens) continue;
-            p.slots[t0 + i] = -1;
-            if (p.positions) p.positions[t0 + i] = 0;
-        }
+    for (int64_t t = rows + (int64_t)blockIdx.x * blockDim.x + tid; t < p.num_tokens; t += step / kRowsPerThread) {
+        p.slots[t] = -1;
+        if (p.positions) p.positions[t] = 0;
+    }
 
     // new lengths and pool state, once every CTA has read the old ones
     bool writes = true;
@@ -265,13 +259,17 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
     }
     if (!writes) return;
     for (int s = tid; s < S; s += blockDim.x) {
-        const int len = p.seq_lens[s];
-        int now = len;
-        if (ok) {
-            const int kept = p.keep_lens ? p.keep_lens[s] : len;
-            now = kept + (p.query_start ? p.query_start[s + 1] - p.query_start[s] : 1);
+        if (ok && one_chunk) {
+            p.new_seq_lens[s] = keep[s] + start[s + 1] - start[s];
+        } else {
+            const int len = p.seq_lens[s];
+            int now = len;
+            if (ok) {
+                const int kept = p.keep_lens ? p.keep_lens[s] : len;
+                now = kept + (p.query_start ? p.query_start[s + 1] - p.query_start[s] : 1);
+            }
+            p.new_seq_lens[s] = now;
         }
-        p.new_seq_lens[s] = now;
     }
     if (tid == 0) {
         p.new_pool_state[0] = ok ? (int)(((int64_t)head + pops) % N) : head;
@@ -330,11 +328,11 @@ extern "C" pa_status pa_build_tables(const pa_tables_args* a, void* stream) {
     if (grid > sm) grid = sm;
     if (grid < 1 || !a->done_counter) grid = 1;
 
-    const size_t smem = sizeof(int) * 6 * kItems * threads;  // 96 KB at 1024 threads
+    const size_t smem = sizeof(int) * (6 * kItems * threads + 4);  // 96 KB at 1024 threads
     static std::atomic<int> ready[pa::kHostDevices];
     if (dev >= pa::kHostDevices || !ready[dev].load()) {
         if (cudaFuncSetAttribute(pa_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(sizeof(int) * 6 * kItems * kMaxThreads)) != cudaSuccess)
+                                 (int)(sizeof(int) * (6 * kItems * kMaxThreads + 4))) != cudaSuccess)
             return PA_ERR_LAUNCH;
         if (dev < pa::kHostDevices) ready[dev].store(1);
     }

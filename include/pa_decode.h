@@ -331,7 +331,7 @@ typedef struct pa_launch_plan {
     int32_t ctas_per_sm;      /* resident CTAs per SM of the partition kernel */
     int32_t grid;             /* CTAs of the persistent partition-kernel grid */
     int32_t dynamic_schedule; /* 1: tiles claimed from tile_counters */
-    int32_t reserved;
+    int32_t partition_tokens; /* tokens per partition of v2: PA_PARTITION_SIZE, or what a differential call chose */
     int64_t tiles;            /* tiles of the partition kernel (an upper bound for unequal lengths) */
 } pa_launch_plan;
 
@@ -368,9 +368,10 @@ pa_status pa_plan(const pa_decode_args* args, pa_launch_plan* plan);
  *   key_cache    the layouts of pa_layout with 2 * num_kv_heads heads of
  *                head_size: heads 2g and 2g + 1 hold the keys of the two maps of kv head g
  *   value_cache  num_kv_heads heads of 2 * head_size
- *   exp_sums, max_logits [rows][num_heads][2][P], tmp_out [rows][num_heads][2][P][2 * head_size]:
- *                Phase 1 statistics per map, before lambda and norm (pa_workspace_elems
- *                with 2 * num_heads heads of 2 * head_size)
+ *   exp_sums, max_logits [rows][num_heads][2][P], tmp_out [rows][num_heads][2][P][2 * head_size]
+ *                (pa_workspace_elems with 2 * num_heads heads of 2 * head_size): room
+ *                for the maps' partitions, which the library makes as long as suits
+ *                the batch (pa_diff_plan tells); what it holds after the call is unspecified
  *   max_query_len * (num_heads / num_kv_heads) <= 8  (one tile holds both maps' rows)
  */
 typedef struct pa_diff_args {

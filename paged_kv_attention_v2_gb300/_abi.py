@@ -95,7 +95,7 @@ class PaLaunchPlan(ctypes.Structure):
         ("ctas_per_sm", ctypes.c_int32),
         ("grid", ctypes.c_int32),
         ("dynamic_schedule", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
+        ("partition_tokens", ctypes.c_int32),
         ("tiles", ctypes.c_int64),
     ]
 

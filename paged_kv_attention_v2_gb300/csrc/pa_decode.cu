@@ -232,6 +232,87 @@ pa_status dispatch(Prepared& pr, pa::LaunchOut* out) {
     return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
 }
 
+/*
+ * How a differential call cuts its sequences: one pass over each (v1, parts ==
+ * 0), or `parts` partitions of part_len tokens (a multiple of the page) for the
+ * longest one.  Its statistics are no part of the interface, so the partitions
+ * need not be PA_PARTITION_SIZE long: a tile costs about a microsecond at its end
+ * and writes both maps' outputs, which long sequences save by fewer and longer
+ * partitions (4 x 100000 bf16, groups of seven: 137 us with 196 partitions, 127
+ * with 33), and a short sequence is cut in halves rather than in 512 and a rest.
+ * The estimate, in microseconds, for n partitions:
+ *     rounds of the grid x (bytes of a tile / rate of a CTA + 1)  + 3.5 for the merge,
+ * where a CTA's rate is the least of its own (cta), its share of what the SM's
+ * consumers manage (sm) and its share of the memory's, as measured in KB/us; for
+ * sequences of different lengths the tiles go to whichever CTA is free, and the
+ * end is ragged by a tile.  At most the partitions the caller's workspace holds.
+ */
+struct Split {
+    int parts;
+    int part_len;
+};
+
+Split choose_split(const pa_decode_args* a, const Prepared& pr, int sms, int max_parts) {
+    const bool wide = pr.la.head_size > 128, two = pr.la.group_tiles == 2, f32 = a->dtype == PA_DTYPE_F32;
+    const bool fp8 = pr.kv != PA_KV_SAME;
+    double cta, sm;
+    if (wide) {
+        cta = sm = f32 ? 24e3 : fp8 ? (two ? 37e3 : 45e3) : (two ? 51e3 : 55e3);
+    } else {
+        cta = f32 ? (two ? 31e3 : 20e3) : fp8 ? 19e3 : (two ? 30e3 : 38e3);
+        sm = f32 ? (two ? 31e3 : 36e3) : fp8 ? (two ? 31e3 : 40e3) : 76e3;
+    }
+    const double memory = 6.8e6;
+    const double token = 2.0 * pr.la.head_size * (fp8 ? 1 : (f32 ? 4 : 2));  // bytes of a token of one kv head
+    const int64_t resident = (int64_t)sms * pr.ctas_per_sm, heads = (int64_t)a->num_seqs * a->num_kv_heads;
+    const int64_t longest = a->max_seq_len > 0 ? a->max_seq_len : 1, pages = (longest + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
+    bool equal = true;
+    double total = (double)longest * a->num_seqs;
+    if (a->seq_lens_host) {
+        total = 0;
+        for (int32_t i = 0; i < a->num_seqs; ++i) {
+            int64_t l = a->seq_lens_host[i];
+            l = l < 0 ? 0 : (l > longest ? longest : l);
+            total += (double)l;
+            equal = equal && l == (a->seq_lens_host[0] < longest ? a->seq_lens_host[0] : longest);
+        }
+    }
+    Split best = {0, PA_PARTITION_SIZE};
+    double least = -1;
+    const int tries = max_parts < 64 ? max_parts : 64;
+    for (int n = a->mode == PA_MODE_V2 ? 1 : 0; n <= tries; ++n) {
+        if (a->mode == PA_MODE_V1 && n > 0) break;
+        if (n == 1 && max_parts > 1) continue;  // one partition: the pass without a merge is better
+        // 0: one pass; the last try: as many as there may be
+        const int64_t want = n == 0 ? 1 : (n == tries ? max_parts : n);
+        const int64_t len = (pages + want - 1) / want * PA_BLOCK_SIZE, parts = (longest + len - 1) / len;
+        const double tokens = (double)(len < longest ? len : longest);
+        double t;
+        if (equal) {
+            const int64_t tiles = heads * parts, rounds = (tiles + resident - 1) / resident;
+            const int64_t grid = (tiles + rounds - 1) / rounds;
+            double rate = sm / (double)((grid + sms - 1) / sms);
+            if (cta < rate) rate = cta;
+            if (memory / (double)grid < rate) rate = memory / (double)grid;
+            t = (double)rounds * (tokens * token / rate + 1.0);
+        } else {
+            const double tiles = total * a->num_kv_heads / tokens + 0.5 * (double)heads;
+            const double grid = tiles < (double)resident ? tiles : (double)resident;
+            double rate = sm / std::ceil(grid / sms);
+            if (cta < rate) rate = cta;
+            if (memory / grid < rate) rate = memory / grid;
+            t = total * a->num_kv_heads * token / (grid * rate) + (tiles < grid ? 1.0 : tiles / grid) + tokens * token / rate;
+        }
+        if (n > 0) t += 3.5;
+        if (least < 0 || t < least) {
+            least = t;
+            best.parts = n == 0 ? 0 : (int)parts;
+            best.part_len = (int)len;
+        }
+    }
+    return best;
+}
+
 // Host-visible checks of pa_decode (every error returned before any launch),
 // then the kernel parameters, the v1 / v2 choice and the tile order.  With `df`
 // (whose decode member `a` is) the call is a differential one: num_heads and
@@ -333,6 +414,7 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
     p.withhold_page = g_withhold_page.load();
     p.tile_ctr = nullptr;  // set below once the mode is known
     p.metadata_ready = a->metadata_ready ? 1 : 0;
+    p.part_len = PA_PARTITION_SIZE;
     if (df) {
         p.lambdas = df->lambdas;
         p.lambda_stride = df->lambda_row_stride;
@@ -368,13 +450,22 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
         pr.ctas_per_sm = lo.occ;
     }
     int mode = a->mode;
-    if (mode == PA_MODE_AUTO)
+    int parts = max_parts;  // partitions of the longest sequence
+    if (df) {
+        const Split sp = choose_split(a, pr, sm, max_parts);
+        mode = sp.parts == 0 ? PA_MODE_V1 : PA_MODE_V2;
+        if (mode == PA_MODE_V2) {
+            parts = sp.parts;
+            p.part_len = sp.part_len;
+            p.max_parts = parts;
+        }
+    } else if (mode == PA_MODE_AUTO)
         mode = pa_choose_mode_for_lengths(a->num_seqs, a->num_kv_heads, a->max_seq_len, sm, pr.ctas_per_sm,
                                           a->seq_lens_host);
     const bool v1 = mode == PA_MODE_V1;
     if (!v1 && !workspace_ok()) return PA_ERR_WORKSPACE;
     p.v1 = v1 ? 1 : 0;
-    la.tiles_upper = (int64_t)a->num_seqs * (v1 ? 1 : max_parts) * a->num_kv_heads;
+    la.tiles_upper = (int64_t)a->num_seqs * (v1 ? 1 : parts) * a->num_kv_heads;
     // Dynamic tile schedule: only for batches whose tiles differ in size (the
     // host lengths hold sequences of different page counts in v1, partition
     // counts in v2), where it balanced the ragged workload (551 -> 536 us);
@@ -384,7 +475,7 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
         auto units_of = [&](int32_t i) {
             int64_t l = a->seq_lens_host[i];
             l = l < 0 ? 0 : (l > a->max_seq_len ? a->max_seq_len : l);
-            return v1 ? (l + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE : (l + PA_PARTITION_SIZE - 1) / PA_PARTITION_SIZE;
+            return v1 ? (l + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE : (l + p.part_len - 1) / p.part_len;
         };
         bool varied = false;
         const int64_t u0 = units_of(0);
@@ -399,7 +490,7 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
         if (l2_bytes_for_current_device(&l2) != 0) return PA_ERR_LAUNCH;
         const int64_t rows = multi ? a->num_query_tokens : a->num_seqs;
         const int64_t heads = df ? 2 * (int64_t)a->num_heads : a->num_heads;  // rows of tmp_out
-        const int64_t tmp_bytes = v1 ? 0 : rows * heads * max_parts * la.head_size * 4;
+        const int64_t tmp_bytes = v1 ? 0 : rows * heads * parts * la.head_size * 4;
         p.kv_evict_first = tmp_bytes <= (int64_t)l2 / 2 ? 1 : 0;
     }
     return PA_OK;
@@ -420,6 +511,7 @@ pa_status plan_of(const pa_decode_args* a, const pa_diff_args* df, Prepared& pr,
     plan->ctas_per_sm = pr.ctas_per_sm;
     plan->grid = (int32_t)lo.grid;
     plan->dynamic_schedule = pr.p.tile_ctr ? 1 : 0;
+    plan->partition_tokens = pr.p.part_len;
     plan->tiles = pr.la.tiles_upper;
     return PA_OK;
 }

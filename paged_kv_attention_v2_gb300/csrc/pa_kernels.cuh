@@ -55,13 +55,17 @@ constexpr int kConsumerWarps = 4;  // consumer warps per CTA
 constexpr int kConsumerWarps5 = 5; // consumer warps per CTA, 16-bit or fp32 caches with one n-tile
 constexpr int kPrefetchPages = 16; // pages of the first tile prefetched into L2 before the grid wait
 // Value heads of 256 (differential attention with keys of 128): stages twice as
-// large, one CTA per SM.
-constexpr int kStages16Wide = 8;   // 16-bit caches: 16 KB each, eight consumer warps
-constexpr int kStagesFp8Wide = 16; // fp8 caches: 8 KB each, eight consumer warps
-constexpr int kStagesF32Wide = 4;  // fp32 caches: 32 KB each, four consumer warps
-constexpr int kConsumerWarpsWide = 8;
+// large, one CTA per SM.  16-bit caches: five warps and ten stages (one n-tile),
+// six warps in three page streams and nine stages (two), which leave the warps
+// all the registers they want (eight warps are capped at 168 and spill: 64 ragged
+// sequences, keys of 128 bf16, 171 -> 150 us; 4 x 50000, groups of seven, 150 -> 143).
+constexpr int kStages16Wide = 10, kConsumerWarps16Wide = 5;
+constexpr int kStages16Widex2 = 9, kConsumerWarps16Widex2 = 6;
+constexpr int kStagesFp8Wide = 16, kConsumerWarpsFp8Wide = 8;  // fp8 caches: 8 KB stages
+constexpr int kStagesF32Wide = 4, kConsumerWarpsF32Wide = 4;   // fp32 caches: 32 KB stages
 constexpr int kReduceWarpMaxParts = 64;  // warp-per-row reduce up to this many partitions per row
 
+constexpr int kDiffReduceFewParts = 4;  // differential rows: one warp per row up to this many partitions
 constexpr int kReduceWarpsPerCta = 8;  // warp-per-row reduce: rows per CTA
 
 struct Params {
@@ -95,6 +99,7 @@ struct Params {
     uint32_t zero;           // 0 (mbar_arrive_after)
     // differential attention (the DIFF kernels): num_heads and group count
     // differential heads; statistics and tmp_out have two rows per head, one per map
+    int part_len;            // tokens per partition (kPart in the other kernels)
     const float* lambdas;    // lambda of (row, head) at row * lambda_stride + head
     int64_t lambda_stride;
     const float* norm_weight;  // [value head size], or NULL (ones)
@@ -113,6 +118,26 @@ __device__ __forceinline__ void report(const Params& p, int bits) {
 
 __device__ __forceinline__ int clamp_len(const Params& p, int raw) {
     return raw < 0 ? 0 : (raw > p.max_seq_len ? p.max_seq_len : raw);
+}
+
+// Tokens per partition: fixed, or for a differential call as the host chose.
+template <bool DIFF>
+__device__ __forceinline__ int part_len(const Params& p) {
+    if constexpr (DIFF) return p.part_len;
+    return kPart;
+}
+
+// cap * tanh(v / cap).  The differential kernels, whose consumers are short of
+// issue slots with both maps' logits, take tanh(x) = 1 - 2 / (exp(2x) + 1) with the
+// hardware's exponential and reciprocal: a few steps of 1 in absolute terms (the
+// logit is off by some 2^-22 cap), infinities included.
+template <bool DIFF>
+__device__ __forceinline__ float soft_cap(const Params& p, float v) {
+    if constexpr (DIFF) {
+        const float e = exp2f(v * p.inv_softcap * (2.f * kLog2e));
+        return p.softcap - __fdividef(2.f * p.softcap, e + 1.f);
+    }
+    return p.softcap * tanhf(v * p.inv_softcap);
 }
 
 // First key inside the sliding window of a query at position pos (0 without one).
@@ -294,8 +319,9 @@ __device__ void prefetch_first_tile(const Params& p, int lane) {
     guess_unit(p, u, seq, part);
     if (seq >= p.num_seqs) return;
     const int len = clamp_len(p, __ldcg(p.seq_lens + seq));
-    const int tb = part * kPart;
-    const int te = p.v1 ? len : min(len, tb + kPart);
+    const int plen = part_len<C::kDiff>(p);
+    const int tb = part * plen;
+    const int te = p.v1 ? len : min(len, tb + plen);
     const int npg = min(kPrefetchPages, tile_pages(tb, te));
     if (lane < npg) {
         const int blk = __ldcg(p.block_tables + (int64_t)seq * p.max_blocks_per_seq + tb / kBS + lane);
@@ -320,6 +346,7 @@ template <class C, int HEAD, int STAGES>
 __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk,
                          const CUtensorMap* tmv, int lane) {
     const int S = p.num_seqs, Hkv = p.num_kv_heads;
+    const int plen = part_len<C::kDiff>(p);
     const char* kbase = static_cast<const char*>(p.key_cache);
     const char* vbase = static_cast<const char*>(p.value_cache);
     const char* qbase = static_cast<const char*>(p.query);
@@ -346,8 +373,8 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
             // v1: one tile per sequence; v2: one per partition that has keys in
             // the window (fused v2 keeps one empty tile for an empty sequence so
             // that its output row is written)
-            c_p0 = window_lo(p, c_len, c_qn) / kPart;
-            c_units = p.v1 ? 1 : (c_len + kPart - 1) / kPart - c_p0;
+            c_p0 = window_lo(p, c_len, c_qn) / plen;
+            c_units = p.v1 ? 1 : (c_len + plen - 1) / plen - c_p0;
             if (p.fused && c_units == 0) c_units = 1;
         }
         c_incl = c_units;
@@ -365,7 +392,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
     if (!p.v1 && p.window_left < 0) {
         int spec_part;
         guess_unit(p, (int)blockIdx.x / Hkv, spec_seq, spec_part);
-        spec_tb = spec_part * kPart;
+        spec_tb = spec_part * plen;
         const int idx = spec_tb / kBS + lane;
         if (spec_seq < S && idx < p.max_blocks_per_seq)
             spec_ids = __ldg(p.block_tables + (int64_t)spec_seq * p.max_blocks_per_seq + idx);
@@ -417,8 +444,8 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
         t.qn = __shfl_sync(0xffffffffu, c_qn, j);
         const int lo = window_lo(p, t.len, t.qn);
         t.part = __shfl_sync(0xffffffffu, c_p0, j) + rel - excl;
-        t.tb = p.v1 ? lo : max(t.part * kPart, lo);
-        t.te = p.v1 ? t.len : min(t.len, t.part * kPart + kPart);
+        t.tb = p.v1 ? lo : max(t.part * plen, lo);
+        t.te = p.v1 ? t.len : min(t.len, t.part * plen + plen);
         t.npages = tile_pages(t.tb, t.te);
         t.valid = true;
         return t;
@@ -785,7 +812,7 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
 template <typename T, int HEAD, bool L2ONLY>
 __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int h, int len, int qn, int qi,
                                                int lane);
-template <int HEAD, bool L2ONLY>
+template <int HEAD, bool L2ONLY, bool DIFF>
 __device__ __forceinline__ void merge_stats_row(const Params& p, int64_t srow, int h, int len, int qn, int qi,
                                                 int lane, float (&acc)[HEAD / 32]);
 
@@ -804,7 +831,7 @@ __device__ __noinline__ void merge_group(const Params& p, int seq_kvh_base, int 
             float o[2][HEAD / 32];
 #pragma unroll
             for (int map = 0; map < 2; ++map)
-                merge_stats_row<HEAD, true>(p, 2 * (row * p.num_heads + h) + map, h, len, qn, qi, lane, o[map]);
+                merge_stats_row<HEAD, true, true>(p, 2 * (row * p.num_heads + h) + map, h, len, qn, qi, lane, o[map]);
             diff_row<T, HEAD>(p, row, h, o[0], o[1], lane);
         } else {
             merge_row_warp<T, HEAD, true>(p, (int64_t)q0 + qi, seq_kvh_base + (r - qi * G), len, qn, qi, lane);
@@ -826,7 +853,8 @@ __device__ bool tile_finish(const Params& p, const TileDesc& d, const Smem& sm, 
     if (!consumer_sync(sm, mphase, lane)) return false;  // epilogue done, merge buffers free
     if (!p.fused || p.v1) return true;
     if (tid == 0) {
-        const int P = (d.len + kPart - 1) / kPart - window_lo(p, d.len, d.qn) / kPart;
+        const int plen = part_len<C::kDiff>(p);
+        const int P = (d.len + plen - 1) / plen - window_lo(p, d.len, d.qn) / plen;
         int* counter = p.counters + (int64_t)d.seq * p.num_kv_heads + d.kvh;
         // releases this CTA's partition results (every warp's, seen through the
         // barrier above) before the count; acquires the others' with it
@@ -1215,7 +1243,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = s[nt][e] * p.scale;
-                    if (has_cap) v = p.softcap * tanhf(v * p.inv_softcap);
+                    if (has_cap) v = soft_cap<C::kDiff>(p, v);
                     if (has_alibi) v += sl[nt][e & 1] * (float)(tlo + ((e >> 1) << 3) - origin);
                     z[nt][e] = v;
                 }
@@ -1591,7 +1619,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = (s[nt][e] + s2[nt][e]) * p.scale;
-                    if (has_cap) v = p.softcap * tanhf(v * p.inv_softcap);
+                    if (has_cap) v = soft_cap<C::kDiff>(p, v);
                     if (has_alibi) v += sl[nt][e & 1] * (float)(tok0 + ((e >> 1) ? thi : tlo) - origin);
                     z[nt][e] = v;
                 }
@@ -1897,7 +1925,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = (s[nt][e] + s2[nt][e]) * p.scale;
-                    if (has_cap) v = p.softcap * tanhf(v * p.inv_softcap);
+                    if (has_cap) v = soft_cap<C::kDiff>(p, v);
                     if (has_alibi) v += sl[nt][e & 1] * (float)(tok0 + r + ((e >> 1) << 3) - origin);
                     z[nt][e] = v;
                 }
@@ -2017,11 +2045,15 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 // two n-tiles fills an SM's shared memory with one CTA (16 KB stages): no cap.
 // fp8 with one n-tile: capped for three CTAs per SM (128 registers: fifteen
 // warps put four on some SM sub-partition, whose register file is 16 K).
-// Value heads of 256 hold one CTA per SM.
+// Value heads of 256 hold one CTA per SM.  Differential fp8 kernels with two
+// n-tiles hold one n-tile's registers per warp: three CTAs too (4 x 100000 e4m3,
+// groups of seven: 132 us with two, 102 with three, 118 with four, which spill).
 template <typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV, bool MQ, bool DIFF>
 __global__ void __launch_bounds__((NC + 1) * 32,
                                   (HEAD > 128 || (std::is_same<T, float>::value && NT > 1))
                                       ? 1
+                                      : (DIFF && KV != kKvSame)
+                                      ? 3
                                       : ((NT > 1 || std::is_same<T, float>::value) ? 2 : (KV != kKvSame ? 3 : 1)))
     pa_partition_kernel(const Params p, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {
@@ -2119,7 +2151,7 @@ __global__ void __launch_bounds__(WARPS * 32) pa_reduce_kernel(const Params p) {
     const int len = clamp_len(p, p.seq_lens[s]);
     const int hi = len - qn + qi;                      // the query token's position
     const int P = hi >= 0 ? (hi + kPart) / kPart : 0;  // partitions holding its keys
-    const int p0 = window_lo_at(p, hi) / kPart;        // partitions before p0: outside the window
+    const int p0 = window_lo_at(p, hi) / kPart;     // partitions before p0: outside the window
     const int64_t row = (int64_t)q0 + qi;
     const int64_t sb = (row * p.num_heads + h) * p.max_parts;
     float* ml = p.max_logits + sb;
@@ -2235,14 +2267,15 @@ __global__ void __launch_bounds__(WARPS * 32) pa_reduce_kernel(const Params p) {
 // outputs are read with an evict_first hint (their last use).
 // merge_stats_row does this for one row `srow` of the statistics, leaving the
 // merged output row in acc (columns lane_col).
-template <int HEAD, bool L2ONLY>
+template <int HEAD, bool L2ONLY, bool DIFF>
 __device__ __forceinline__ void merge_stats_row(const Params& p, int64_t srow, int h, int len, int qn, int qi,
                                                 int lane, float (&acc)[HEAD / 32]) {
     constexpr int VEC = HEAD / 32;  // columns per lane: 8 (HEAD 256), 4 (HEAD 128) or 2 (HEAD 64)
     constexpr int PRE = 8;          // partition outputs loaded before the weights are known
     const int hi = len - qn + qi;                      // the query token's position
-    const int P = hi >= 0 ? (hi + kPart) / kPart : 0;  // partitions holding its keys
-    const int p0 = window_lo_at(p, hi) / kPart;        // partitions before p0: outside the window
+    const int plen = part_len<DIFF>(p);
+    const int P = hi >= 0 ? (hi + plen) / plen : 0;  // partitions holding its keys
+    const int p0 = window_lo_at(p, hi) / plen;     // partitions before p0: outside the window
     const int64_t sb = srow * p.max_parts;
     float* ml = p.max_logits + sb;
     float* es = p.exp_sums + sb;
@@ -2355,7 +2388,7 @@ template <typename T, int HEAD, bool L2ONLY>
 __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int h, int len, int qn, int qi,
                                                int lane) {
     float acc[HEAD / 32];
-    merge_stats_row<HEAD, L2ONLY>(p, row * p.num_heads + h, h, len, qn, qi, lane, acc);
+    merge_stats_row<HEAD, L2ONLY, false>(p, row * p.num_heads + h, h, len, qn, qi, lane, acc);
     store_row<T, HEAD>(static_cast<T*>(p.out) + (row * p.num_heads + h) * HEAD, acc, lane);
 }
 
@@ -2382,11 +2415,150 @@ __global__ void __launch_bounds__(kReduceWarpsPerCta * 32) pa_reduce_warp_kernel
     merge_row_warp<T, HEAD, false>(p, (int64_t)q0 + qi, h, len, qn, qi, lane);
 }
 
-// Phase 2 of differential rows, few partitions: two warps per (sequence, query
-// token, head), one map each (the two merges' round trips overlap); the second
-// hands its row to the first through shared memory.
+// Phase 2 of differential rows, up to kDiffReduceFewParts partitions: one warp per
+// (sequence, query token, head), both maps side by side: the first PRE partition
+// outputs of both are loaded with the statistics, so a row of up to PRE partitions
+// costs one round trip after its length.  (256 x 1000, 4096 rows: 82.5 us for
+// the whole call, with two warps per row 87; but with eight partitions 48.8
+// against 46, so pa_diff_reduce_pair_kernel takes those.)
 template <typename T, int HEAD, bool MQ>
-__global__ void __launch_bounds__(kReduceWarpsPerCta * 32) pa_diff_reduce_warp_kernel(const Params p) {
+__global__ void __launch_bounds__(kReduceWarpsPerCta * 32, HEAD > 128 ? 2 : 4) pa_diff_reduce_warp_kernel(const Params p) {
+    constexpr int VEC = HEAD / 32, PRE = HEAD > 128 ? 2 : 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    const int64_t rid = (int64_t)blockIdx.x * kReduceWarpsPerCta + warp;
+    const int64_t nrows = (int64_t)p.num_seqs * (MQ ? p.max_q_len : 1) * p.num_heads;
+    if (rid >= nrows) return;
+    const int sq = (int)(rid / p.num_heads), h = (int)(rid - (int64_t)sq * p.num_heads);
+    const int s = MQ ? sq / p.max_q_len : sq, qi = MQ ? sq - s * p.max_q_len : 0;
+    int q0 = s, qn = 1;
+    if constexpr (MQ) {
+        query_rows(p, s, q0, qn);
+        if (qi >= qn) return;
+    }
+    const int len = clamp_len(p, p.seq_lens[s]);
+    const int hi = len - qn + qi;                       // the query token's position
+    const int plen = part_len<true>(p);
+    const int P = hi >= 0 ? (hi + plen) / plen : 0;     // partitions holding its keys
+    const int p0 = window_lo_at(p, hi) / plen;          // partitions before p0: outside the window
+    const int64_t row = (int64_t)q0 + qi, sb = 2 * (row * p.num_heads + h) * p.max_parts;
+    const uint64_t pol = l2_policy_evict_first();       // partition outputs: last use
+    auto load_out = [&](int map, int q, float (&t)[VEC]) {
+        const float* at = p.tmp_out + (sb + (int64_t)map * p.max_parts + q) * HEAD + lane * 4;
+#pragma unroll
+        for (int c = 0; c < VEC; c += 4) {
+            const float4 v = ld_global_v4_hint(at + c * 32, pol);
+            t[c] = v.x; t[c + 1] = v.y; t[c + 2] = v.z; t[c + 3] = v.w;
+        }
+    };
+    float* ml[2] = {p.max_logits + sb, p.max_logits + sb + p.max_parts};
+    float* es[2] = {p.exp_sums + sb, p.exp_sums + sb + p.max_parts};
+
+    float pre[2][PRE][VEC];
+#pragma unroll
+    for (int map = 0; map < 2; ++map)
+#pragma unroll
+        for (int k = 0; k < PRE; ++k) {
+            if (p0 + k < P) {
+                load_out(map, p0 + k, pre[map][k]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) pre[map][k][v] = 0.f;
+            }
+        }
+    const int q1 = p0 + lane;
+    float m1[2], e1[2], M[2], invW[2];
+#pragma unroll
+    for (int map = 0; map < 2; ++map) {
+        m1[map] = q1 < P ? ml[map][q1] : -INFINITY;
+        e1[map] = q1 < P ? es[map][q1] : 0.f;
+    }
+#pragma unroll
+    for (int map = 0; map < 2; ++map) {
+        // global max and weight sum over the row's partitions (lanes, then the warp)
+        float m = m1[map], w = m == -INFINITY ? 0.f : e1[map];
+        for (int q = q1 + 32; q < P; q += 32) {
+            const float mq = ml[map][q], eq = es[map][q];
+            if (mq == -INFINITY) continue;
+            if (mq > m) {
+                w = m == -INFINITY ? 0.f : w * expf(m - mq);
+                m = mq;
+            }
+            w += expf(mq - m) * eq;
+        }
+        float mx = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        w = m == -INFINITY ? 0.f : w * expf(m - mx);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        M[map] = mx;
+        invW[map] = w > 0.f ? 1.f / w : 0.f;
+    }
+
+    float o[2][VEC];
+#pragma unroll
+    for (int map = 0; map < 2; ++map) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) o[map][v] = 0.f;
+        // lane i holds the weight of partition p0 + 32 j + i of the current group j
+        float c = m1[map] == -INFINITY ? 0.f : expf(m1[map] - M[map]) * e1[map] * invW[map];
+#pragma unroll
+        for (int k = 0; k < PRE; ++k) {
+            const float ck = __shfl_sync(0xffffffffu, c, k);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) o[map][v] = fmaf(ck, pre[map][k][v], o[map][v]);
+        }
+        for (int qb = p0 + PRE; qb < P; qb += PRE) {
+            if (((qb - p0) & 31) == 0) {
+                const int q = qb + lane;
+                c = 0.f;
+                if (q < P) {
+                    const float mq = ml[map][q];
+                    c = mq == -INFINITY ? 0.f : expf(mq - M[map]) * es[map][q] * invW[map];
+                }
+            }
+            float t[PRE][VEC];
+#pragma unroll
+            for (int k = 0; k < PRE; ++k) {
+                if (qb + k < P) {
+                    load_out(map, qb + k, t[k]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) t[k][v] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < PRE; ++k) {
+                const float ck = __shfl_sync(0xffffffffu, c, (qb - p0 + k) & 31);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) o[map][v] = fmaf(ck, t[k][v], o[map][v]);
+            }
+        }
+    }
+    diff_row<T, HEAD>(p, row, h, o[0], o[1], lane);
+    // statistics: sequence frame -> absolute ALiBi positions; unused partitions
+    // padded (every read of this row's statistics is above, in this warp)
+    __syncwarp();
+    const float shift = p.alibi ? __ldg(p.alibi + h) * (float)(len - 1) : 0.f;
+    for (int q = lane; q < 2 * p.max_parts; q += 32) {
+        const int map = q >= p.max_parts, at = q - map * p.max_parts;
+        if (at >= p0 && at < P) {
+            if (p.alibi) ml[map][at] += shift;
+        } else {
+            ml[map][at] = -INFINITY;
+            es[map][at] = 0.f;
+        }
+    }
+}
+
+// Phase 2 of differential rows, more partitions: two warps per (sequence, query
+// token, head), one map each (eight partition outputs in flight per map); the
+// second hands its row to the first through shared memory.
+template <typename T, int HEAD, bool MQ>
+__global__ void __launch_bounds__(kReduceWarpsPerCta * 32) pa_diff_reduce_pair_kernel(const Params p) {
     constexpr int VEC = HEAD / 32, ROWS = kReduceWarpsPerCta / 2;
     __shared__ float second[ROWS][HEAD];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, map = warp & 1;
@@ -2406,8 +2578,8 @@ __global__ void __launch_bounds__(kReduceWarpsPerCta * 32) pa_diff_reduce_warp_k
     const int64_t row = (int64_t)q0 + qi;
     float o[VEC];
     if (mine) {
-        merge_stats_row<HEAD, false>(p, 2 * (row * p.num_heads + h) + map, h, clamp_len(p, p.seq_lens[s]), qn, qi,
-                                     lane, o);
+        merge_stats_row<HEAD, false, true>(p, 2 * (row * p.num_heads + h) + map, h, clamp_len(p, p.seq_lens[s]), qn,
+                                           qi, lane, o);
         if (map)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) second[warp >> 1][lane_col<HEAD>(lane, v)] = o[v];
@@ -2448,8 +2620,9 @@ __global__ void __launch_bounds__(WARPS * 32) pa_diff_reduce_kernel(const Params
     }
     const int len = clamp_len(p, p.seq_lens[s]);
     const int hi = len - qn + qi;                      // the query token's position
-    const int P = hi >= 0 ? (hi + kPart) / kPart : 0;  // partitions holding its keys
-    const int p0 = window_lo_at(p, hi) / kPart;        // partitions before p0: outside the window
+    const int plen = part_len<true>(p);
+    const int P = hi >= 0 ? (hi + plen) / plen : 0;  // partitions holding its keys
+    const int p0 = window_lo_at(p, hi) / plen;     // partitions before p0: outside the window
     const int64_t row = (int64_t)q0 + qi;
     const int64_t sb = (2 * (row * p.num_heads + h) + map) * p.max_parts;
     float* ml = p.max_logits + sb;

@@ -45,10 +45,16 @@ constexpr int kMaxDevices = 64;
 template <typename T, int HEAD, int NT, int LAYOUT, int KV, bool MQ, bool DIFF = false>
 cudaError_t launch_main(const Params& p_in, const LaunchArgs& la, bool* fused) {
     constexpr bool F32 = std::is_same<T, float>::value, WIDE = HEAD > 128;
-    constexpr int STAGES = WIDE ? (F32 ? kStagesF32Wide : (KV == kKvSame ? kStages16Wide : kStagesFp8Wide))
+    constexpr int STAGES = WIDE ? (F32               ? kStagesF32Wide
+                                   : KV != kKvSame ? kStagesFp8Wide
+                                   : NT == 1       ? kStages16Wide
+                                                   : kStages16Widex2)
                            : F32 ? (NT == 1 ? kStagesF32 : kStagesF32x2)
                                  : (KV == kKvSame ? (NT == 1 ? kStages16 : kStages16x2) : kStagesFp8);
-    constexpr int NC = WIDE ? (F32 ? kConsumerWarps : kConsumerWarpsWide)
+    constexpr int NC = WIDE ? (F32               ? kConsumerWarpsF32Wide
+                               : KV != kKvSame ? kConsumerWarpsFp8Wide
+                               : NT == 1       ? kConsumerWarps16Wide
+                                               : kConsumerWarps16Widex2)
                             : ((KV == kKvSame && NT == 1) ? kConsumerWarps5 : kConsumerWarps);
     using C = Cfg<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ, DIFF>;
     auto kern = pa_partition_kernel<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ, DIFF>;
@@ -208,9 +214,13 @@ cudaError_t launch_diff_reduce(const Params& p, const LaunchArgs& la) {
         cfg.blockDim = dim3(16 * 32);
         return cudaLaunchKernelEx(&cfg, pa_diff_reduce_kernel<T, HEAD, 16, HEAD == 128 ? 8 : 4, MQ>, p);
     }
-    cfg.gridDim = dim3((unsigned)((rows + kReduceWarpsPerCta / 2 - 1) / (kReduceWarpsPerCta / 2)));
     cfg.blockDim = dim3(kReduceWarpsPerCta * 32);
-    return cudaLaunchKernelEx(&cfg, pa_diff_reduce_warp_kernel<T, HEAD, MQ>, p);
+    if (p.max_parts <= kDiffReduceFewParts) {
+        cfg.gridDim = dim3((unsigned)((rows + kReduceWarpsPerCta - 1) / kReduceWarpsPerCta));
+        return cudaLaunchKernelEx(&cfg, pa_diff_reduce_warp_kernel<T, HEAD, MQ>, p);
+    }
+    cfg.gridDim = dim3((unsigned)((rows + kReduceWarpsPerCta / 2 - 1) / (kReduceWarpsPerCta / 2)));
+    return cudaLaunchKernelEx(&cfg, pa_diff_reduce_pair_kernel<T, HEAD, MQ>, p);
 }
 
 template <typename T, int HEAD, int NT, int KV, bool MQ>

@@ -128,7 +128,8 @@ def diff_plan(args: _abi.PaDiffArgs) -> dict:
     return {"mode": "v1" if pl.mode == _abi.PA_MODE_V1 else "v2",
             "merge_in_kernel": bool(pl.merge_in_kernel), "kernels": int(pl.kernels),
             "ctas_per_sm": int(pl.ctas_per_sm), "grid": int(pl.grid),
-            "dynamic_schedule": bool(pl.dynamic_schedule), "tiles": int(pl.tiles)}
+            "dynamic_schedule": bool(pl.dynamic_schedule), "tiles": int(pl.tiles),
+            "partition_tokens": int(pl.partition_tokens)}
 
 
 def pa_diff_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *, lambdas, stream=None, **kw) -> None:

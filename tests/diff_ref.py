@@ -49,12 +49,12 @@ def logical(cache, table, length, layout, is_key, kv):
     return c.reshape(-1, c.shape[2], c.shape[3])[:length].numpy()
 
 
-def diff_ref(case):
+def diff_ref(case, part=PART):
     """out, tol [rows, heads, 2d]; max_logits, exp_sums [rows, heads, 2, P] in 64 bits."""
     q = case["query"].double().numpy()
     rows, heads, _, d = q.shape
     g = heads // case["kv_heads"]
-    parts = max(1, -(-case["max_seq_len"] // PART))
+    parts = max(1, -(-case["max_seq_len"] // part))
     out, tol = np.zeros((rows, heads, 2 * d)), np.zeros((rows, heads, 2 * d))
     ml = np.full((rows, heads, 2, parts), -np.inf)
     es = np.zeros((rows, heads, 2, parts))
@@ -97,8 +97,8 @@ def diff_ref(case):
                     a = np.exp(z - zmax)
                     total = a.sum()
                     a /= total
-                    for p in range(lo // PART, pos // PART + 1):
-                        zp = z[(t // PART) == p]
+                    for p in range(lo // part, pos // part + 1):
+                        zp = z[(t // part) == p]
                         ml[r, h, m, p], es[r, h, m, p] = zp.max(), np.exp(zp - zp.max()).sum()
                     av = a @ np.abs(vv)
                     o.append(a @ vv)

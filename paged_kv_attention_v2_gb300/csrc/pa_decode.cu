@@ -241,27 +241,39 @@ pa_status dispatch(Prepared& pr, pa::LaunchOut* out) {
  * partitions (4 x 100000 bf16, groups of seven: 137 us with 196 partitions, 127
  * with 33), and a short sequence is cut in halves rather than in 512 and a rest.
  * The estimate, in microseconds, for n partitions:
- *     rounds of the grid x (bytes of a tile / rate of a CTA + 1)  + 3.5 for the merge,
- * where a CTA's rate is the least of its own (cta), its share of what the SM's
- * consumers manage (sm) and its share of the memory's, as measured in KB/us; for
- * sequences of different lengths the tiles go to whichever CTA is free, and the
- * end is ragged by a tile.  At most the partitions the caller's workspace holds.
+ *     rounds of the grid x (time of a tile + tile_us) + 3.5 for the merge,
+ * a tile taking the longer of its bytes at its share of the memory's rate and its
+ * pages, in whole turns of the CTA's page streams, at the rate of a CTA alone
+ * (cta) or its share of what an SM's consumers manage (sm).  For sequences of
+ * different lengths the tiles go to whichever CTA is free, and the end is ragged
+ * by a tile.  At most as many partitions as the caller's workspace holds.  The
+ * rates (KB/us) and times are fitted to 20 shapes x 18 partition counts; the
+ * choice was within 3 % of the best of them.
  */
+struct Rates {
+    double cta, sm, tile_us;
+    int streams;
+};
+
+Rates diff_rates(bool wide, bool two, bool f32, bool fp8) {
+    if (wide) {
+        if (f32) return two ? Rates{23e3, 23e3, 2.0, 2} : Rates{24e3, 24e3, 2.6, 4};
+        if (fp8) return two ? Rates{39e3, 39e3, 3.0, 4} : Rates{46.5e3, 46.5e3, 2.3, 8};
+        return two ? Rates{52e3, 52e3, 1.6, 3} : Rates{55e3, 55e3, 1.0, 5};
+    }
+    if (f32) return two ? Rates{32e3, 32e3, 2.0, 2} : Rates{20e3, 36e3, 1.0, 5};
+    if (fp8) return two ? Rates{13.5e3, 36e3, 2.5, 2} : Rates{19e3, 40e3, 1.0, 4};
+    return two ? Rates{30e3, 45e3, 1.8, 2} : Rates{38e3, 76e3, 1.0, 5};
+}
+
 struct Split {
     int parts;
     int part_len;
 };
 
 Split choose_split(const pa_decode_args* a, const Prepared& pr, int sms, int max_parts) {
-    const bool wide = pr.la.head_size > 128, two = pr.la.group_tiles == 2, f32 = a->dtype == PA_DTYPE_F32;
-    const bool fp8 = pr.kv != PA_KV_SAME;
-    double cta, sm;
-    if (wide) {
-        cta = sm = f32 ? 24e3 : fp8 ? (two ? 37e3 : 45e3) : (two ? 51e3 : 55e3);
-    } else {
-        cta = f32 ? (two ? 31e3 : 20e3) : fp8 ? 19e3 : (two ? 30e3 : 38e3);
-        sm = f32 ? (two ? 31e3 : 36e3) : fp8 ? (two ? 31e3 : 40e3) : 76e3;
-    }
+    const bool f32 = a->dtype == PA_DTYPE_F32, fp8 = pr.kv != PA_KV_SAME;
+    const Rates k = diff_rates(pr.la.head_size > 128, pr.la.group_tiles == 2, f32, fp8);
     const double memory = 6.8e6;
     const double token = 2.0 * pr.la.head_size * (fp8 ? 1 : (f32 ? 4 : 2));  // bytes of a token of one kv head
     const int64_t resident = (int64_t)sms * pr.ctas_per_sm, heads = (int64_t)a->num_seqs * a->num_kv_heads;
@@ -287,21 +299,20 @@ Split choose_split(const pa_decode_args* a, const Prepared& pr, int sms, int max
         const int64_t want = n == 0 ? 1 : (n == tries ? max_parts : n);
         const int64_t len = (pages + want - 1) / want * PA_BLOCK_SIZE, parts = (longest + len - 1) / len;
         const double tokens = (double)(len < longest ? len : longest);
+        const double turns = std::ceil(tokens / (PA_BLOCK_SIZE * k.streams)) * (PA_BLOCK_SIZE * k.streams);
+        auto tile_time = [&](double grid) {
+            const double share = k.sm / std::ceil(grid / sms);
+            const double consumed = turns * token / (share < k.cta ? share : k.cta), moved = tokens * token * grid / memory;
+            return consumed > moved ? consumed : moved;
+        };
         double t;
         if (equal) {
             const int64_t tiles = heads * parts, rounds = (tiles + resident - 1) / resident;
-            const int64_t grid = (tiles + rounds - 1) / rounds;
-            double rate = sm / (double)((grid + sms - 1) / sms);
-            if (cta < rate) rate = cta;
-            if (memory / (double)grid < rate) rate = memory / (double)grid;
-            t = (double)rounds * (tokens * token / rate + 1.0);
+            t = (double)rounds * (tile_time((double)((tiles + rounds - 1) / rounds)) + k.tile_us);
         } else {
             const double tiles = total * a->num_kv_heads / tokens + 0.5 * (double)heads;
             const double grid = tiles < (double)resident ? tiles : (double)resident;
-            double rate = sm / std::ceil(grid / sms);
-            if (cta < rate) rate = cta;
-            if (memory / grid < rate) rate = memory / grid;
-            t = total * a->num_kv_heads * token / (grid * rate) + (tiles < grid ? 1.0 : tiles / grid) + tokens * token / rate;
+            t = (tiles / grid + 1.0) * (tile_time(grid) + k.tile_us);
         }
         if (n > 0) t += 3.5;
         if (least < 0 || t < least) {

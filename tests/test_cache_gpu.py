@@ -1,6 +1,6 @@
 """GPU tests of pa_build_tables and pa_append_kv: every output against the plain
 statements of cache_ref.py, bit for bit (nothing here is rounded but fp8, whose
-quotient is one IEEE fp32 division, rounded by torch's own conversion)."""
+value is one fp32 product with 1 / scale, rounded by torch's own conversion)."""
 from __future__ import annotations
 
 import numpy as np
@@ -211,10 +211,10 @@ BITS = {1: torch.uint8, 2: torch.int16, 4: torch.int32}
 
 
 def _quantised(x, kv, scale):
-    """Element bits of a row: x itself, or fp8(x / scale), beyond the largest value that value."""
+    """Element bits of a row: x itself, or fp8(x * (1 / scale)), beyond the largest value that value."""
     if kv is None:
         return x.cpu().view(BITS[x.element_size()]).numpy()
-    q = x.cpu().float() / torch.tensor(scale, dtype=torch.float32)
+    q = x.cpu().float() * (torch.tensor(1.0) / torch.tensor(scale, dtype=torch.float32))
     top = torch.finfo(FP8[kv]).max
     return q.clamp(-top, top).to(FP8[kv]).view(torch.uint8).numpy()
 
@@ -227,11 +227,17 @@ def _slots(kind, tokens, blocks, rng):
             out += [int(ids[b + (o + i) // 16]) * 16 + (o + i) % 16 for i in range(n)]
             b += (o + n - 1) // 16 + 1
         out = np.array(out)
+    elif kind == "prompt":
+        out = np.zeros(tokens)
     elif kind == "backwards":  # successive slots, falling
         out = 16 * (blocks - 1) + 7 - np.arange(tokens)
     else:
         out = rng.permutation(blocks * 16)[:tokens]
     out = out.astype(np.int64)
+    if kind == "prompt":  # one run from an odd place, and padding
+        out = 16 * 3 + 11 + np.arange(tokens)
+        out[-2:] = -1
+        return out
     if tokens > 3:
         out[rng.random(tokens) < 0.1] = -1
         out[-1] = -2 ** 31
@@ -296,6 +302,15 @@ def test_append(dtype, kv, layout, tokens, kind):
 @pytest.mark.parametrize("hk,dk,hv,dv", [(1, 128, 1, 128), (2, 64, 1, 128), (6, 128, 3, 256), (4, 256, 5, 64)])
 def test_append_heads_and_sizes(dtype, kv, layout, hk, dk, hv, dv):
     _run(dtype, kv, layout, 83, hk, dk, hv, dv, "runs", strided=True, seed=hk + dv)
+
+
+@pytest.mark.parametrize("layout", ["split", "nhd"])
+@pytest.mark.parametrize("dtype,kv", TYPES)
+@pytest.mark.parametrize("kind,tokens,hk,hv,size", [("prompt", 3001, 2, 2, 128), ("runs", 2700, 1, 2, 64),
+                                                    ("random", 1500, 2, 2, 256), ("prompt", 2432, 1, 1, 256)])
+def test_append_many_rows(dtype, kv, layout, kind, tokens, hk, hv, size):
+    """Blocks of 32 rows and more, which begin with a page where they can."""
+    _run(dtype, kv, layout, tokens, hk, size, hv, size, kind, strided=True, seed=tokens)
 
 
 @pytest.mark.parametrize("layout", ["split", "nhd"])

@@ -102,6 +102,7 @@ def _append(**over):
     ({"kv_dtype": 1}, _abi.PA_ERR_INVALID_ARG),
     ({"kv_dtype": _abi.PA_KV_FP8_E4M3, "dtype": _abi.PA_DTYPE_F32}, _abi.PA_ERR_UNSUPPORTED),
     ({"k_scale": float("nan")}, _abi.PA_ERR_INVALID_ARG),
+    ({"v_scale": 1e-40}, _abi.PA_ERR_INVALID_ARG),
     ({"key": None}, _abi.PA_ERR_INVALID_ARG),
     ({"slots": None}, _abi.PA_ERR_INVALID_ARG),
     ({"value": 8}, _abi.PA_ERR_INVALID_ARG),

@@ -262,7 +262,7 @@ Rates diff_rates(bool wide, bool two, bool f32, bool fp8) {
         return two ? Rates{52e3, 52e3, 1.6, 3} : Rates{55e3, 55e3, 1.0, 5};
     }
     if (f32) return two ? Rates{32e3, 32e3, 2.0, 2} : Rates{20e3, 36e3, 1.0, 5};
-    if (fp8) return two ? Rates{13.5e3, 36e3, 2.5, 2} : Rates{19e3, 40e3, 1.0, 4};
+    if (fp8) return two ? Rates{25e3, 38e3, 2.8, 5} : Rates{19e3, 40e3, 1.0, 4};
     return two ? Rates{30e3, 45e3, 1.8, 2} : Rates{38e3, 76e3, 1.0, 5};
 }
 

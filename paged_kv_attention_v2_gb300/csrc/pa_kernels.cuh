@@ -51,6 +51,7 @@ constexpr int kStages16x2 = 10;    // 16-bit caches, two n-tiles (paired page st
 constexpr int kStagesFp8 = 12;     // fp8 caches (three CTAs per SM fit)
 constexpr int kStagesF32 = 5;      // fp32 caches, one n-tile (two CTAs per SM)
 constexpr int kStagesF32x2 = 8;    // fp32 caches, two n-tiles (one CTA per SM)
+constexpr int kStagesFp8x2Diff = 15; // fp8 caches, two n-tiles of a differential call (five warps)
 constexpr int kConsumerWarps = 4;  // consumer warps per CTA
 constexpr int kConsumerWarps5 = 5; // consumer warps per CTA, 16-bit or fp32 caches with one n-tile
 constexpr int kPrefetchPages = 16; // pages of the first tile prefetched into L2 before the grid wait
@@ -208,10 +209,12 @@ struct Cfg {
     // 34.2 -> 32.7 µs for the one-page stages.)
     static constexpr int kStageBytes = 2 * kPageBytes;  // K page, then V page
     static constexpr int kMaxG = NT * 8;                   // MMA columns: rows (heads x query tokens) handled
-    // 16-bit caches with two n-tiles, and every differential kernel with two:
-    // warps in pairs of page streams, one n-tile each; every page is consumed by
-    // two warps.
-    static constexpr bool kPairs = NT == 2 && (DIFF || (KV == kKvSame && !kF32));
+    // 16-bit caches with two n-tiles, and differential kernels with two but fp8
+    // ones of value heads of 128: warps in pairs of page streams, one n-tile each;
+    // every page is consumed by two warps.  (fp8: the pair would convert every
+    // value twice; one warp with both n-tiles, five warps and fifteen stages: 32 x
+    // 4096 e4m3 with four tokens 65 -> 57 us.)
+    static constexpr bool kPairs = NT == 2 && (DIFF ? (KV == kKvSame || HEAD > 128) : (KV == kKvSame && !kF32));
     static constexpr int kMergeRows = kPairs ? 8 : kMaxG;  // merge-buffer rows per warp
     static constexpr int kPageWarps = kPairs ? 2 : 1;      // warps that release each page
     static constexpr int kQBytes = kRows * HEAD * kElem;
@@ -976,7 +979,7 @@ __device__ __forceinline__ void settle_max(float (&m)[NT][2], float (&mx)[NT][2]
 // combination of both halves' last ones.
 template <class C, int KQ>
 __device__ __forceinline__ uint32_t last_query_word(const uint32_t (&q)[KQ][2]) {
-    if constexpr (C::kDiff && !C::kPairs)
+    if constexpr (C::kDiff && C::kMaxG == 8)
         return q[KQ / 2 - 1][1] | __shfl_xor_sync(0xffffffffu, q[KQ - 1][1], 16);
     else
         return q[KQ - 1][1];
@@ -1591,6 +1594,8 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                     fp8x4_to_f16<KV>(w[2 * u + 1], a1, a3);
 #pragma unroll
                     for (int nt = 0; nt < NTW; ++nt) {
+                        // (differential, two n-tiles: each meets its own map's keys only)
+                        if (C::kDiff && NTW == 2 && (kk + u) / (KT / 2) != nt) continue;
                         if (u)
                             mma_16816<false>(s2[nt], a0, a1, a2, a3, qb[nt][kk + u][0], qb[nt][kk + u][1]);
                         else
@@ -2045,15 +2050,11 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 // two n-tiles fills an SM's shared memory with one CTA (16 KB stages): no cap.
 // fp8 with one n-tile: capped for three CTAs per SM (128 registers: fifteen
 // warps put four on some SM sub-partition, whose register file is 16 K).
-// Value heads of 256 hold one CTA per SM.  Differential fp8 kernels with two
-// n-tiles hold one n-tile's registers per warp: three CTAs too (4 x 100000 e4m3,
-// groups of seven: 132 us with two, 102 with three, 118 with four, which spill).
+// Value heads of 256 hold one CTA per SM.
 template <typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV, bool MQ, bool DIFF>
 __global__ void __launch_bounds__((NC + 1) * 32,
                                   (HEAD > 128 || (std::is_same<T, float>::value && NT > 1))
                                       ? 1
-                                      : (DIFF && KV != kKvSame)
-                                      ? 3
                                       : ((NT > 1 || std::is_same<T, float>::value) ? 2 : (KV != kKvSame ? 3 : 1)))
     pa_partition_kernel(const Params p, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv) {

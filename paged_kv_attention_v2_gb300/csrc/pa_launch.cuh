@@ -45,13 +45,16 @@ constexpr int kMaxDevices = 64;
 template <typename T, int HEAD, int NT, int LAYOUT, int KV, bool MQ, bool DIFF = false>
 cudaError_t launch_main(const Params& p_in, const LaunchArgs& la, bool* fused) {
     constexpr bool F32 = std::is_same<T, float>::value, WIDE = HEAD > 128;
-    constexpr int STAGES = WIDE ? (F32               ? kStagesF32Wide
+    constexpr bool FP8X2 = DIFF && !WIDE && NT == 2 && KV != kKvSame;
+    constexpr int STAGES = FP8X2  ? kStagesFp8x2Diff
+                           : WIDE ? (F32               ? kStagesF32Wide
                                    : KV != kKvSame ? kStagesFp8Wide
                                    : NT == 1       ? kStages16Wide
                                                    : kStages16Widex2)
                            : F32 ? (NT == 1 ? kStagesF32 : kStagesF32x2)
                                  : (KV == kKvSame ? (NT == 1 ? kStages16 : kStages16x2) : kStagesFp8);
-    constexpr int NC = WIDE ? (F32               ? kConsumerWarpsF32Wide
+    constexpr int NC = FP8X2  ? kConsumerWarps5
+                       : WIDE ? (F32               ? kConsumerWarpsF32Wide
                                : KV != kKvSame ? kConsumerWarpsFp8Wide
                                : NT == 1       ? kConsumerWarps16Wide
                                                : kConsumerWarps16Widex2)

@@ -1070,6 +1070,10 @@ __device__ __forceinline__ void zero_v_tail8(uint32_t vpage, int valid, int lane
 template <class C, typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC>
 __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane) {
     constexpr bool BF = C::kBF16;
+    // P in two 16-bit terms: bf16 keeps 8 significant bits of it.  A differential
+    // output is a difference, normalised: fp16 takes two as well (one alone makes
+    // its error half as large again as the rounding of the output).
+    constexpr bool kTwoP = BF || C::kDiff;
     constexpr int KT = HEAD / 16;  // k-steps of Q.K^T, m-tiles of P.V
     // Two n-tiles: the warps work in pairs of page streams, one n-tile each
     // (rows nt0 * 8 .. nt0 * 8 + 7) on the pages j = pfirst (mod PSTRIDE), so
@@ -1266,9 +1270,9 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
                 const uint32_t x1 = pack2<BF>(p2, p3);  // token r+8
                 pb[nt][0] = movmatrix_trans(x0);         // -> B[k = token 2cq..][n = head r]
                 pb[nt][1] = movmatrix_trans(x1);
-                if constexpr (BF) {
-                    // bf16 keeps 8 significant bits; carry the rounding residue
-                    // of P in a second bf16 term so P.V keeps ~16 bits.
+                if constexpr (kTwoP) {
+                    // carry the rounding residue of P in a second term, so that
+                    // P.V keeps ~16 bits (bf16) or ~22 (fp16)
                     const float2 h0 = unpack2<BF>(x0), h1 = unpack2<BF>(x1);
                     pbl[nt][0] = movmatrix_trans(pack2<BF>(p0 - h0.x, p1 - h0.y));
                     pbl[nt][1] = movmatrix_trans(pack2<BF>(p2 - h1.x, p3 - h1.y));
@@ -1294,7 +1298,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
 #pragma unroll
                 for (int nt = 0; nt < NTW; ++nt) {
                     mma_16816<BF>(acc[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-                    if constexpr (BF) mma_16816<BF>(acc[mt][nt], a0, a1, a2, a3, pbl[nt][0], pbl[nt][1]);
+                    if constexpr (kTwoP) mma_16816<BF>(acc[mt][nt], a0, a1, a2, a3, pbl[nt][0], pbl[nt][1]);
                 }
             }
             if constexpr (!kEarlyV) {
@@ -1438,6 +1442,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 template <class C, typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV>
 __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int lane) {
     constexpr bool QBF = C::kBF16;
+    // differential with an fp16 output: P in two fp16 terms (see consumer_mma); a
+    // bf16 output rounds far more off than the one term does
+    constexpr bool kTwoP = C::kDiff && !QBF;
     constexpr int KT = HEAD / 16;
     // differential, two n-tiles: warps in pairs, one map each (see consumer_mma)
     constexpr bool kPairs = C::kPairs;
@@ -1617,7 +1624,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                 if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vw[KT / 2 - 1][3], p.zero);
             }
 
-            uint32_t pb[NTW][2];
+            uint32_t pb[NTW][2], pbl[NTW][2];
             float z[NTW][4];
 #pragma unroll
             for (int nt = 0; nt < NTW; ++nt) {
@@ -1639,8 +1646,14 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
             softmax_page<NTW, KT, C::kMQ>(z, m, mx, l, acc, edge);
 #pragma unroll
             for (int nt = 0; nt < NTW; ++nt) {
-                pb[nt][0] = movmatrix_trans(pack2<false>(z[nt][0], z[nt][1]));  // k-index 2cq.. = tokens tlo
-                pb[nt][1] = movmatrix_trans(pack2<false>(z[nt][2], z[nt][3]));
+                const uint32_t x0 = pack2<false>(z[nt][0], z[nt][1]), x1 = pack2<false>(z[nt][2], z[nt][3]);
+                pb[nt][0] = movmatrix_trans(x0);  // k-index 2cq.. = tokens tlo
+                pb[nt][1] = movmatrix_trans(x1);
+                if constexpr (kTwoP) {
+                    const float2 h0 = unpack2<false>(x0), h1 = unpack2<false>(x1);
+                    pbl[nt][0] = movmatrix_trans(pack2<false>(z[nt][0] - h0.x, z[nt][1] - h0.y));
+                    pbl[nt][1] = movmatrix_trans(pack2<false>(z[nt][2] - h1.x, z[nt][3] - h1.y));
+                }
             }
 
             // acc^T[head dim][head] += V^T . P^T.  Split value page [d][16
@@ -1680,8 +1693,10 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
                         fp8x4_to_f16<KV>(w[2 * u + 1], a1, a3);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NTW; ++nt)
+                    for (int nt = 0; nt < NTW; ++nt) {
                         mma_16816<false>(acc[mt + u][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                        if constexpr (kTwoP) mma_16816<false>(acc[mt + u][nt], a0, a1, a2, a3, pbl[nt][0], pbl[nt][1]);
+                    }
                 }
             }
             if constexpr (!kEarlyV) {

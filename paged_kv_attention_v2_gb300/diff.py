@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import torch
 
 from . import _abi
@@ -89,7 +90,6 @@ def _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambd
         lam = _floats("lambdas", lambdas, device, heads)
     host = None
     if seq_lens_host is not None:
-        import numpy as np
         host = np.ascontiguousarray(seq_lens_host.numpy() if isinstance(seq_lens_host, torch.Tensor) else seq_lens_host,
                                     dtype=np.int32)
         if host.shape != (n,):
@@ -132,7 +132,14 @@ def diff_plan(args: _abi.PaDiffArgs) -> dict:
             "partition_tokens": int(pl.partition_tokens)}
 
 
-def pa_diff_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *, lambdas, stream=None, **kw) -> None:
+def pa_diff_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *, lambdas, num_kv_heads: int,
+                   scale: float, max_seq_len: int, norm: bool = True, norm_weight=None, norm_eps: float = 1e-5,
+                   out_scale: float = 1.0, alibi_slopes=None, softcap: float = 0.0, layout: str = "split",
+                   mode: str = "auto", exp_sums=None, max_logits=None, tmp_out=None, dev_error=None,
+                   event_begin=None, event_end=None, partition_counters=None, window_left: int = -1,
+                   kv_dtype: str | None = None, k_scale: float = 1.0, v_scale: float = 1.0, query_start=None,
+                   max_query_len: int | None = None, seq_lens_host=None, tile_counters=None,
+                   metadata_ready: bool = False, stream=None) -> None:
     """Enqueue differential attention of the query rows over the paged cache.
 
     query [rows, num_heads, 2, head_size], out [rows, num_heads, 2 * head_size];
@@ -144,5 +151,9 @@ def pa_diff_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *
     with the workspace of alloc_diff_workspace.  At most 8 query tokens x heads
     per kv head.  Raises PaDecodeError with the library's status on failure.
     """
-    packed, _host = _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambdas, **kw)
+    packed, _host = _pack_diff(
+        out, query, key_cache, value_cache, block_tables, seq_lens, lambdas, num_kv_heads, scale, max_seq_len, norm,
+        norm_weight, norm_eps, out_scale, alibi_slopes, softcap, layout, mode, exp_sums, max_logits, tmp_out, dev_error,
+        event_begin, event_end, partition_counters, window_left, kv_dtype, k_scale, v_scale, query_start, max_query_len,
+        seq_lens_host, tile_counters, metadata_ready)
     _call("pa_diff_decode", packed, stream, query.get_device())

@@ -11,9 +11,10 @@ where
         of sum |q k| lost each; softcap, scale and ALiBi take a few roundings of their
         own results:  2^-23 ((d / 8 + 24) S_t + 4 cap + 4 |bias_t|), S_t = scale sum |q k|,
         and a bf16 query against fp8 keys goes through fp16 (2^-25 below its normal range)
-  u_p   is half a step of a softmax weight as the P.V operand: 2^-11 (fp16; and an
-        absolute 2^-25 where it is subnormal, against a sum of at least one), 2^-17
-        (bf16 in two terms), 2^-21 (fp32 in three tf32 terms)
+  u_p   is half a step of a softmax weight as the P.V operand: 2^-21 (fp16 in two
+        terms; and an absolute 2^-25 where it is subnormal, against a sum of at least
+        one), 2^-11 (a bf16 query over an fp8 cache: fp16 in one), 2^-17 (bf16 in two
+        terms), 2^-21 (fp32 in three tf32 terms)
   u_s   is the summation over n tokens, in pages of 16 and one merge per partition,
         with a step 2^-23 for each: 2^-23 (n / 16 + 64)
 and y = s w o / r, r = sqrt(mean o^2 + eps), by
@@ -26,7 +27,7 @@ import numpy as np
 import torch
 
 BS, PART = 16, 512
-U_P = {"f16": 2.0 ** -11, "bf16": 2.0 ** -17, "f32": 2.0 ** -21}
+U_P = {"f16": 2.0 ** -21, "bf16": 2.0 ** -17, "f32": 2.0 ** -21, "bf16 over fp8": 2.0 ** -11}
 HALF = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 TORCH = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 FP8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
@@ -62,7 +63,7 @@ def diff_ref(case, part=PART):
     lam = case["lambdas"].double().numpy()
     w = np.ones(2 * d) if case["norm_weight"] is None else case["norm_weight"].double().numpy()
     dtype, kv = case["dtype"], case["kv"]
-    pdt = "f16" if kv else dtype
+    pdt = "bf16 over fp8" if kv and dtype == "bf16" else dtype
     cap, scale = case["softcap"], float(np.float32(case["scale"]))
     for s, length in enumerate(case["lens"]):
         length = int(min(max(length, 0), case["max_seq_len"]))
@@ -103,7 +104,7 @@ def diff_ref(case, part=PART):
                     av = a @ np.abs(vv)
                     o.append(a @ vv)
                     e = (a * dz) @ np.abs(vv) + av * (a * dz).sum() + av * (U_P[pdt] + 2.0 ** -23 * (len(t) / 16 + 64))
-                    if pdt == "f16":
+                    if kv or dtype == "f16":
                         e = e + 2.0 ** -25 * np.abs(vv).sum(0)
                     err.append(e)
                 f = lam[r, h] if lam.ndim == 2 else lam[h]

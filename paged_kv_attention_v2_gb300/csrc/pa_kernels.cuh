@@ -63,7 +63,9 @@ constexpr int kPrefetchPages = 16; // pages of the first tile prefetched into L2
 constexpr int kStages16Wide = 10, kConsumerWarps16Wide = 5;
 constexpr int kStages16Widex2 = 9, kConsumerWarps16Widex2 = 6;
 constexpr int kStagesFp8Wide = 16, kConsumerWarpsFp8Wide = 8;  // fp8 caches: 8 KB stages
-constexpr int kStagesF32Wide = 4, kConsumerWarpsF32Wide = 4;   // fp32 caches: 32 KB stages
+constexpr int kStagesF32Wide = 5, kConsumerWarpsF32Wide = 5;   // fp32 caches: 32 KB stages
+constexpr int kStagesF32Widex2 = 3, kConsumerWarpsF32Widex2 = 6;
+constexpr int kStagesF32x2Diff = 8, kConsumerWarpsF32x2Diff = 8;  // fp32, value heads of 128, two n-tiles
 constexpr int kReduceWarpMaxParts = 64;  // warp-per-row reduce up to this many partitions per row
 
 constexpr int kDiffReduceFewParts = 4;  // differential rows: one warp per row up to this many partitions
@@ -217,6 +219,11 @@ struct Cfg {
     static constexpr bool kPairs = NT == 2 && (DIFF ? (KV == kKvSame || HEAD > 128) : (KV == kKvSame && !kF32));
     static constexpr int kMergeRows = kPairs ? 8 : kMaxG;  // merge-buffer rows per warp
     static constexpr int kPageWarps = kPairs ? 2 : 1;      // warps that release each page
+    // Differential fp32: K and V of a stage have barriers of their own.  A warp
+    // holds its stage through a page's whole work, and there are no more stages
+    // than warps: the key half is refilled while P.V runs, the value half during
+    // the next page's Q.K^T (32 x 4096, groups of four: 102 -> 86 us).
+    static constexpr bool kHalves = DIFF && kF32;
     static constexpr int kQBytes = kRows * HEAD * kElem;
     static constexpr int kTD = 2;                          // tile descriptor ring depth
     static constexpr int kMergeStride = HEAD + 4;          // floats; +4 breaks bank conflicts
@@ -232,7 +239,7 @@ struct Cfg {
     static constexpr int oML = oMerge + NC * kMergeRows * kMergeStride * 4;
     static constexpr int oDesc = oML + NC * kMergeRows * 8;
     static constexpr int oBar = (oDesc + kTD * (int)sizeof(TileDesc) + 7) & ~7;
-    static constexpr int oAbort = oBar + (2 * STAGES + 2 * kTD + 1) * 8;
+    static constexpr int oAbort = oBar + ((kHalves ? 4 : 2) * STAGES + 2 * kTD + 1) * 8;
     static constexpr int kSmemBytes = oAbort + 16 + 1024;  // + slack for 1024-B alignment
 
     static_assert(kPageBytes % 1024 == 0 || !kTensorMap, "swizzled pages need 1024-B alignment");
@@ -256,6 +263,7 @@ struct Smem {
     float2* ml;
     TileDesc* desc;
     uint32_t full, empty, td_full, td_empty;  // shared addresses of barrier arrays
+    uint32_t full_v, empty_v;  // of the value halves (Cfg::kHalves)
     uint32_t merge_bar;  // consumer warps: partial states written / epilogue reads done
     volatile int* abort;     // [0] give-up flag, [1] never set (drain waits), [2] last-arriver flag
     uint64_t wait_ns;        // limit of every barrier wait
@@ -530,7 +538,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
                     if (lok && !withhold) {
                         const uint32_t fb = sm.full + st * 8;
                         const uint32_t dk = sm.ring + st * C::kStageBytes, dv = dk + C::kPageBytes;
-                        mbar_arrive_expect_tx(fb, 2 * C::kPageBytes);
+                        mbar_arrive_expect_tx(fb, C::kHalves ? C::kPageBytes : 2 * C::kPageBytes);
                         const int64_t page = (int64_t)blk * Hkv + cur.kvh;
                         if constexpr (C::kTensorMap && C::kKvElem == 1) {
                             // fp8 NHD: one box of 16 token rows x HEAD bytes per page
@@ -553,14 +561,33 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
                                 tensor4d_g2s_hint(dk, tmk, 0, 0, 0, (int)(2 * page), fb, kvpol);
                             else
                                 tensor3d_g2s_hint(dk, tmk, 0, y, 0, fb, kvpol);
-                            tensor3d_g2s_hint(dv, tmv, 0, y, 0, fb, kvpol);
+                            if constexpr (!C::kHalves) tensor3d_g2s_hint(dv, tmv, 0, y, 0, fb, kvpol);
                         } else {
                             bulk_g2s_hint(dk, kbase + page * C::kPageBytes, C::kPageBytes, fb, kvpol);
-                            bulk_g2s_hint(dv, vbase + page * C::kPageBytes, C::kPageBytes, fb, kvpol);
+                            if constexpr (!C::kHalves)
+                                bulk_g2s_hint(dv, vbase + page * C::kPageBytes, C::kPageBytes, fb, kvpol);
                         }
                     }
                 }
                 ok = __all_sync(0xffffffffu, lok);
+                if constexpr (C::kHalves) {
+                    if (ok && lane < nb) {
+                        const uint32_t gg = g + (uint32_t)lane;
+                        const uint32_t st = gg % STAGES, ph = (gg / STAGES) & 1;
+                        lok = mbar_wait(sm.empty_v + st * 8, ph ^ 1, sm.abort, sm.wait_ns);
+                        if (lok) {
+                            const uint32_t fb = sm.full_v + st * 8;
+                            const uint32_t dv = sm.ring + st * C::kStageBytes + C::kPageBytes;
+                            const int64_t page = (int64_t)blk * Hkv + cur.kvh;
+                            mbar_arrive_expect_tx(fb, C::kPageBytes);
+                            if constexpr (C::kTensorMap)
+                                tensor3d_g2s_hint(dv, tmv, 0, (int)(page * kBS), 0, fb, kvpol);
+                            else
+                                bulk_g2s_hint(dv, vbase + page * C::kPageBytes, C::kPageBytes, fb, kvpol);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, lok);
+                }
                 g += (uint32_t)nb;
                 if (b0 == 0) {  // first batch out: load the next ids while the rest streams
                     if (pc + 32 < cur.npages) {
@@ -602,6 +629,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
         for (uint32_t st = 0; st < STAGES && st < g; ++st) {
             const uint32_t last = g - 1 - ((g - 1 - st) % STAGES);
             mbar_wait(sm.full + st * 8, (last / STAGES) & 1, sm.abort + 1, sm.wait_ns);
+            if constexpr (C::kHalves) mbar_wait(sm.full_v + st * 8, (last / STAGES) & 1, sm.abort + 1, sm.wait_ns);
         }
         // Dynamic schedule: the last CTA to be done with claiming (its arrival
         // releases its claims) sets both counters back to zero for the next call.
@@ -1883,11 +1911,14 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             const int tok0 = page0 + j * kBS;
             const int valid = min(kBS, d.tok_end - tok0);
             const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;
-            if (valid < kBS) {
-                zero_v_tail32<LAYOUT, HEAD>(vp, valid, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
+            auto zero_tail = [&]() {
+                if (valid < kBS) {
+                    zero_v_tail32<LAYOUT, HEAD>(vp, valid, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            };
+            if constexpr (!C::kHalves) zero_tail();
 
             // S^T[token][row] = K . Q^T; the four 8 x 4 blocks (tokens 0-7 /
             // 8-15, head dims 8kk..+3 / +4..+7) of a k-step are its A fragment,
@@ -1898,6 +1929,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             // sum across the k-steps of a page or, for P.V below, the pages of
             // a tile: without it a 24-head, group-12 fp32 case missed the 1e-5
             // tolerance even with the rounded split.
+            uint32_t klast = 0;  // the last word read of the key page
             float s[NTW][4], s2[NTW][4];
 #pragma unroll
             for (int nt = 0; nt < NTW; ++nt)
@@ -1913,6 +1945,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                         : kp + khalf + (uint32_t)((cg >> 3) * 2048 + (li + ((lj & 1) << 3)) * 128 +
                                           (((cg & 7) ^ li) << 4));
                 ldsm_x4(ka, a[0], a[1], a[2], a[3]);
+                klast = a[3];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
 #pragma unroll
@@ -1935,6 +1968,11 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sa[e] = __fadd_rn(sa[e], t[e]);
                 }
+            }
+
+            if constexpr (C::kHalves) {  // the key half goes back, the value half has to be there
+                __syncwarp();
+                if (lane == 0) mbar_arrive_after(sm.empty + st * 8, klast, p.zero);
             }
 
             // logits, online softmax, P^T as B fragments (hi and lo) per n-tile
@@ -1977,6 +2015,15 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                 }
             }
 
+            if constexpr (C::kHalves) {
+                if (!warp_wait(sm.full_v + st * 8, ph, sm.abort, sm.wait_ns)) {
+                    report(p, PA_DEVERR_TIMEOUT);
+                    *sm.abort = 1;
+                    return;
+                }
+                zero_tail();
+            }
+
             // acc^T[head dim][row] += V^T . P^T; A fragment of (m-tile mt,
             // k-step ks): head dims 16mt + r / + 8 by k-indices cq / cq + 4
             uint32_t vlast = 0;  // the page's last read
@@ -2017,7 +2064,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vlast, p.zero);
+            if (lane == 0) mbar_arrive_after((C::kHalves ? sm.empty_v : sm.empty) + st * 8, vlast, p.zero);
         }
 
         float* mw = sm.merge + warp * C::kMergeRows * C::kMergeStride;
@@ -2090,6 +2137,8 @@ __global__ void __launch_bounds__((NC + 1) * 32,
     sm.td_full = sm.empty + STAGES * 8;
     sm.td_empty = sm.td_full + C::kTD * 8;
     sm.merge_bar = sm.td_empty + C::kTD * 8;
+    sm.full_v = sm.merge_bar + 8;
+    sm.empty_v = sm.full_v + STAGES * 8;
     sm.abort = reinterpret_cast<volatile int*>(gen + C::oAbort);
     sm.wait_ns = p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs;
 
@@ -2099,6 +2148,10 @@ __global__ void __launch_bounds__((NC + 1) * 32,
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(sm.full + s * 8, 1);
             mbar_init(sm.empty + s * 8, C::kPageWarps);
+            if constexpr (C::kHalves) {
+                mbar_init(sm.full_v + s * 8, 1);
+                mbar_init(sm.empty_v + s * 8, C::kPageWarps);
+            }
         }
         for (int s = 0; s < C::kTD; ++s) {
             mbar_init(sm.td_full + s * 8, 1);

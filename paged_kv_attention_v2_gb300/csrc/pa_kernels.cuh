@@ -843,9 +843,8 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
 template <typename T, int HEAD, bool L2ONLY>
 __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int h, int len, int qn, int qi,
                                                int lane);
-template <int HEAD, bool L2ONLY, bool DIFF>
-__device__ __forceinline__ void merge_stats_row(const Params& p, int64_t srow, int h, int len, int qn, int qi,
-                                                int lane, float (&acc)[HEAD / 32]);
+template <typename T, int HEAD, bool L2ONLY>
+__device__ __forceinline__ void diff_merge_row(const Params& p, int64_t row, int h, int len, int qn, int qi, int lane);
 
 // The rows of one (sequence, kv head), one per consumer warp at a time.  Not
 // inlined: its loads then never share a register allocation with the page
@@ -857,13 +856,7 @@ __device__ __noinline__ void merge_group(const Params& p, int seq_kvh_base, int 
     for (int r = warp; r < qn * G; r += NC) {
         const int qi = MQ ? r / G : 0;
         if constexpr (DIFF) {
-            const int64_t row = (int64_t)q0 + qi;
-            const int h = seq_kvh_base + (r - qi * G);
-            float o[2][HEAD / 32];
-#pragma unroll
-            for (int map = 0; map < 2; ++map)
-                merge_stats_row<HEAD, true, true>(p, 2 * (row * p.num_heads + h) + map, h, len, qn, qi, lane, o[map]);
-            diff_row<T, HEAD>(p, row, h, o[0], o[1], lane);
+            diff_merge_row<T, HEAD, true>(p, (int64_t)q0 + qi, seq_kvh_base + (r - qi * G), len, qn, qi, lane);
         } else {
             merge_row_warp<T, HEAD, true>(p, (int64_t)q0 + qi, seq_kvh_base + (r - qi * G), len, qn, qi, lane);
         }
@@ -2484,44 +2477,29 @@ __global__ void __launch_bounds__(kReduceWarpsPerCta * 32) pa_reduce_warp_kernel
     merge_row_warp<T, HEAD, false>(p, (int64_t)q0 + qi, h, len, qn, qi, lane);
 }
 
-// Phase 2 of differential rows, up to kDiffReduceFewParts partitions: one warp per
-// (sequence, query token, head), both maps side by side: the first PRE partition
-// outputs of both are loaded with the statistics, so a row of up to PRE partitions
-// costs one round trip after its length.  (256 x 1000, 4096 rows: 82.5 us for
-// the whole call, with two warps per row 87; but with eight partitions 48.8
-// against 46, so pa_diff_reduce_pair_kernel takes those.)
-template <typename T, int HEAD, bool MQ>
-__global__ void __launch_bounds__(kReduceWarpsPerCta * 32, HEAD > 128 ? 2 : 4) pa_diff_reduce_warp_kernel(const Params p) {
+// Phase 2 of one differential (query row, head) by one warp, both maps side by side:
+// the first PRE partition outputs of both are loaded with the statistics, so a row
+// of up to PRE partitions costs one round trip; then lambda, norm and the output
+// row, and the row's statistics as merge_stats_row leaves them.  L2ONLY as there.
+template <typename T, int HEAD, bool L2ONLY>
+__device__ __forceinline__ void diff_merge_row(const Params& p, int64_t row, int h, int len, int qn, int qi, int lane) {
     constexpr int VEC = HEAD / 32, PRE = HEAD > 128 ? 2 : 4;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_launch_dependents();
-    pdl_wait_primary();
-
-    const int64_t rid = (int64_t)blockIdx.x * kReduceWarpsPerCta + warp;
-    const int64_t nrows = (int64_t)p.num_seqs * (MQ ? p.max_q_len : 1) * p.num_heads;
-    if (rid >= nrows) return;
-    const int sq = (int)(rid / p.num_heads), h = (int)(rid - (int64_t)sq * p.num_heads);
-    const int s = MQ ? sq / p.max_q_len : sq, qi = MQ ? sq - s * p.max_q_len : 0;
-    int q0 = s, qn = 1;
-    if constexpr (MQ) {
-        query_rows(p, s, q0, qn);
-        if (qi >= qn) return;
-    }
-    const int len = clamp_len(p, p.seq_lens[s]);
     const int hi = len - qn + qi;                       // the query token's position
     const int plen = part_len<true>(p);
     const int P = hi >= 0 ? (hi + plen) / plen : 0;     // partitions holding its keys
     const int p0 = window_lo_at(p, hi) / plen;          // partitions before p0: outside the window
-    const int64_t row = (int64_t)q0 + qi, sb = 2 * (row * p.num_heads + h) * p.max_parts;
+    const int64_t sb = 2 * (row * p.num_heads + h) * p.max_parts;
     const uint64_t pol = l2_policy_evict_first();       // partition outputs: last use
     auto load_out = [&](int map, int q, float (&t)[VEC]) {
         const float* at = p.tmp_out + (sb + (int64_t)map * p.max_parts + q) * HEAD + lane * 4;
 #pragma unroll
         for (int c = 0; c < VEC; c += 4) {
-            const float4 v = ld_global_v4_hint(at + c * 32, pol);
+            const float4 v = L2ONLY ? __ldcg(reinterpret_cast<const float4*>(at + c * 32))
+                                    : ld_global_v4_hint(at + c * 32, pol);
             t[c] = v.x; t[c + 1] = v.y; t[c + 2] = v.z; t[c + 3] = v.w;
         }
     };
+    auto ld_stat = [&](const float* a) { return L2ONLY ? __ldcg(a) : *a; };
     float* ml[2] = {p.max_logits + sb, p.max_logits + sb + p.max_parts};
     float* es[2] = {p.exp_sums + sb, p.exp_sums + sb + p.max_parts};
 
@@ -2541,15 +2519,15 @@ __global__ void __launch_bounds__(kReduceWarpsPerCta * 32, HEAD > 128 ? 2 : 4) p
     float m1[2], e1[2], M[2], invW[2];
 #pragma unroll
     for (int map = 0; map < 2; ++map) {
-        m1[map] = q1 < P ? ml[map][q1] : -INFINITY;
-        e1[map] = q1 < P ? es[map][q1] : 0.f;
+        m1[map] = q1 < P ? ld_stat(ml[map] + q1) : -INFINITY;
+        e1[map] = q1 < P ? ld_stat(es[map] + q1) : 0.f;
     }
 #pragma unroll
     for (int map = 0; map < 2; ++map) {
         // global max and weight sum over the row's partitions (lanes, then the warp)
         float m = m1[map], w = m == -INFINITY ? 0.f : e1[map];
         for (int q = q1 + 32; q < P; q += 32) {
-            const float mq = ml[map][q], eq = es[map][q];
+            const float mq = ld_stat(ml[map] + q), eq = ld_stat(es[map] + q);
             if (mq == -INFINITY) continue;
             if (mq > m) {
                 w = m == -INFINITY ? 0.f : w * expf(m - mq);
@@ -2585,8 +2563,8 @@ __global__ void __launch_bounds__(kReduceWarpsPerCta * 32, HEAD > 128 ? 2 : 4) p
                 const int q = qb + lane;
                 c = 0.f;
                 if (q < P) {
-                    const float mq = ml[map][q];
-                    c = mq == -INFINITY ? 0.f : expf(mq - M[map]) * es[map][q] * invW[map];
+                    const float mq = ld_stat(ml[map] + q);
+                    c = mq == -INFINITY ? 0.f : expf(mq - M[map]) * ld_stat(es[map] + q) * invW[map];
                 }
             }
             float t[PRE][VEC];
@@ -2621,6 +2599,29 @@ __global__ void __launch_bounds__(kReduceWarpsPerCta * 32, HEAD > 128 ? 2 : 4) p
             es[map][at] = 0.f;
         }
     }
+}
+
+// Phase 2 of differential rows, up to kDiffReduceFewParts partitions: one warp per
+// (sequence, query token, head).  (256 x 1000, 4096 rows: 82.5 us for the whole
+// call, with two warps per row 87; but with eight partitions 48.8 against 46, so
+// pa_diff_reduce_pair_kernel takes those.)
+template <typename T, int HEAD, bool MQ>
+__global__ void __launch_bounds__(kReduceWarpsPerCta * 32, HEAD > 128 ? 2 : 4) pa_diff_reduce_warp_kernel(const Params p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    const int64_t rid = (int64_t)blockIdx.x * kReduceWarpsPerCta + warp;
+    const int64_t nrows = (int64_t)p.num_seqs * (MQ ? p.max_q_len : 1) * p.num_heads;
+    if (rid >= nrows) return;
+    const int sq = (int)(rid / p.num_heads), h = (int)(rid - (int64_t)sq * p.num_heads);
+    const int s = MQ ? sq / p.max_q_len : sq, qi = MQ ? sq - s * p.max_q_len : 0;
+    int q0 = s, qn = 1;
+    if constexpr (MQ) {
+        query_rows(p, s, q0, qn);
+        if (qi >= qn) return;
+    }
+    diff_merge_row<T, HEAD, false>(p, (int64_t)q0 + qi, h, clamp_len(p, p.seq_lens[s]), qn, qi, lane);
 }
 
 // Phase 2 of differential rows, more partitions: two warps per (sequence, query

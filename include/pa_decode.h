@@ -373,6 +373,7 @@ pa_status pa_plan(const pa_decode_args* args, pa_launch_plan* plan);
  *                for the maps' partitions, which the library makes as long as suits
  *                the batch (pa_diff_plan tells); what it holds after the call is unspecified
  *   max_query_len * (num_heads / num_kv_heads) <= 8  (one tile holds both maps' rows)
+ *   max_seq_len  at most 2^30
  */
 typedef struct pa_diff_args {
     pa_decode_args decode;

@@ -16,7 +16,8 @@ _LAYOUT = {"split": _abi.PA_LAYOUT_SPLIT, "nhd": _abi.PA_LAYOUT_NHD}
 _KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP8_E5M2}
 _DTYPE = {torch.float32: _abi.PA_DTYPE_F32, torch.float16: _abi.PA_DTYPE_F16,
           torch.bfloat16: _abi.PA_DTYPE_BF16}
-_BYTES = {torch.float32: 4, torch.float16: 2, torch.bfloat16: 2}
+# cache element types of each kv_dtype (None: the rows' own)
+_CACHE = {"e4m3": (torch.uint8, torch.float8_e4m3fn), "e5m2": (torch.uint8, torch.float8_e5m2)}
 _TABLES = _abi.packer(_abi.PaTablesArgs)
 _APPEND = _abi.packer(_abi.PaAppendArgs)
 _PAGE = _abi.PA_BLOCK_SIZE
@@ -114,7 +115,7 @@ def _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_
         raise ValueError(f"{tokens} keys and {v_tokens} values")
     if value.dtype is not dtype or dtype not in _DTYPE:
         raise ValueError("key and value must both be float32, float16 or bfloat16")
-    kv_bytes = _BYTES[dtype] if kv_dtype is None else 1
+    types = (dtype,) if kv_dtype is None else _CACHE[kv_dtype]
     blocks = key_cache.shape[0]
     if value_cache.shape[0] != blocks:
         raise ValueError(f"{blocks} key pages and {value_cache.shape[0]} value pages")
@@ -126,9 +127,8 @@ def _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_
         raise ValueError("key and value must be on one device")
     for name, cache, page in (("key_cache", key_cache, k_heads * k_size * _PAGE),
                               ("value_cache", value_cache, v_heads * v_size * _PAGE)):
-        if cache.element_size() != kv_bytes:
-            raise ValueError(f"{name} has {cache.element_size()}-byte elements, kv_dtype "
-                             f"{kv_dtype or 'same as key'} needs {kv_bytes}")
+        if cache.dtype not in types:
+            raise ValueError(f"{name} is {cache.dtype}, kv_dtype {kv_dtype or 'same as key'} needs {types[0]}")
         if cache.numel() != blocks * page or not cache.is_contiguous() or cache.get_device() != device:
             raise ValueError(f"{name} must be contiguous, {blocks} pages of {page} elements, on the call's device")
     # the stride of a dimension of one is never used
@@ -158,8 +158,8 @@ def pa_append_kv(key, value, key_cache, value_cache, slots, *, layout: str = "sp
     head size] (fp32, fp16 or bf16; token and head strides may be anything that is
     a multiple of 16 bytes, as in a slice of a fused projection), slots [tokens]
     int32 from pa_build_tables (negative: skip), caches in the split or NHD
-    layout; kv_dtype "e4m3" / "e5m2" quantises to fp8 caches holding K / k_scale
-    and V / v_scale.
+    layout; kv_dtype "e4m3" / "e5m2" quantises to fp8 caches (torch's fp8 types or
+    raw uint8) holding K / k_scale and V / v_scale.
     """
     args = _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_scale, v_scale, dev_error)
     _call("pa_append_kv", args, stream, key.get_device())

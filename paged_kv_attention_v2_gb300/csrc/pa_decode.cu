@@ -361,6 +361,7 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
     if (df && (!std::isfinite(df->norm_eps) || !std::isfinite(df->out_scale) || (df->norm != 0 && df->norm_eps <= 0.f) ||
                df->lambda_row_stride < 0))
         return PA_ERR_INVALID_ARG;
+    if (df && a->max_seq_len > 1 << 30) return PA_ERR_UNSUPPORTED;  // length + partition in 32 bits
     if (a->num_seqs == 0) {
         pr.empty = true;
         return PA_OK;
@@ -531,7 +532,7 @@ pa_status plan_of(const pa_decode_args* a, const pa_diff_args* df, Prepared& pr,
 
 extern "C" {
 
-int32_t pa_version(void) { return (1 << 16) | 0; }
+int32_t pa_version(void) { return (1 << 16) | 1; }
 
 int32_t pa_max_num_partitions(int32_t max_seq_len) {
     if (max_seq_len <= 0) return 1;

@@ -12,7 +12,7 @@ import numpy as np
 import torch
 
 from . import _abi
-from .cache import _BYTES, _DTYPE, _KV, _LAYOUT, _PAGE, _call, _ints, _pointer
+from .cache import _CACHE, _DTYPE, _KV, _LAYOUT, _PAGE, _call, _ints, _pointer
 
 _DIFF = _abi.packer(_abi.PaDiffArgs)
 _MODE = {"auto": _abi.PA_MODE_AUTO, "v1": _abi.PA_MODE_V1, "v2": _abi.PA_MODE_V2}
@@ -68,12 +68,11 @@ def _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambd
     if block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
     blocks = key_cache.shape[0]
-    elem = _BYTES[dtype] if kv_dtype is None else 1
+    types = (dtype,) if kv_dtype is None else _CACHE[kv_dtype]
     numel = blocks * 2 * num_kv_heads * _PAGE * size
     for name, c in (("key_cache", key_cache), ("value_cache", value_cache)):
-        if c.element_size() != elem:
-            raise ValueError(f"{name} has {c.element_size()}-byte elements, kv_dtype "
-                             f"{kv_dtype or 'same as query'} needs {elem}")
+        if c.dtype not in types:
+            raise ValueError(f"{name} is {c.dtype}, kv_dtype {kv_dtype or 'same as query'} needs {types[0]}")
         if c.shape[0] != blocks or c.numel() != numel or not c.is_contiguous() or c.get_device() != device:
             raise ValueError(f"{name} must be contiguous on the call's device, {numel} elements in {blocks} pages "
                              f"(it holds {c.numel()} in {c.shape[0]})")

@@ -143,11 +143,16 @@ def test_binding_refuses_what_only_the_tensors_know():
     with pytest.raises(ValueError):
         pa.pa_append_kv(*good, layout="nhd")                                     # not on a GPU
     for at, bad in ((1, h(4, 2, 64)), (1, h(5, 2, 64).float()), (2, h(7, 2, 16, 128)), (3, h(6, 2, 16, 64)),
-                    (2, h(7, 2, 64, 16).transpose(2, 3)), (4, i(4)), (0, h(5, 64, 2).transpose(1, 2))):
+                    (2, h(7, 2, 64, 16).transpose(2, 3)), (3, h(7, 2, 16, 64).bfloat16()), (4, i(4)), (0, h(5, 64, 2).transpose(1, 2))):
         with pytest.raises(ValueError):
             cache.make_append_args(*good[:at], bad, *good[at + 1:], layout="nhd")
     with pytest.raises(ValueError):
         cache.make_append_args(*good, layout="nhd", kv_dtype="e4m3")             # 2-byte caches
+    fp8 = [torch.zeros((7, 2, 16, 64), dtype=t) for t in (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)]
+    for c in fp8[:2]:
+        cache.make_append_args(*good[:2], c, c, good[4], layout="nhd", kv_dtype="e4m3")
+    with pytest.raises(ValueError):
+        cache.make_append_args(*good[:2], fp8[2], fp8[2], good[4], layout="nhd", kv_dtype="e4m3")
     # one row: its strides are never used, whatever they are
     odd = torch.as_strided(h(200), (1, 1, 64), (3, 5, 1))
     a = cache.make_append_args(odd, odd, h(7, 1, 16, 64), h(7, 1, 16, 64), i(1), layout="nhd")

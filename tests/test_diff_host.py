@@ -69,6 +69,7 @@ def _args(**over):
     ({"out_scale": float("inf")}, _abi.PA_ERR_INVALID_ARG),
     ({"tmp_out": None}, _abi.PA_ERR_WORKSPACE),
     ({"query": None}, _abi.PA_ERR_INVALID_ARG),
+    ({"max_seq_len": (1 << 30) + 1, "max_blocks_per_seq": 1 << 27}, _abi.PA_ERR_UNSUPPORTED),
     ({"out": 8}, _abi.PA_ERR_INVALID_ARG),
     ({"kv_dtype": _abi.PA_KV_FP8_E4M3, "dtype": _abi.PA_DTYPE_F32}, _abi.PA_ERR_UNSUPPORTED),
     ({"query_start": 16, "num_query_tokens": 4, "max_query_len": 3}, _abi.PA_ERR_UNSUPPORTED),  # 4 heads x 3 > 8
@@ -100,7 +101,7 @@ def test_binding_refuses_what_only_the_tensors_know():
         pa.pa_diff_decode(*good.values(), **kw)                      # not on a GPU
     for bad in (dict(query=c["query"][:, :, 0]), dict(out=out[:, :, :64]), dict(out=out.float()),
                 dict(query=c["query"][:1], out=out[:1]), dict(key_cache=c["key_cache"][:, :2].contiguous()),
-                dict(value_cache=c["value_cache"][:-1]), dict(value_cache=c["value_cache"].float()),
+                dict(value_cache=c["value_cache"][:-1]), dict(value_cache=c["value_cache"].view(torch.bfloat16)), dict(value_cache=c["value_cache"].float()),
                 dict(key_cache=c["key_cache"].transpose(0, 1)), dict(block_tables=i32(c["table"]).long()),
                 dict(block_tables=i32(c["table"][:1]))):
         with pytest.raises(ValueError):

@@ -65,7 +65,7 @@ class Model:
         self.v_rows = [[] for _ in range(n)]
 
     def step(self):
-        """One step on the GPU: five calls (three here), nothing read back."""
+        """One step on the GPU: three calls, nothing read back."""
         pa.pa_build_tables(self.table, self.lens, self.ring, self.pool, self.slots, max_seq_len=self.max_len,
                            keep_lens=self.keep, query_start=self.start, positions=self.positions,
                            done_counter=self.counter, dev_error=self.err)

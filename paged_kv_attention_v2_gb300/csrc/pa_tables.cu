@@ -172,8 +172,11 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
 
     const bool one_chunk = S <= chunk;
     const int rows = !ok || S == 0 ? 0 : (one_chunk ? start[S] : (p.query_start ? p.query_start[S] : S));  // with a token
-    const int step = (int)(gridDim.x * blockDim.x) * kRowsPerThread;
-    const int first = (int)(blockIdx.x * blockDim.x + tid) * kRowsPerThread;
+    // this CTA's rows: successive ones, so that a thread's next four are mostly
+    // of the same sequence or the next
+    const int64_t share = ((int64_t)p.num_tokens / kRowsPerThread / gridDim.x + 1) * kRowsPerThread;
+    const int64_t first = blockIdx.x * share + tid * kRowsPerThread, end = (blockIdx.x + 1) * share;
+    const int step = (int)blockDim.x * kRowsPerThread;
 
     if (ok) {
         bool bad_id = false;
@@ -189,11 +192,12 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
             const int row0 = start[0];
             const int row1 = start[n];
             // rows [row0, row1): four successive rows per thread
-            auto page_id = [&](int j, int page, bool first_token) {
-                int32_t* entry = p.block_tables + (int64_t)(base + j) * p.max_blocks_per_seq + page;
+            int j = 0;  // the sequence of the row at hand, within the chunk
+            auto page_id = [&](int page, bool first_token) {
+                int32_t* entry = p.block_tables + (base + j) * p.max_blocks_per_seq + page;  // below 2^31 entries
                 if (page < own[j]) return *entry;
-                int64_t k = (int64_t)head + pop0[j] + (page - own[j]);
-                if (k >= N) k -= N;
+                uint32_t k = (uint32_t)head + (uint32_t)(pop0[j] + page - own[j]);  // both below 2^27
+                if (k >= (uint32_t)N) k -= N;
                 const int id = p.free_ring[k];
                 if (first_token) *entry = id;  // of a new page: always one of this call's
                 return id;
@@ -203,14 +207,17 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
                 bad_id = true;
                 return -1;
             };
-            for (int64_t q = first; q < row1; q += step) {
+            for (int64_t q = first; q < end && q < row1; q += step) {
                 if (q + kRowsPerThread <= row0) continue;
                 const int t = max((int)q, row0);
-                int j = p.query_start ? last_at_most(start, n, t) : t - base;
+                if (!p.query_start)
+                    j = t - base;
+                else if (start[j + 1] <= t)
+                    j += last_at_most(start + j, n - j, t);
                 if (p.vec && t == q && t + kRowsPerThread <= start[j + 1]) {  // four tokens of one sequence
                     const int pos = keep[j] + t - start[j], page = pos >> 4, off = pos & 15;
-                    const int id = page_id(j, page, off == 0);
-                    const int next = off > kBS - kRowsPerThread ? page_id(j, page + 1, true) : id;
+                    const int id = page_id(page, off == 0);
+                    const int next = off > kBS - kRowsPerThread ? page_id(page + 1, true) : id;
                     int slot[kRowsPerThread];
 #pragma unroll
                     for (int i = 0; i < kRowsPerThread; ++i)
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
                 for (int r = t; r < q + kRowsPerThread && r < row1; ++r) {
                     while (start[j + 1] <= r) ++j;  // ends: start[n] = row1
                     const int pos = keep[j] + r - start[j], off = pos & 15;
-                    p.slots[r] = slot_at(page_id(j, pos >> 4, off == 0), off);
+                    p.slots[r] = slot_at(page_id(pos >> 4, off == 0), off);
                     if (p.positions) p.positions[r] = pos;
                 }
             }
@@ -241,7 +248,8 @@ __global__ void __launch_bounds__(kMaxThreads) pa_tables_kernel(const TablesPara
         if (bad_id && p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
     }
     // padding
-    for (int64_t t = rows + (int64_t)blockIdx.x * blockDim.x + tid; t < p.num_tokens; t += step / kRowsPerThread) {
+    for (int64_t t = rows + (int64_t)blockIdx.x * blockDim.x + tid; t < p.num_tokens;
+         t += (int64_t)gridDim.x * blockDim.x) {
         p.slots[t] = -1;
         if (p.positions) p.positions[t] = 0;
     }

@@ -273,3 +273,33 @@ def test_identical_maps_cancel_and_lambda_zero_is_plain_attention():
     # both are within half a step of fp16 P (2^-11) and of the output of the same sums
     ref = diff_ref(c)
     assert np.all(np.abs((a.out - torch.cat(half, 2)).double().cpu().numpy()) <= 2 * ref[1])
+
+
+@pytest.mark.parametrize("n,longest,kv_heads,group,low,high", [
+    (128, 1200, 4, 2, 1, 4),       # a warp merges both maps
+    (24, 6000, 2, 4, 5, 32),       # two warps per row
+    (1, 30000, 2, 2, 33, 64),      # few rows of many partitions: a CTA per row
+    (3, 34000, 1, 5, 65, 100),
+])
+def test_every_merge(n, longest, kv_heads, group, low, high):
+    """Each kernel that merges partitions, by the number of them the plan shows."""
+    c = make_case(13, "bf16", None, 64, "nhd", kv_heads, group, np.full(n, longest), alibi=True)
+    call = Call(c, "v2")
+    tokens = call.plan()["partition_tokens"]
+    assert low <= -(-longest // tokens) <= high and tokens % 16 == 0, tokens
+    call.run().check(diff_ref(c))
+
+
+@pytest.mark.parametrize("dtype,kv,size,group", [("f32", None, 64, 4), ("f32", None, 64, 7), ("f32", None, 128, 2),
+                                                 ("f16", None, 64, 8), ("bf16", None, 128, 3), ("f16", "e4m3", 64, 8)])
+def test_calls_repeat_bit_for_bit(dtype, kv, size, group):
+    """Short sequences, whose page tails are zeroed, beside long ones: a stage handed
+    back before its last read has returned shows as calls that differ."""
+    lens = np.full(40, 97)
+    lens[0], lens[-1] = 17000, 16223
+    c = make_case(14, dtype, kv, size, "split", 4, group, lens)
+    call = Call(c, "v2", host_lens=False)
+    first, differ = call.run().out.clone(), torch.zeros((), device=DEV)
+    for _ in range(400):
+        differ += (call.run().out != first).any()
+    assert int(differ) == 0 and not torch.isnan(first).any()

@@ -258,7 +258,7 @@ struct Rates {
 Rates diff_rates(bool wide, bool two, bool f32, bool fp8) {
     if (wide) {
         if (f32) return two ? Rates{33e3, 33e3, 2.5, 3} : Rates{35e3, 35e3, 2.5, 5};
-        if (fp8) return two ? Rates{39e3, 39e3, 3.0, 4} : Rates{46.5e3, 46.5e3, 2.3, 8};
+        if (fp8) return two ? Rates{36e3, 36e3, 3.0, 4} : Rates{49e3, 49e3, 1.8, 6};
         return two ? Rates{52e3, 52e3, 1.6, 3} : Rates{55e3, 55e3, 1.0, 5};
     }
     if (f32) return two ? Rates{37e3, 37e3, 2.4, 4} : Rates{28.5e3, 52e3, 1.0, 5};

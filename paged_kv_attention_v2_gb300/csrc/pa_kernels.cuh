@@ -62,7 +62,9 @@ constexpr int kPrefetchPages = 16; // pages of the first tile prefetched into L2
 // sequences, keys of 128 bf16, 171 -> 150 us; 4 x 50000, groups of seven, 150 -> 143).
 constexpr int kStages16Wide = 10, kConsumerWarps16Wide = 5;
 constexpr int kStages16Widex2 = 9, kConsumerWarps16Widex2 = 6;
-constexpr int kStagesFp8Wide = 16, kConsumerWarpsFp8Wide = 8;  // fp8 caches: 8 KB stages
+// fp8 caches, 8 KB stages (one n-tile on eight warps, which spill: 32 x 4096 e4m3 92 us, on six 89)
+constexpr int kStagesFp8Wide = 18, kConsumerWarpsFp8Wide = 6;
+constexpr int kStagesFp8Widex2 = 16, kConsumerWarpsFp8Widex2 = 8;
 constexpr int kStagesF32Wide = 5, kConsumerWarpsF32Wide = 5;   // fp32 caches: 32 KB stages
 constexpr int kStagesF32Widex2 = 3, kConsumerWarpsF32Widex2 = 6;
 constexpr int kStagesF32x2Diff = 8, kConsumerWarpsF32x2Diff = 8;  // fp32, value heads of 128, two n-tiles

@@ -67,8 +67,8 @@ typedef struct pa_tables_args {
     int32_t* positions;         /* [num_tokens] or NULL */
     int32_t* new_seq_lens;      /* [num_seqs]; may be seq_lens itself */
     int32_t* new_pool_state;    /* [2]; may be pool_state itself */
-    int32_t num_seqs;
-    int32_t num_tokens;         /* rows of slots and positions; >= num_seqs without query_start */
+    int32_t num_seqs;           /* at most 2^30 */
+    int32_t num_tokens;         /* rows of slots and positions, at most 2^30; >= num_seqs without query_start */
     int32_t num_blocks;         /* pages of the cache, below 2^27 (slots are int32) */
     int32_t block_size;         /* must be PA_BLOCK_SIZE */
     int32_t max_seq_len;        /* upper bound of the lengths before and after */
@@ -106,7 +106,7 @@ typedef struct pa_append_args {
     void* value_cache;
     const int32_t* slots; /* [num_tokens] */
     int64_t key_stride, key_head_stride, value_stride, value_head_stride; /* elements */
-    int32_t num_tokens;
+    int32_t num_tokens;  /* at most 2^30 */
     int32_t num_key_heads, key_head_size;     /* head sizes: 64, 128 or 256 */
     int32_t num_value_heads, value_head_size;
     int32_t num_blocks;  /* pages in each cache, below 2^27 */

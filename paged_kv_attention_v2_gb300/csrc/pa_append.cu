@@ -377,6 +377,7 @@ extern "C" pa_status pa_append_kv(const pa_append_args* a, void* stream) {
     if (!std::isfinite(a->k_scale) || !std::isfinite(a->v_scale)) return PA_ERR_INVALID_ARG;
     if (a->kv_dtype != PA_KV_SAME && a->dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;
     if (a->block_size != PA_BLOCK_SIZE || a->num_blocks >= 1 << 27) return PA_ERR_UNSUPPORTED;
+    if (a->num_tokens > 1 << 30) return PA_ERR_UNSUPPORTED;  // rows rounded up to blocks in 32 bits
     if (!size_ok(a->key_head_size) || !size_ok(a->value_head_size)) return PA_ERR_UNSUPPORTED;
     if ((int64_t)a->num_key_heads + a->num_value_heads > 65535) return PA_ERR_UNSUPPORTED;
     if (a->num_tokens == 0) return PA_OK;

@@ -297,6 +297,8 @@ extern "C" pa_status pa_build_tables(const pa_tables_args* a, void* stream) {
         return PA_ERR_INVALID_ARG;
     if (a->block_size != PA_BLOCK_SIZE) return PA_ERR_UNSUPPORTED;
     if (a->num_blocks >= 1 << 27) return PA_ERR_UNSUPPORTED;
+    // rows and sequences counted past their end, by a thread's step, in 32 bits
+    if (a->num_tokens > 1 << 30 || a->num_seqs > 1 << 30) return PA_ERR_UNSUPPORTED;
     if ((int64_t)a->num_seqs * a->max_blocks_per_seq >= (int64_t)1 << 31) return PA_ERR_UNSUPPORTED;
     if ((int64_t)a->max_blocks_per_seq * PA_BLOCK_SIZE < (int64_t)a->max_seq_len) return PA_ERR_INVALID_ARG;
     if (!a->query_start && a->num_tokens < a->num_seqs) return PA_ERR_INVALID_ARG;

@@ -62,6 +62,9 @@ def _tables(**over):
     ({"max_blocks_per_seq": 6}, _abi.PA_ERR_INVALID_ARG),
     ({"max_seq_len": -1}, _abi.PA_ERR_INVALID_ARG),
     ({"num_seqs": 1 << 20, "num_tokens": 1 << 20, "max_blocks_per_seq": 1 << 11}, _abi.PA_ERR_UNSUPPORTED),
+    ({"num_tokens": (1 << 30) + 1}, _abi.PA_ERR_UNSUPPORTED),   # counted in 32 bits
+    ({"num_seqs": (1 << 30) + 1, "num_tokens": 1 << 30, "query_start": 16, "max_seq_len": 0, "max_blocks_per_seq": 1},
+     _abi.PA_ERR_UNSUPPORTED),
     ({"block_tables": None}, _abi.PA_ERR_INVALID_ARG),
     ({"seq_lens": None}, _abi.PA_ERR_INVALID_ARG),
     ({"free_ring": None}, _abi.PA_ERR_INVALID_ARG),
@@ -109,6 +112,7 @@ def _append(**over):
     ({"key_cache": 8}, _abi.PA_ERR_INVALID_ARG),
     ({"key_stride": 257}, _abi.PA_ERR_INVALID_ARG),
     ({"value_head_stride": 4}, _abi.PA_ERR_INVALID_ARG),
+    ({"num_tokens": (1 << 30) + 1}, _abi.PA_ERR_UNSUPPORTED),
     ({"num_tokens": 0, "key": None}, _abi.PA_OK),
 ])
 def test_append_refusals(lib, over, expect):

@@ -374,6 +374,8 @@ pa_status pa_plan(const pa_decode_args* args, pa_launch_plan* plan);
  *                the batch (pa_diff_plan tells); what it holds after the call is unspecified
  *   max_query_len * (num_heads / num_kv_heads) <= 8  (one tile holds both maps' rows)
  *   max_seq_len  at most 2^30
+ *   num_query_tokens may pass query_start[num_seqs] (a padded batch): the rows of
+ *                out behind the last token stay as they were; 0 is a no-op
  */
 typedef struct pa_diff_args {
     pa_decode_args decode;

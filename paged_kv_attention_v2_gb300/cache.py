@@ -43,19 +43,20 @@ def _call(name: str, args: bytes, stream, device: int) -> None:
         raise PaDecodeError(st, name)
 
 
-def _pointer(name: str, t, dtype, device: int, numel: int = -1) -> int:
-    """Address of a contiguous tensor of `dtype` on `device` (None: 0), of `numel` elements if given."""
+def _pointer(name: str, t, dtype, device: int, numel: int = -1, room: bool = False) -> int:
+    """Address of a contiguous tensor of `dtype` on `device` (None: 0), of `numel`
+    elements if given (with `room` at least as many)."""
     if t is None:
         return 0
     if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on the call's device")
-    if numel >= 0 and t.numel() != numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, expected {numel}")
+    if numel >= 0 and t.numel() != numel and not (room and t.numel() > numel):
+        raise ValueError(f"{name} holds {t.numel()} elements, expected {'at least ' if room else ''}{numel}")
     return t.data_ptr()
 
 
-def _ints(name: str, t, device: int, numel: int = -1) -> int:
-    return _pointer(name, t, torch.int32, device, numel)
+def _ints(name: str, t, device: int, numel: int = -1, room: bool = False) -> int:
+    return _pointer(name, t, torch.int32, device, numel, room)
 
 
 def _pack_tables(block_tables, seq_lens, free_ring, pool_state, slots, max_seq_len, keep_lens, query_start,

@@ -362,7 +362,7 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
                df->lambda_row_stride < 0))
         return PA_ERR_INVALID_ARG;
     if (df && a->max_seq_len > 1 << 30) return PA_ERR_UNSUPPORTED;  // length + partition in 32 bits
-    if (a->num_seqs == 0) {
+    if (a->num_seqs == 0 || (df && multi && a->num_query_tokens == 0)) {
         pr.empty = true;
         return PA_OK;
     }

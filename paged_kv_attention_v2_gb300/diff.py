@@ -37,8 +37,8 @@ def alloc_diff_workspace(rows: int, num_heads: int, head_size: int, max_seq_len:
     return ws
 
 
-def _floats(name: str, t, device: int, numel: int = -1) -> int:
-    return _pointer(name, t, torch.float32, device, numel)
+def _floats(name: str, t, device: int, numel: int = -1, room: bool = False) -> int:
+    return _pointer(name, t, torch.float32, device, numel, room)
 
 
 def _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambdas, num_kv_heads, scale, max_seq_len,
@@ -98,10 +98,10 @@ def _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambd
         value_cache.data_ptr(), _ints("block_tables", block_tables, device), _ints("seq_lens", seq_lens, device, n),
         n, heads, num_kv_heads, size, blocks, _PAGE, max_seq_len, block_tables.shape[1], scale, softcap,
         _floats("alibi_slopes", alibi_slopes, device, heads), _DTYPE[dtype], _LAYOUT[layout], _MODE[mode],
-        _floats("exp_sums", exp_sums, device, stats), _floats("max_logits", max_logits, device, stats),
-        _floats("tmp_out", tmp_out, device, stats * 2 * size), _ints("dev_error", dev_error, device, 1),
+        _floats("exp_sums", exp_sums, device, stats, True), _floats("max_logits", max_logits, device, stats, True),
+        _floats("tmp_out", tmp_out, device, stats * 2 * size, True), _ints("dev_error", dev_error, device, 1),
         0 if event_begin is None else event_begin.cuda_event, 0 if event_end is None else event_end.cuda_event,
-        _ints("partition_counters", partition_counters, device, n * num_kv_heads),
+        _ints("partition_counters", partition_counters, device, n * num_kv_heads, True),
         window_left + 1 if window_left >= 0 else 0, _KV[kv_dtype], k_scale, v_scale,
         _ints("query_start", query_start, device, n + 1), tokens, most,
         0 if host is None else host.__array_interface__["data"][0], _ints("tile_counters", tile_counters, device, 2),
@@ -147,7 +147,8 @@ def pa_diff_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *
     2 * head_size, in the split or NHD layout; lambdas fp32 [num_heads], or [rows,
     num_heads] for a lambda per token; norm, norm_weight [2 * head_size] fp32,
     norm_eps and out_scale of the heads' RMS norm.  Everything else as pa_decode,
-    with the workspace of alloc_diff_workspace.  At most 8 query tokens x heads
+    with the workspace of alloc_diff_workspace (that of a larger batch or a greater
+    length will do).  Rows behind query_start[num_seqs] are left as they were.  At most 8 query tokens x heads
     per kv head.  Raises PaDecodeError with the library's status on failure.
     """
     packed, _host = _pack_diff(

@@ -158,6 +158,44 @@ def test_masked_rows_of_a_padded_batch_stay(mode):
     assert (big[3:] == 7).all()
 
 
+@pytest.mark.parametrize("mode", ["v1", "v2", "v2f", "auto"])
+@pytest.mark.parametrize("q_len", [[2, 1, 0], [0, 0, 0]])
+def test_rows_behind_the_last_token_of_the_call_stay(mode, q_len):
+    """A call padded to eight rows, in the workspace of a larger batch still."""
+    c = make_case(5, "bf16", "e4m3", 64, "nhd", 2, 2, (30, 1600, 0), q_len=[2, 1, 0], per_row=True)
+    call = Call(c, mode)
+    wide = lambda t, v: torch.cat([t, torch.full((8 - t.shape[0],) + tuple(t.shape[1:]), v, dtype=t.dtype, device=DEV)])  # noqa: E731
+    nan = float("nan")
+    call.tensors[0] = out = wide(call.tensors[0], 7.0)
+    call.tensors[1] = wide(call.tensors[1], nan)
+    call.kw["lambdas"] = wide(call.kw["lambdas"], nan)
+    call.kw["query_start"] = _int(np.concatenate([[0], np.cumsum(q_len)]))
+    room = pa.alloc_diff_workspace(11, 4, 64, 5000, DEV, num_seqs=9 if mode == "v2f" else None, num_kv_heads=3)
+    call.kw.update(room)
+    call.ws.update(room)
+    rows = sum(q_len)
+    if rows == 0:
+        out.fill_(7.0)
+    for _ in range(2):
+        call.run()
+    torch.cuda.synchronize()
+    assert (out[rows:] == 7).all()
+    if rows:
+        call.out = out[:rows]
+        call.check(diff_ref(c))
+    assert int(call.err) == 0
+
+
+def test_no_rows_of_several_sequences():
+    c = make_case(6, "f16", None, 64, "split", 2, 2, (30, 600), q_len=[1, 1])
+    call = Call(c, "v2")
+    call.tensors[0], call.tensors[1] = call.tensors[0][:0].clone(), call.tensors[1][:0].clone()
+    call.kw["query_start"] = _int([0, 0, 0])
+    call.run()
+    torch.cuda.synchronize()
+    assert int(call.err) == 0
+
+
 @pytest.mark.parametrize("mode", ["v1", "v2", "v2f"])
 def test_bad_metadata_is_reported_and_harmless(mode):
     c = make_case(3, "f16", None, 64, "nhd", 2, 3, (100, 600, 40))

@@ -75,6 +75,7 @@ def _args(**over):
     ({"query_start": 16, "num_query_tokens": 4, "max_query_len": 3}, _abi.PA_ERR_UNSUPPORTED),  # 4 heads x 3 > 8
     ({"query_start": 16, "num_query_tokens": 4, "max_query_len": 0}, _abi.PA_ERR_INVALID_ARG),
     ({"num_seqs": 0}, _abi.PA_OK),
+    ({"query_start": 16, "num_query_tokens": 0, "max_query_len": 1, "query": None, "out": None}, _abi.PA_OK),
 ])
 def test_refusals(lib, over, expect):
     assert lib.pa_diff_decode(ctypes.byref(_args(**over)), None) == expect
@@ -157,3 +158,19 @@ def test_packed_arguments_are_the_struct(cls):
     data = pack.pack(*range(1, len(fields) + 1))
     for i, (at, t) in enumerate(fields):
         assert t.from_buffer_copy(data, at).value == i + 1
+
+
+def test_binding_takes_the_workspace_of_a_larger_batch():
+    c = make_case(1, "f16", None, 64, "split", 2, 2, (20, 40))
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32))  # noqa: E731
+    args = (torch.empty((2, 4, 128), dtype=torch.float16), c["query"], c["key_cache"], c["value_cache"], i32(c["table"]),
+            i32(c["lens"]))
+    kw = dict(lambdas=c["lambdas"], num_kv_heads=2, scale=0.1, max_seq_len=40)
+    room = dict(exp_sums=torch.empty(5, 4, 2, 3), max_logits=torch.empty(5, 4, 2, 3), tmp_out=torch.empty(5, 4, 2, 3, 128),
+                partition_counters=torch.zeros((5, 2), dtype=torch.int32))
+    make_diff_args(*args, **kw, **room)
+    for name, t in room.items():  # one element less than this call needs
+        need = {"exp_sums": 16, "max_logits": 16, "tmp_out": 16 * 128, "partition_counters": 4}[name]
+        make_diff_args(*args, **kw, **{name: t.flatten()[:need]})
+        with pytest.raises(ValueError):
+            make_diff_args(*args, **kw, **{name: t.flatten()[:need - 1]})

@@ -257,11 +257,11 @@ struct Rates {
 
 Rates diff_rates(bool wide, bool two, bool f32, bool fp8) {
     if (wide) {
-        if (f32) return two ? Rates{33e3, 33e3, 2.5, 3} : Rates{35e3, 35e3, 2.5, 5};
+        if (f32) return two ? Rates{34.5e3, 34.5e3, 2.5, 3} : Rates{58e3, 58e3, 2.0, 5};
         if (fp8) return two ? Rates{36e3, 36e3, 3.0, 4} : Rates{49e3, 49e3, 1.8, 6};
         return two ? Rates{52e3, 52e3, 1.6, 3} : Rates{55e3, 55e3, 1.0, 5};
     }
-    if (f32) return two ? Rates{37e3, 37e3, 2.4, 4} : Rates{28.5e3, 52e3, 1.0, 5};
+    if (f32) return two ? Rates{35e3, 35e3, 2.4, 4} : Rates{33.5e3, 62e3, 1.0, 5};
     if (fp8) return two ? Rates{25e3, 38e3, 2.8, 5} : Rates{19e3, 40e3, 1.0, 4};
     return two ? Rates{30e3, 45e3, 1.8, 2} : Rates{38e3, 76e3, 1.0, 5};
 }

@@ -226,7 +226,8 @@ struct Cfg {
     // Differential fp32: K and V of a stage have barriers of their own.  A warp
     // holds its stage through a page's whole work, and there are no more stages
     // than warps: the key half is refilled while P.V runs, the value half during
-    // the next page's Q.K^T (32 x 4096, groups of four: 102 -> 86 us).
+    // the next page's Q.K^T (32 x 4096, groups of four, with the products still in
+    // tf32: 102 -> 86 us).
     static constexpr bool kHalves = DIFF && kF32;
     static constexpr int kQBytes = kRows * HEAD * kElem;
     static constexpr int kTD = 2;                          // tile descriptor ring depth
@@ -1795,15 +1796,8 @@ template <class C, int HEAD, int NT, int LAYOUT, int STAGES, int NC>
 __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lane) {
     constexpr int KT = HEAD / 8;   // k-steps of Q.K^T (8 head dims each)
     constexpr int MT = HEAD / 16;  // m-tiles of P.V (16 head dims each)
-    // differential, two n-tiles: warps in pairs, one map each (see consumer_mma)
-    constexpr bool kPairs = C::kPairs;
-    constexpr int NTW = kPairs ? 1 : NT;
-    constexpr int PSTRIDE = kPairs ? NC / 2 : NC;
-    constexpr int KQ = kPairs ? KT / 2 : KT;
-    const int nt0 = kPairs ? warp / PSTRIDE : 0;
-    const int pfirst = kPairs ? warp % PSTRIDE : warp;
-    const uint32_t khalf = kPairs ? (uint32_t)nt0 * (C::kPageBytes / 2) : 0u;
-    constexpr bool QSPLIT = NTW == 1 && KQ <= 16;  // Q held split for the whole tile
+    static_assert(!C::kDiff && !C::kPairs, "differential heads: consumer_fma");
+    constexpr bool QSPLIT = NT == 1;  // Q held split for the whole tile
     const int G = p.group;
     const int r = lane >> 2, cq = lane & 3;
     const bool has_alibi = p.alibi != nullptr;
@@ -1824,39 +1818,37 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 
         // Q as B fragments (k = head dim 8kk + cq / + 4, n = row nt * 8 + r):
         // hi and lo terms (one n-tile) or the raw words (two)
-        uint32_t qa[NTW][KQ][2];
-        uint32_t qlo[QSPLIT ? KQ : 1][2];
+        uint32_t qa[NT][KT][2];
+        uint32_t qlo[QSPLIT ? KT : 1][2];
         {
             const float* q = reinterpret_cast<const float*>(
                 __cvta_shared_to_generic(sm.q + slot * C::kQBytes));
 #pragma unroll
-            for (int nt = 0; nt < NTW; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int kk = 0; kk < KQ; ++kk)
+                for (int kk = 0; kk < KT; ++kk)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int v = (nt0 + nt) * 8 + r, row = C::row_of(v);
-                        const int k0 = kPairs ? nt0 * (HEAD / 2) + kk * 8 : kk * 8;
-                        const bool mine = row < GE && (!C::kDiff || kPairs || kk / (KT / 2) == v / C::kRows);
-                        const uint32_t x = mine ? __float_as_uint(q[row * HEAD + k0 + cq + 4 * e]) : 0u;
+                        const int v = nt * 8 + r;
+                        const uint32_t x = v < GE ? __float_as_uint(q[v * HEAD + kk * 8 + cq + 4 * e]) : 0u;
                         if constexpr (QSPLIT)
                             split_tf32(x, qa[nt][kk][e], qlo[kk][e]);
                         else
                             qa[nt][kk][e] = x;
                     }
         }
-        const uint32_t qlast = last_query_word<C, KQ>(qa[NTW - 1]);
+        const uint32_t qlast = last_query_word<C, KT>(qa[NT - 1]);
         __syncwarp();
         // Q and descriptor are in registers (lane 0 takes part in the last read)
         if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);
 
-        float sl[NTW][2];
-        int klo[NTW][2], khi[NTW][2];  // key range of this lane's rows within the tile
+        float sl[NT][2];
+        int klo[NT][2], khi[NT][2];  // key range of this lane's rows within the tile
 #pragma unroll
-        for (int nt = 0; nt < NTW; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int v = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
+                const int v = nt * 8 + 2 * cq + e;
                 sl[nt][e] = (has_alibi && v < GE) ? __ldg(p.alibi + d.kvh * G + v % G) : 0.f;
                 int lo = d.tok_begin, hi = d.tok_end - 1;
                 if (C::kMQ && v < GE) {
@@ -1871,10 +1863,10 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
         const int lo_all = C::kMQ ? max(d.tok_begin, window_lo_at(p, d.len - 1)) : d.tok_begin;
         const int origin = d.tok_end - 1;
 
-        float m[NTW][2], l[NTW][2], mx[NTW][2];  // reference max, sum, this lane's running max
-        float acc[MT][NTW][4];
+        float m[NT][2], l[NT][2], mx[NT][2];  // reference max, sum, this lane's running max
+        float acc[MT][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NTW; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = mx[nt][0] = mx[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
@@ -1892,9 +1884,9 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
         const int src0 = 4 * tk0 + (r >> 1), src1 = 4 * tk1 + (r >> 1);
         // stage and phase of page j: advanced per page with one n-tile, computed
         // per page with two (whose registers are all taken)
-        uint32_t st = (gbase + (uint32_t)pfirst) % STAGES, ph = ((gbase + (uint32_t)pfirst) / STAGES) & 1;
-        for (int j = pfirst; j < npages; j += PSTRIDE, advance_stage<STAGES, PSTRIDE>(st, ph)) {
-            if constexpr (NTW > 1) {
+        uint32_t st = (gbase + (uint32_t)warp) % STAGES, ph = ((gbase + (uint32_t)warp) / STAGES) & 1;
+        for (int j = warp; j < npages; j += NC, advance_stage<STAGES, NC>(st, ph)) {
+            if constexpr (NT > 1) {
                 st = (gbase + (uint32_t)j) % STAGES;
                 ph = ((gbase + (uint32_t)j) / STAGES) & 1;
             }
@@ -1908,14 +1900,11 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             const int tok0 = page0 + j * kBS;
             const int valid = min(kBS, d.tok_end - tok0);
             const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;
-            auto zero_tail = [&]() {
-                if (valid < kBS) {
-                    zero_v_tail32<LAYOUT, HEAD>(vp, valid, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-            };
-            if constexpr (!C::kHalves) zero_tail();
+            if (valid < kBS) {
+                zero_v_tail32<LAYOUT, HEAD>(vp, valid, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
 
             // S^T[token][row] = K . Q^T; the four 8 x 4 blocks (tokens 0-7 /
             // 8-15, head dims 8kk..+3 / +4..+7) of a k-step are its A fragment,
@@ -1926,27 +1915,25 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             // sum across the k-steps of a page or, for P.V below, the pages of
             // a tile: without it a 24-head, group-12 fp32 case missed the 1e-5
             // tolerance even with the rounded split.
-            uint32_t klast = 0;  // the last word read of the key page
-            float s[NTW][4], s2[NTW][4];
+            float s[NT][4], s2[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NTW; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < KQ; ++kk) {
+            for (int kk = 0; kk < KT; ++kk) {
                 uint32_t a[4], ah[4], al[4];
                 const int cg = 2 * kk + (lj >> 1);  // 16-byte chunk of the head dims
                 const uint32_t ka =
                     LAYOUT == kSplit
-                        ? kp + khalf + (uint32_t)((cg * kBS + li + ((lj & 1) << 3)) * 16)
-                        : kp + khalf + (uint32_t)((cg >> 3) * 2048 + (li + ((lj & 1) << 3)) * 128 +
+                        ? kp + (uint32_t)((cg * kBS + li + ((lj & 1) << 3)) * 16)
+                        : kp + (uint32_t)((cg >> 3) * 2048 + (li + ((lj & 1) << 3)) * 128 +
                                           (((cg & 7) ^ li) << 4));
                 ldsm_x4(ka, a[0], a[1], a[2], a[3]);
-                klast = a[3];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
 #pragma unroll
-                for (int nt = 0; nt < NTW; ++nt) {
+                for (int nt = 0; nt < NT; ++nt) {
                     uint32_t bh[2], bl[2];
                     if constexpr (QSPLIT) {
                         bh[0] = qa[nt][kk][0];
@@ -1967,16 +1954,11 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                 }
             }
 
-            if constexpr (C::kHalves) {  // the key half goes back, the value half has to be there
-                __syncwarp();
-                if (lane == 0) mbar_arrive_after(sm.empty + st * 8, klast, p.zero);
-            }
-
             // logits, online softmax, P^T as B fragments (hi and lo) per n-tile
-            uint32_t pbh[NTW][2][2], pbl[NTW][2][2];
-            float z[NTW][4];
+            uint32_t pbh[NT][2][2], pbl[NT][2][2];
+            float z[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NTW; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float v = (s[nt][e] + s2[nt][e]) * p.scale;
@@ -1992,9 +1974,9 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                     if (t1 < klo[nt][1] || t1 > khi[nt][1]) z[nt][3] = -INFINITY;
                 }
             }
-            softmax_page<NTW, MT, C::kMQ>(z, m, mx, l, acc, edge);
+            softmax_page<NT, MT, C::kMQ>(z, m, mx, l, acc, edge);
 #pragma unroll
-            for (int nt = 0; nt < NTW; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
                 // z[nt]: p of (token r, row 2cq), (token r, row 2cq + 1),
                 // (token r + 8, row 2cq), (token r + 8, row 2cq + 1)
                 const float* pv = z[nt];
@@ -2010,15 +1992,6 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                     split_tf32(__float_as_uint((r & 1) ? o0 : e0), pbh[nt][ks][0], pbl[nt][ks][0]);
                     split_tf32(__float_as_uint((r & 1) ? o1 : e1), pbh[nt][ks][1], pbl[nt][ks][1]);
                 }
-            }
-
-            if constexpr (C::kHalves) {
-                if (!warp_wait(sm.full_v + st * 8, ph, sm.abort, sm.wait_ns)) {
-                    report(p, PA_DEVERR_TIMEOUT);
-                    *sm.abort = 1;
-                    return;
-                }
-                zero_tail();
             }
 
             // acc^T[head dim][row] += V^T . P^T; A fragment of (m-tile mt,
@@ -2050,7 +2023,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 #pragma unroll
                     for (int e = 0; e < 4; ++e) split_tf32(a[e], ah[e], al[e]);
 #pragma unroll
-                    for (int nt = 0; nt < NTW; ++nt) {
+                    for (int nt = 0; nt < NT; ++nt) {
                         float t[4] = {0.f, 0.f, 0.f, 0.f};
                         mma_1688_tf32(t, al[0], al[1], al[2], al[3], pbh[nt][ks][0], pbh[nt][ks][1]);
                         mma_1688_tf32(t, ah[0], ah[1], ah[2], ah[3], pbl[nt][ks][0], pbl[nt][ks][1]);
@@ -2061,13 +2034,13 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_after((C::kHalves ? sm.empty_v : sm.empty) + st * 8, vlast, p.zero);
+            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vlast, p.zero);
         }
 
         float* mw = sm.merge + warp * C::kMergeRows * C::kMergeStride;
-        settle_max<NTW, MT>(m, mx, l, acc);
+        settle_max<NT, MT>(m, mx, l, acc);
 #pragma unroll
-        for (int nt = 0; nt < NTW; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], o);
@@ -2085,6 +2058,307 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             if (r == 0) {
                 sm.ml[warp * C::kMergeRows + h0] = make_float2(m[nt][0], l[nt][0]);
                 sm.ml[warp * C::kMergeRows + h0 + 1] = make_float2(m[nt][1], l[nt][1]);
+            }
+        }
+        if (!consumer_sync(sm, mphase, lane)) {
+            report(p, PA_DEVERR_TIMEOUT);
+            *sm.abort = 1;
+            return;
+        }
+        if (!tile_finish<C, float, HEAD, NC>(p, d, sm, warp, lane, mphase)) {
+            report(p, PA_DEVERR_TIMEOUT);
+            *sm.abort = 1;
+            return;
+        }
+        gbase += (uint32_t)npages;
+    }
+}
+
+// fp32 differential heads, on the fp32 units.  A tile has at most eight columns
+// per warp, so a page is 16 x (HEAD / 2) x 8 + 16 x HEAD x 8 multiply-adds: 768
+// instructions of a warp at value heads of 128.  (As three tf32 products each it
+// is 96 m16n8k8 MMAs of some fifty cycles.  GPU time with those and so: 32 x 4096,
+// groups of four, 87 and 81.4 us, of eight 116 and 119; heads of 256 247 and 162,
+// of eight, 16 sequences, 135 and 131; two short sequences 17.4 and 15.0.  And
+// every product is rounded once.)  What bounds it is what shared memory returns
+// to registers, 128 bytes a cycle: per page of a warp 128 + 192 cycles, so packed
+// fp32 pairs, which need P or V twice, cost more than they save (86.7).  Column
+// v = 4 hb + i of a lane's half hb is map hb of row i (one n-tile), or row v of
+// the warp's map (a pair of warps).
+//
+// Q.K^T: lane (tg, dq, hb) sums four tokens by its half's four columns over a
+// quarter dq of the map's head dims, one 16-byte chunk in four; its j-th token is
+// tg + 4 (j ^ dq), so that eight successive lanes read eight distinct chunks of
+// 128 bytes in both layouts, and two exchanges (dq bit 0, then bit 1) leave each
+// lane the sum of token tg + 4 dq.  Q stays in shared memory for the whole tile.
+//
+// P.V: a lane owns HEAD / 32 head dims of all eight columns; P goes through the
+// warp's part of the merge buffer, which is free until the end of the tile.  NHD
+// pages: four successive dims per 16-byte read, token by token.  Split pages
+// ([d][16 tokens], 64-byte rows): every 32nd dim, and a lane begins with token
+// quad (lane / 2) % 4, so that eight lanes read 128 distinct bytes.  A page's sum
+// is added to the tile's once.
+template <class C, int HEAD, int LAYOUT, int STAGES, int NC>
+__device__ void consumer_fma(const Params& p, const Smem& sm, int warp, int lane) {
+    constexpr int IT = HEAD / 32;  // 16-byte key chunks of a lane
+    constexpr int DV = HEAD / 32;  // head dims of a lane in P.V
+    // Loops of value heads of 256 unrolled half as far: the whole page's work in one
+    // piece misses the instruction cache (split, groups of four, 176 us; 167 so;
+    // heads of 128 the other way round, 81.4 and 82.1)
+    constexpr int kUC = HEAD > 128 ? 2 : 4, kUT = HEAD > 128 ? 8 : 16, kUN = HEAD > 128 ? 2 : 4;
+    constexpr bool kPairs = C::kPairs;
+    constexpr int PSTRIDE = kPairs ? NC / 2 : NC;
+    const int pfirst = kPairs ? warp % PSTRIDE : warp;
+    const int tg = lane & 3, dq = (lane >> 2) & 3, hb = lane >> 4;
+    const int map = kPairs ? warp / PSTRIDE : hb, row0 = kPairs ? hb * 4 : 0;
+    const int tt = tg + 4 * dq;  // this lane's token of a page, after the exchanges
+    const int G = p.group;
+    const bool has_alibi = p.alibi != nullptr;
+    const bool has_cap = p.softcap > 0.f;
+    // byte offsets in the key page of the lane's first chunk, token j
+    uint32_t koff[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int t = tg + 4 * (j ^ dq), cg = map * (HEAD / 8) + dq;
+        koff[j] = LAYOUT == kSplit ? (uint32_t)((cg * kBS + t) * 16)
+                                   : (uint32_t)((cg >> 3) * 2048 + t * 128 + ((dq ^ (t & 7)) << 4));
+    }
+    float* mw = sm.merge + warp * C::kMergeRows * C::kMergeStride;
+    const uint32_t ps = smem_u32(mw);  // P of the page at hand
+    uint32_t gbase = 0;
+    uint32_t mphase = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k % C::kTD;
+        if (!warp_wait(sm.td_full + slot * 8, (k / C::kTD) & 1, sm.abort, sm.wait_ns)) {
+            report(p, PA_DEVERR_TIMEOUT);
+            *sm.abort = 1;
+            return;
+        }
+        const TileDesc d = sm.desc[slot];
+        if (d.flags & kTileStop) return;
+        const int qn = C::kMQ ? d.qn : 1;
+        const int GE = qn * G;  // query rows: token v / G, head kvh * G + v % G
+        const uint32_t qs = sm.q + slot * C::kQBytes + (uint32_t)((row0 * HEAD + map * (HEAD / 2) + dq * 4) * 4);
+
+        float sl[4];
+        int klo[4], khi[4];  // key range of this lane's columns within the tile
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = row0 + i;
+            sl[i] = (has_alibi && v < GE) ? __ldg(p.alibi + d.kvh * G + v % G) : 0.f;
+            int lo = d.tok_begin, hi = d.tok_end - 1;
+            if (C::kMQ && v < GE) {
+                const int pos = d.len - qn + v / G;
+                hi = min(hi, pos);
+                lo = max(lo, window_lo_at(p, pos));
+            }
+            klo[i] = lo;
+            khi[i] = hi;
+        }
+        const int hi_all = C::kMQ ? min(d.tok_end - 1, d.len - qn) : d.tok_end - 1;
+        const int lo_all = C::kMQ ? max(d.tok_begin, window_lo_at(p, d.len - 1)) : d.tok_begin;
+        const int origin = d.tok_end - 1;
+
+        float m[4], l[4], mx[4];  // reference max, this lane's sum and running max
+        float acc[DV][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = mx[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < DV; ++x)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) acc[x][v] = 0.f;
+        // moves the references to the warp's running max, with l and acc
+        auto move_max = [&]() {
+            float al[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float mn = mx[i];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                // equal: also a column without a key so far (-inf)
+                al[i] = mn == m[i] ? 1.f : exp2f((m[i] - mn) * kLog2e);
+                m[i] = mn;
+                l[i] *= al[i];
+            }
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const float a = __shfl_sync(0xffffffffu, al[v & 3], (v >> 2) << 4);
+#pragma unroll
+                for (int x = 0; x < DV; ++x) acc[x][v] *= a;
+            }
+        };
+
+        const int npages = tile_pages(d.tok_begin, d.tok_end);
+        const int page0 = d.tok_begin / kBS * kBS;
+        uint32_t qlast = 0;  // the last word read of the query rows
+        uint32_t st = (gbase + (uint32_t)pfirst) % STAGES, ph = ((gbase + (uint32_t)pfirst) / STAGES) & 1;
+        for (int j = pfirst; j < npages; j += PSTRIDE, advance_stage<STAGES, PSTRIDE>(st, ph)) {
+            if (!warp_wait(sm.full + st * 8, ph, sm.abort, sm.wait_ns)) {
+                report(p, PA_DEVERR_TIMEOUT);
+                *sm.abort = 1;
+                return;
+            }
+            const uint32_t kp = sm.ring + st * C::kStageBytes;
+            const uint32_t vp = kp + C::kPageBytes;
+            const int tok0 = page0 + j * kBS;
+            const int valid = min(kBS, d.tok_end - tok0);
+            const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;
+
+            float s[4][4];  // [token j][column i]
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[t][i] = 0.f;
+            uint32_t klast = 0;
+#pragma unroll kUC
+            for (int c = 0; c < IT; ++c) {
+                float4 q[4], x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = lds_v4(qs + (uint32_t)(i * HEAD * 4 + c * 64));
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    x[t] = lds_v4(kp + (LAYOUT == kSplit ? koff[t] + c * (4 * kBS * 16)
+                                                         : (koff[t] ^ ((c & 1) << 6)) + (c >> 1) * 2048));
+                qlast = __float_as_uint(q[3].w);
+                klast = __float_as_uint(x[3].w);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[t][i] = fmaf(q[i].x, x[t].x, s[t][i]);
+                        s[t][i] = fmaf(q[i].y, x[t].y, s[t][i]);
+                        s[t][i] = fmaf(q[i].z, x[t].z, s[t][i]);
+                        s[t][i] = fmaf(q[i].w, x[t].w, s[t][i]);
+                    }
+            }
+            __syncwarp();  // the key half goes back
+            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, klast, p.zero);
+
+            // the quarters' sums: lane dq keeps the even j, whose tokens are the
+            // odd j's of lane dq ^ 1; then j = 0 against lane dq ^ 2
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[0][i] += __shfl_xor_sync(0xffffffffu, s[1][i], 4);
+                s[2][i] += __shfl_xor_sync(0xffffffffu, s[3][i], 4);
+                s[0][i] += __shfl_xor_sync(0xffffffffu, s[2][i], 8);
+            }
+
+            // logits and online softmax (see softmax_page)
+            float z[4];
+            bool need = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = s[0][i] * p.scale;
+                if (has_cap) v = soft_cap<false>(p, v);
+                if (has_alibi) v += sl[i] * (float)(tok0 + tt - origin);
+                if (row0 + i >= GE || (edge && (tok0 + tt < klo[i] || tok0 + tt > khi[i]))) v = -INFINITY;
+                z[i] = v;
+                mx[i] = fmaxf(mx[i], v);
+                need |= v - m[i] > kLazyMax;
+            }
+            if (__any_sync(0xffffffffu, need)) move_max();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // a column without a key so far: 0 as reference, so that no -inf - -inf appears
+                z[i] = exp2f((z[i] - (m[i] == -INFINITY ? 0.f : m[i])) * kLog2e);
+                l[i] += z[i];
+            }
+            if constexpr (LAYOUT == kSplit) {  // [column][token], the halves 16 banks apart
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sts_f32(ps + (uint32_t)((hb * 80 + i * 16 + tt) * 4), z[i]);
+            } else {  // [token][column]
+                sts_v4(ps + (uint32_t)((tt * 8 + hb * 4) * 4), make_float4(z[0], z[1], z[2], z[3]));
+            }
+            __syncwarp();
+
+            if (!warp_wait(sm.full_v + st * 8, ph, sm.abort, sm.wait_ns)) {
+                report(p, PA_DEVERR_TIMEOUT);
+                *sm.abort = 1;
+                return;
+            }
+            if (valid < kBS) {
+                zero_v_tail32<LAYOUT, HEAD>(vp, valid, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+
+            uint32_t vlast = 0;  // the page's last read
+            float o[DV][8];      // the page's sum
+#pragma unroll
+            for (int x = 0; x < DV; ++x)
+#pragma unroll
+                for (int v = 0; v < 8; ++v) o[x][v] = 0.f;
+            if constexpr (LAYOUT == kSplit) {
+#pragma unroll kUN
+                for (int n = 0; n < 4; ++n) {
+                    const int quad = (n + (lane >> 1)) & 3;
+                    float4 x[DV];
+#pragma unroll
+                    for (int i = 0; i < DV; ++i) x[i] = lds_v4(vp + (uint32_t)((lane + 32 * i) * 64 + quad * 16));
+                    vlast = __float_as_uint(x[DV - 1].w);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        const float4 w = lds_v4(ps + (uint32_t)(((v >> 2) * 80 + (v & 3) * 16 + quad * 4) * 4));
+#pragma unroll
+                        for (int i = 0; i < DV; ++i) {
+                            o[i][v] = fmaf(w.x, x[i].x, o[i][v]);
+                            o[i][v] = fmaf(w.y, x[i].y, o[i][v]);
+                            o[i][v] = fmaf(w.z, x[i].z, o[i][v]);
+                            o[i][v] = fmaf(w.w, x[i].w, o[i][v]);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll kUT
+                for (int t = 0; t < kBS; ++t) {
+                    const float4 a = lds_v4(ps + (uint32_t)(t * 32)), b = lds_v4(ps + (uint32_t)(t * 32 + 16));
+                    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int i = 0; i < DV; i += 4) {
+                        const float4 x = lds_v4(vp + (uint32_t)((i + (lane >> 3)) * 2048 + t * 128 +
+                                                                (((lane ^ t) & 7) << 4)));
+                        vlast = __float_as_uint(x.w);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            o[i][v] = fmaf(w[v], x.x, o[i][v]);
+                            o[i + 1][v] = fmaf(w[v], x.y, o[i + 1][v]);
+                            o[i + 2][v] = fmaf(w[v], x.z, o[i + 2][v]);
+                            o[i + 3][v] = fmaf(w[v], x.w, o[i + 3][v]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < DV; ++x)
+#pragma unroll
+                for (int v = 0; v < 8; ++v) acc[x][v] += o[x][v];
+            __syncwarp();  // also: P has been read
+            if (lane == 0) mbar_arrive_after(sm.empty_v + st * 8, vlast, p.zero);
+        }
+        __syncwarp();
+        // descriptor and query rows have been read
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);
+
+        move_max();  // the exact statistics
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+            if ((lane & 15) == 0) sm.ml[warp * C::kMergeRows + hb * 4 + i] = make_float2(m[i], l[i]);
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            if constexpr (LAYOUT == kSplit) {
+#pragma unroll
+                for (int i = 0; i < DV; ++i) mw[v * C::kMergeStride + lane + 32 * i] = acc[i][v];
+            } else {
+#pragma unroll
+                for (int i = 0; i < DV; i += 4)
+                    *reinterpret_cast<float4*>(mw + v * C::kMergeStride + (i * 32 + lane * 4)) =
+                        make_float4(acc[i][v], acc[i + 1][v], acc[i + 2][v], acc[i + 3][v]);
             }
         }
         if (!consumer_sync(sm, mphase, lane)) {
@@ -2176,6 +2450,8 @@ __global__ void __launch_bounds__((NC + 1) * 32,
 
     if (warp == NC) {
         producer<C, HEAD, STAGES>(p, sm, &tmk, &tmv, lane);
+    } else if constexpr (C::kF32 && DIFF) {
+        consumer_fma<C, HEAD, LAYOUT, STAGES, NC>(p, sm, warp, lane);
     } else if constexpr (C::kF32) {
         consumer_tf32<C, HEAD, NT, LAYOUT, STAGES, NC>(p, sm, warp, lane);
     } else {

@@ -341,3 +341,15 @@ def test_calls_repeat_bit_for_bit(dtype, kv, size, group):
     for _ in range(400):
         differ += (call.run().out != first).any()
     assert int(differ) == 0 and not torch.isnan(first).any()
+
+
+@pytest.mark.parametrize("layout", ["split", "nhd"])
+@pytest.mark.parametrize("size,group", [(64, 3), (64, 8), (128, 1), (128, 7)])
+def test_identical_maps_cancel_in_fp32(layout, size, group):
+    """Both maps take the same sums in the same order, whichever lanes or warps hold them."""
+    c = make_case(14, "f32", None, size, layout, 2, group, (1600, 33, 0, 250), norm=False, softcap=20.0, alibi=True)
+    c["query"][:, :, 1] = c["query"][:, :, 0]
+    c["key_cache"][:, 1::2] = c["key_cache"][:, 0::2]
+    c["lambdas"].fill_(1.0)
+    for mode in ("v1", "v2", "v2f"):
+        assert (Call(c, mode).run().out == 0).all()

@@ -1096,9 +1096,13 @@ __device__ __forceinline__ void zero_v_tail8(uint32_t vpage, int valid, int lane
 template <class C, typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC>
 __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane) {
     constexpr bool BF = C::kBF16;
-    // P in two 16-bit terms: bf16 keeps 8 significant bits of it.  A differential
-    // output is a difference, normalised: fp16 takes two as well (one alone makes
-    // its error half as large again as the rounding of the output).
+    // P in two 16-bit terms: bf16 keeps 8 significant bits of it, two terms 17.  A
+    // differential output is a difference, normalised, and what one map's weights lose
+    // grows as the maps cancel: fp16 takes two as well, 22 bits of a weight of a 2^-10th
+    // or more of the reference and an absolute 2^-25 below (fp16's subnormal step).
+    // Maps that cancel to a fiftieth, against the output's own rounding: fp16 2.06e-4
+    // (2.06e-4), bf16 1.66e-3 (1.65e-3); a third bf16 term changes neither that nor
+    // 4 x 100000, where what is left is the fp32 sums'.
     constexpr bool kTwoP = BF || C::kDiff;
     constexpr int KT = HEAD / 16;  // k-steps of Q.K^T, m-tiles of P.V
     // Two n-tiles: the warps work in pairs of page streams, one n-tile each
@@ -1297,8 +1301,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
                 pb[nt][0] = movmatrix_trans(x0);         // -> B[k = token 2cq..][n = head r]
                 pb[nt][1] = movmatrix_trans(x1);
                 if constexpr (kTwoP) {
-                    // carry the rounding residue of P in a second term, so that
-                    // P.V keeps ~16 bits (bf16) or ~22 (fp16)
+                    // the rounding residue of P as a second term
                     const float2 h0 = unpack2<BF>(x0), h1 = unpack2<BF>(x1);
                     pbl[nt][0] = movmatrix_trans(pack2<BF>(p0 - h0.x, p1 - h0.y));
                     pbl[nt][1] = movmatrix_trans(pack2<BF>(p2 - h1.x, p3 - h1.y));
@@ -1468,9 +1471,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 template <class C, typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV>
 __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int lane) {
     constexpr bool QBF = C::kBF16;
-    // differential with an fp16 output: P in two fp16 terms (see consumer_mma); a
-    // bf16 output rounds far more off than the one term does
-    constexpr bool kTwoP = C::kDiff && !QBF;
+    // differential: P in two fp16 terms, whatever the output (see consumer_mma).  With
+    // one, maps that nearly cancel pass a bf16 output's own rounding (1.65e-3 of the
+    // norm): lambda 0.95 5.4e-3, lambda 1 1.4e-2; with two 1.66e-3.  The second term
+    // costs 32 x 4096 e4m3 with four tokens 57.3 -> 62.9 us, 4 x 100000 e4m3, groups of
+    // seven, 76.4 -> 83.5, and up to four rows nothing (28.5).
+    constexpr bool kTwoP = C::kDiff;
     constexpr int KT = HEAD / 16;
     // differential, two n-tiles: warps in pairs, one map each (see consumer_mma)
     constexpr bool kPairs = C::kPairs;

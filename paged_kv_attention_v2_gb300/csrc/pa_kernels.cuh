@@ -135,16 +135,28 @@ __device__ __forceinline__ int part_len(const Params& p) {
 // cap * tanh(v / cap).  With QUICK (the differential kernels of 16-bit queries,
 // whose consumers are short of issue slots with both maps' logits: e4m3 with four
 // tokens 93 -> 88 us) as tanh(x) = 1 - 2 / (exp(2x) + 1) with the hardware's
-// exponential and reciprocal: a few steps of 1 in absolute terms, so that the
-// logit is off by some 2^-22 cap, far below the output's rounding; infinities
-// included.  An fp32 output would show it (1.6e-6 against 5e-7).
+// exponential and reciprocal; infinities included.  That is a few steps of 1 off,
+// so the logit by some 2^-22 cap, whatever its size: 1.5e-5 at kQuickCap, well below
+// what 16-bit keys and queries round to, but 0.1 at a cap of 1e6.  Above kQuickCap
+// logits under a quarter of the cap take tanh's series instead (x^11 of it is below
+// 2^-26 of x), larger ones are 2^-20 of themselves off.  (Same call, each way: no
+// series 67.0 us, so 69.5, the series at any cap 72.6, and tanhf above kQuickCap 69.9
+// but 2 to 5 % on calls without a cap, whose code it makes longer.)  An fp32 output
+// would show the quick form (1.6e-6 against 5e-7).
+constexpr float kQuickCap = 64.f;
 template <bool QUICK>
 __device__ __forceinline__ float soft_cap(const Params& p, float v) {
+    const float x = v * p.inv_softcap;
     if constexpr (QUICK) {
-        const float e = exp2f(v * p.inv_softcap * (2.f * kLog2e));
-        return p.softcap - __fdividef(2.f * p.softcap, e + 1.f);
+        float z = p.softcap - __fdividef(2.f * p.softcap, exp2f(x * (2.f * kLog2e)) + 1.f);
+        if (p.softcap > kQuickCap) {
+            const float x2 = x * x;
+            const float y = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835, -17.f / 315), 2.f / 15), -1.f / 3), 1.f);
+            if (fabsf(x) < 0.25f) z = p.softcap * (x * y);
+        }
+        return z;
     }
-    return p.softcap * tanhf(v * p.inv_softcap);
+    return p.softcap * tanhf(x);
 }
 
 // First key inside the sliding window of a query at position pos (0 without one).

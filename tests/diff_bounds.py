@@ -11,9 +11,11 @@ reference that the weights are taken against and u = 2^-24 (half a step of fp32)
             fp16: |q - fp16(q)| |k| more.  fp32 keys: a chain of d / 4 fused
             multiply-adds, two exchange additions, the scale and one more rounding:
             u (d / 4 + 4) S_t.
-  softcap   tanhf path: the reciprocal of the cap, its product, tanhf (two steps) and the
-            product with the cap:  8 u |z|.  Quick form (16-bit queries, caps up to
-            QUICK_CAP): 4 2^-23 cap.
+  softcap   tanhf path (fp32): the reciprocal of the cap, its product, tanhf (two steps)
+            and the product with the cap:  8 u |z|.  Quick form (16-bit queries): four
+            steps of 1 times the cap, 4 2^-23 cap; above QUICK_CAP that only from a
+            quarter of the cap on (where |z| >= 0.24 cap: 2^-18 |z|), below it a series
+            of five terms, whose rounding is within that of tanhf.
   alibi     slope x distance and its addition, relative to the sequence's last token:
             2 u |bias_t| + u |z_t|
   weight    exp2((z - m) log2 e): 4 u |z_t - m| in the exponent, and exp2f's own two
@@ -75,8 +77,10 @@ def tight_ref(case):
                     if kv and dtype == "bf16":
                         dz = dz + abs(scale) * (np.abs(kk) @ np.abs(q[r, h, m] - q16[r, h, m]))
                     if cap > 0:
+                        quarter = np.abs(z) >= 0.25 * cap
                         z = cap * np.tanh(z / cap)
-                        dz = dz + (4 * 2.0 ** -23 * cap if cap <= QUICK_CAP and not f32 else 8 * u * np.abs(z))
+                        quick = 4 * 2.0 ** -23 * cap if cap <= QUICK_CAP else np.where(quarter, 2.0 ** -18, 8 * u) * np.abs(z)
+                        dz = dz + (8 * u * np.abs(z) if f32 else quick)
                     if case["alibi"] is not None:
                         bias = float(case["alibi"][h]) * (t - pos)
                         z = z + bias

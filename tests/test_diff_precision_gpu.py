@@ -38,3 +38,23 @@ def test_maps_that_nearly_cancel(dtype, kv, size, layout, group):
 @pytest.mark.parametrize("dtype,kv", TYPES)
 def test_maps_that_nearly_cancel_for_several_tokens(dtype, kv):
     _check(nearly_equal_maps(make_case(22, dtype, kv, 64, "split", 2, 2, LENS, q_len=[4, 1, 2, 3])), ("v1", "v2"))
+
+
+@pytest.mark.parametrize("cap", [30.0, 64.0, 65.0, 1e4, 1e6, 1e30])
+@pytest.mark.parametrize("dtype,kv", TYPES)
+@pytest.mark.parametrize("group", [2, 8])
+def test_softcap_of_any_size(dtype, kv, group, cap):
+    """The cap's error goes by the logit: a large cap is as good as none."""
+    _check(make_case(23, dtype, kv, 64, "nhd", 2, group, LENS, softcap=cap, mult=1.5), ("v1", "v2"))
+
+
+@pytest.mark.parametrize("dtype,kv", TYPES)
+def test_logits_beyond_the_softcap(dtype, kv):
+    """Logits from far below to far above the cap."""
+    for cap, mult in ((0.5, 2.0), (20.0, 4.0), (80.0, 8.0), (200.0, 8.0)):
+        _check(make_case(25, dtype, kv, 64, "split", 2, 4, LENS, softcap=cap, mult=mult), ("v1", "v2"))
+
+
+@pytest.mark.parametrize("dtype,kv", [("f16", None), ("bf16", "e4m3")])
+def test_softcap_of_any_size_for_wide_heads_and_several_tokens(dtype, kv):
+    _check(make_case(24, dtype, kv, 128, "split", 2, 2, LENS, q_len=[2, 4, 1, 3], softcap=1e6), ("v1", "v2"))

@@ -88,9 +88,9 @@ pa_status pa_build_tables(const pa_tables_args* args, void* stream);
  * Stores the key and value rows of a step's tokens: token t goes to the slot
  * slots[t] = 16 * block + offset of both caches,
  *     K(block, head, offset) = key[t][head],   V(block, head, offset) = value[t][head],
- * times 1 / k_scale or 1 / v_scale (in fp32) and rounded to the nearest fp8 value
- * (half to even; beyond the largest finite value, that value; a NaN stays one)
- * when kv_dtype is fp8, and otherwise copied bit by bit.  A negative slot is skipped (padding); one past
+ * divided by k_scale or v_scale (the quotient rounded to fp32) and rounded to the
+ * nearest fp8 value (half to even; beyond the largest finite value, that value; a NaN
+ * stays one) when kv_dtype is fp8, and otherwise copied bit by bit.  A negative slot is skipped (padding); one past
  * the cache is skipped and reported (PA_DEVERR_SLOT).  The slots of a call are
  * distinct (of a slot given twice each element is that of one of its rows).
  * Slots that no row names keep their bytes.

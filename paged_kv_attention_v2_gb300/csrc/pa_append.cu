@@ -14,9 +14,11 @@
 // one are whole; with 32 one in two, 32768 tokens bf16 74 us) do not wait for
 // their slots.  Few rows are spread over more CTAs of eight rows each: the
 // scattered single-element stores of 32 tokens took 4 us on four CTAs, 2.1 now.
-// Measured, 32768 tokens (floor 40.7 us at the copy rate, e4m3 30.6): split keys
-// bf16 48.9, e4m3 40; split values bf16 44.3 when they begin with a page, 53.8 when
-// inside one, e4m3 53; NHD bf16 40.5 (39.5), e4m3 30-34 (29.6).
+// Measured, 32768 tokens, both at 6.8 TB/s (floor): split keys bf16 48.8 us (40.7), e4m3
+// 43.4 (30.6); split values bf16 44.1 (40.7) when they begin with a page, 50.4 when inside
+// one, e4m3 54.8 (30.6); keys and values NHD, bf16 40.5 (39.5), e4m3 36.2 (29.6).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -34,6 +36,22 @@ constexpr int kBS = PA_BLOCK_SIZE;
 constexpr int kThreads = 256;
 constexpr int kRows = 64, kFewRows = 8;  // rows per CTA
 
+// How a cache is scaled: its values are fp8(x / scale), the quotient rounded in fp32.
+// y = x (1 / scale) is at most two steps off it, and y + (x - y scale) (1 / scale), the
+// residual exact in a fused multiply-add, is the quotient to 2^-22 of a step before it
+// is rounded (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  With rows of at most 11 bits that can differ from
+// the rounded quotient at an fp8 tie (at most 5 bits) only where the scale's mantissa
+// is all ones: x - tie scale is a multiple of 2^-27, and near half a step of the tie
+// times the scale for no other.  There, where the residual may leave fp32's range
+// (scales outside 2^-80 .. 2^80) and beyond `top`, where y may be infinite, the chunk
+// is divided.  32768 tokens e4m3, keys split / values split / NHD: y alone 40.1 / 53.2 /
+// 33.8 us, so 43.4 / 54.8 / 36.2, every element divided 95.7 / 99.8 / 75.6.
+struct Scale {
+    float inv, scale;
+    float top;  // largest |y| taken so; -1: divide everything
+};
+
 struct AppendParams {
     const void* key;
     const void* value;
@@ -42,7 +60,7 @@ struct AppendParams {
     const int32_t* slots;
     int64_t key_stride, key_head_stride, value_stride, value_head_stride;
     int num_tokens, num_key_heads, key_head_size, num_value_heads, value_head_size, num_blocks;
-    float k_inv, v_inv;  // 1 / scale
+    Scale k, v;
     int32_t* dev_error;
 };
 
@@ -55,10 +73,24 @@ __device__ __forceinline__ uint32_t to_fp8x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, KV == kE4M3 ? __NV_E4M3 : __NV_E5M2);
 }
 
-// 16 bytes of the cache from the input row at src (16-byte aligned): the same
-// bytes, or 16 elements times `inv` quantised.
+// 16 elements divided and quantised.  Not inlined: its registers are no chunk's in flight.
 template <typename T, int KV>
-__device__ __forceinline__ uint4 load_chunk(const T* src, float inv) {
+__device__ __noinline__ uint4 divided_chunk(const T* src, float scale) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = __fdiv_rn((float)src[4 * i + k], scale);
+        o[i] = to_fp8x2<KV>(y[0], y[1]) | to_fp8x2<KV>(y[2], y[3]) << 16;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 16 bytes of the cache from the input row at src (16-byte aligned): the same
+// bytes, or 16 elements quantised.
+template <typename T, int KV>
+__device__ __forceinline__ uint4 load_chunk(const T* src, const Scale& q) {
     const uint4* s = reinterpret_cast<const uint4*>(src);
     if constexpr (KV == kSame) {
         return __ldg(s);
@@ -66,12 +98,19 @@ __device__ __forceinline__ uint4 load_chunk(const T* src, float inv) {
         constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
         const uint4 a = __ldg(s), b = __ldg(s + 1);
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        bool divide = false;
+        auto quotient = [&](float x) {
+            const float y = x * q.inv;
+            divide |= !(fabsf(y) <= q.top);
+            return fmaf(-fmaf(y, q.scale, -x), q.inv, y);  // (so a -0 stays one)
+        };
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 lo = pa::unpack2<BF>(w[2 * i]), hi = pa::unpack2<BF>(w[2 * i + 1]);
-            o[i] = to_fp8x2<KV>(lo.x * inv, lo.y * inv) | to_fp8x2<KV>(hi.x * inv, hi.y * inv) << 16;
+            o[i] = to_fp8x2<KV>(quotient(lo.x), quotient(lo.y)) | to_fp8x2<KV>(quotient(hi.x), quotient(hi.y)) << 16;
         }
+        if (divide) return divided_chunk<T, KV>(src, q.scale);
         return make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
@@ -91,7 +130,7 @@ __device__ __forceinline__ int slot_of(const AppendParams& p, int t0, int t, int
 // page of block 0 (pages of one head `block_bytes` apart), SIZE its head size.
 template <typename T, int KV, bool SPLIT, int SIZE, int ROWS>
 __device__ __forceinline__ void move_rows(const AppendParams& p, const T* src, int64_t stride, uint8_t* cache,
-                                          int64_t block_bytes, float inv, int t0, int n) {
+                                          int64_t block_bytes, const Scale& q, int t0, int n) {
     constexpr int E = KV == kSame ? (int)sizeof(T) : 1;  // bytes of a cache element
     constexpr int X = 16 / E, CH = SIZE / X;             // elements of a chunk, chunks of a token's head
     constexpr int ITEMS = ROWS * CH, PER = (ITEMS + kThreads - 1) / kThreads;
@@ -111,7 +150,7 @@ __device__ __forceinline__ void move_rows(const AppendParams& p, const T* src, i
             const int c = SPLIT ? (i >> 5) / (ROWS / 8) * 4 + (i >> 3 & 3) : i % CH;
             at[k] = -1;
             if (i < ITEMS && t < n) {
-                v[k] = load_chunk<T, KV>(src + t * stride + c * X, inv);
+                v[k] = load_chunk<T, KV>(src + t * stride + c * X, q);
                 const int s = slot_of(p, t0, t, n);
                 if (s >= 0)
                     at[k] = (int64_t)(s >> 4) * block_bytes +
@@ -127,7 +166,7 @@ __device__ __forceinline__ void move_rows(const AppendParams& p, const T* src, i
 // Values of the split layout: one head's rows of a block, transposed.
 template <typename T, int KV, int SIZE, int ROWS>
 __device__ __forceinline__ void transpose_rows(const AppendParams& p, const T* src, int64_t stride, uint8_t* cache,
-                                               int64_t block_bytes, float inv, uint8_t* tile) {
+                                               int64_t block_bytes, const Scale& q, uint8_t* tile) {
     constexpr int E = KV == kSame ? (int)sizeof(T) : 1;
     constexpr int X = 16 / E, CH = SIZE / X;
     constexpr bool PAGES = ROWS >= kBS && E < 4;  // whole pages by ldmatrix
@@ -144,7 +183,7 @@ __device__ __forceinline__ void transpose_rows(const AppendParams& p, const T* s
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int i = (k0 + k) * kThreads + tid, t = i / CH, c = i % CH;
-            if (t < n) v[k] = load_chunk<T, KV>(src + (t0 + t) * stride + c * X, inv);
+            if (t < n) v[k] = load_chunk<T, KV>(src + (t0 + t) * stride + c * X, q);
         }
     };
     load(0);
@@ -307,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 5) pa_append_kernel(const AppendPara
     const T* src = static_cast<const T*>(key ? p.key : p.value) + head * (key ? p.key_head_stride : p.value_head_stride);
     const int64_t page = (int64_t)kBS * size * E;
     uint8_t* cache = static_cast<uint8_t*>(key ? p.key_cache : p.value_cache) + head * page;
-    const float inv = key ? p.k_inv : p.v_inv;
+    const Scale q = key ? p.k : p.v;
 
     pa::pdl_launch_dependents();
     pa::pdl_wait_primary();
@@ -315,10 +354,10 @@ __global__ void __launch_bounds__(kThreads, 5) pa_append_kernel(const AppendPara
     auto with_size = [&](auto size_c) {
         constexpr int SIZE = decltype(size_c)::value;
         if (SPLIT && !key) {
-            transpose_rows<T, KV, SIZE, ROWS>(p, src, stride, cache, heads * page, inv, tile);
+            transpose_rows<T, KV, SIZE, ROWS>(p, src, stride, cache, heads * page, q, tile);
         } else {
             const int t0 = blockIdx.x * ROWS;
-            move_rows<T, KV, SPLIT, SIZE, ROWS>(p, src + t0 * stride, stride, cache, heads * page, inv, t0,
+            move_rows<T, KV, SPLIT, SIZE, ROWS>(p, src + t0 * stride, stride, cache, heads * page, q, t0,
                                                 min(ROWS, p.num_tokens - t0));
         }
     };
@@ -328,6 +367,16 @@ __global__ void __launch_bounds__(kThreads, 5) pa_append_kernel(const AppendPara
         with_size(std::integral_constant<int, 128>());
     else
         with_size(std::integral_constant<int, 256>());
+}
+
+Scale scale_of(float scale) {
+    Scale q;
+    q.scale = scale > 0.f ? scale : 1.f;
+    q.inv = 1.f / q.scale;
+    int e;
+    const bool ones = std::frexp(q.scale, &e) == 1.f - 0x1p-24f;
+    q.top = ones || q.scale < 0x1p-80f || q.scale > 0x1p80f ? -1.f : 65536.f;  // above both types' largest value
+    return q;
 }
 
 bool size_ok(int d) { return d == 64 || d == 128 || d == 256; }
@@ -406,9 +455,9 @@ extern "C" pa_status pa_append_kv(const pa_append_args* a, void* stream) {
     p.num_value_heads = a->num_value_heads;
     p.value_head_size = a->value_head_size;
     p.num_blocks = a->num_blocks;
-    p.k_inv = a->k_scale > 0.f ? 1.f / a->k_scale : 1.f;
-    p.v_inv = a->v_scale > 0.f ? 1.f / a->v_scale : 1.f;
-    if (!std::isfinite(p.k_inv) || !std::isfinite(p.v_inv)) return PA_ERR_INVALID_ARG;
+    p.k = scale_of(a->k_scale);
+    p.v = scale_of(a->v_scale);
+    if (!std::isfinite(p.k.inv) || !std::isfinite(p.v.inv)) return PA_ERR_INVALID_ARG;
     p.dev_error = a->dev_error;
 
     bool ok;

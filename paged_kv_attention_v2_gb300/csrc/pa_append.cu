@@ -88,15 +88,17 @@ __device__ __noinline__ uint4 divided_chunk(const T* src, float scale) {
 }
 
 // 16 bytes of the cache from the input row at src (16-byte aligned): the same
-// bytes, or 16 elements quantised.
+// bytes, or 16 elements quantised.  (Plain loads, of the slots too: the previous
+// kernel may write rows and slots while this one is resident, waiting for it, which
+// the read-only path must not be used for.)
 template <typename T, int KV>
 __device__ __forceinline__ uint4 load_chunk(const T* src, const Scale& q) {
     const uint4* s = reinterpret_cast<const uint4*>(src);
     if constexpr (KV == kSame) {
-        return __ldg(s);
+        return *s;
     } else {
         constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
-        const uint4 a = __ldg(s), b = __ldg(s + 1);
+        const uint4 a = s[0], b = s[1];
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         bool divide = false;
         auto quotient = [&](float x) {
@@ -118,7 +120,7 @@ __device__ __forceinline__ uint4 load_chunk(const T* src, const Scale& q) {
 // The slot of row t (-1: none), out of `n` rows at t0.
 __device__ __forceinline__ int slot_of(const AppendParams& p, int t0, int t, int n) {
     if (t >= n) return -1;
-    const int s = __ldg(p.slots + t0 + t);
+    const int s = p.slots[t0 + t];
     if (s >= p.num_blocks * kBS) {
         if (blockIdx.y == 0 && p.dev_error) atomicOr(p.dev_error, PA_DEVERR_SLOT);
         return -1;

@@ -180,8 +180,8 @@ __device__ __forceinline__ void query_rows(const Params& p, int s, int& q0, int&
         qn = 1;
         return;
     }
-    q0 = __ldg(p.query_start + s);
-    qn = __ldg(p.query_start + s + 1) - q0;
+    q0 = p.query_start[s];
+    qn = p.query_start[s + 1] - q0;
     if (qn < 0 || qn > p.max_q_len || q0 < 0 || q0 > p.num_q_rows - min(max(qn, 0), p.max_q_len)) {
         report(p, PA_DEVERR_SEQ_LEN);
         qn = qn < 0 ? 0 : min(qn, p.max_q_len);
@@ -394,7 +394,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
         c_q0 = 0;
         c_qn = 0;
         if (s < S) {
-            const int raw = __ldg(p.seq_lens + s);
+            const int raw = p.seq_lens[s];
             c_len = clamp_len(p, raw);
             if (c_len != raw) report(p, PA_DEVERR_SEQ_LEN);
             query_rows(p, s, c_q0, c_qn);  // a token at a negative position sees no key
@@ -423,7 +423,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
         spec_tb = spec_part * plen;
         const int idx = spec_tb / kBS + lane;
         if (spec_seq < S && idx < p.max_blocks_per_seq)
-            spec_ids = __ldg(p.block_tables + (int64_t)spec_seq * p.max_blocks_per_seq + idx);
+            spec_ids = p.block_tables[(int64_t)spec_seq * p.max_blocks_per_seq + idx];
     }
     load_chunk(0);
     // Final metadata: lengths and block ids are read before the wait for the
@@ -483,7 +483,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
     // used, so that no copy waits on the load.
     auto load_ids = [&](const ProducerTile& t, int pc) {
         return (t.valid && pc + lane < t.npages)
-                   ? __ldg(p.block_tables + (int64_t)t.seq * p.max_blocks_per_seq + t.tb / kBS + pc + lane)
+                   ? p.block_tables[(int64_t)t.seq * p.max_blocks_per_seq + t.tb / kBS + pc + lane]
                    : 0;
     };
     auto check_ids = [&](int blk) {
@@ -698,7 +698,7 @@ template <typename T, int HEAD>
 __device__ __forceinline__ void diff_row(const Params& p, int64_t row, int h, float (&o1)[HEAD / 32],
                                          const float (&o2)[HEAD / 32], int lane) {
     constexpr int VEC = HEAD / 32;
-    const float lambda = __ldg(p.lambdas + row * p.lambda_stride + h);
+    const float lambda = p.lambdas[row * p.lambda_stride + h];
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -714,7 +714,7 @@ __device__ __forceinline__ void diff_row(const Params& p, int64_t row, int h, fl
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         o1[v] *= sc;
-        if (p.norm && p.norm_weight) o1[v] *= __ldg(p.norm_weight + lane_col<HEAD>(lane, v));
+        if (p.norm && p.norm_weight) o1[v] *= p.norm_weight[lane_col<HEAD>(lane, v)];
     }
     store_row<T, HEAD>(static_cast<T*>(p.out) + (row * p.num_heads + h) * HEAD, o1, lane);
 }
@@ -849,7 +849,7 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
                 // partition max into the sequence frame (last token of the
                 // sequence) -- the reduce kernel finishes the shift to absolute
                 // positions after merging.
-                if (p.alibi) m += __ldg(p.alibi + head) * (float)(d.tok_end - d.len);
+                if (p.alibi) m += p.alibi[head] * (float)(d.tok_end - d.len);
                 p.max_logits[ps] = m;
                 p.exp_sums[ps] = L;
             }
@@ -1177,7 +1177,7 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int h = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
-                sl[nt][e] = (has_alibi && h < GE) ? __ldg(p.alibi + d.kvh * G + h % G) : 0.f;
+                sl[nt][e] = (has_alibi && h < GE) ? p.alibi[d.kvh * G + h % G] : 0.f;
             }
         // key range of each of this lane's rows: its query token's position and
         // window, within the tile (padded rows get the tile's range)
@@ -1559,7 +1559,7 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int h = C::row_of((nt0 + nt) * 8 + 2 * cq + e);
-                sl[nt][e] = (has_alibi && h < GE) ? __ldg(p.alibi + d.kvh * G + h % G) : 0.f;
+                sl[nt][e] = (has_alibi && h < GE) ? p.alibi[d.kvh * G + h % G] : 0.f;
             }
         // key range of each of this lane's rows: its query token's position and
         // window, within the tile (padded rows get the tile's range)
@@ -1867,7 +1867,7 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int v = nt * 8 + 2 * cq + e;
-                sl[nt][e] = (has_alibi && v < GE) ? __ldg(p.alibi + d.kvh * G + v % G) : 0.f;
+                sl[nt][e] = (has_alibi && v < GE) ? p.alibi[d.kvh * G + v % G] : 0.f;
                 int lo = d.tok_begin, hi = d.tok_end - 1;
                 if (C::kMQ && v < GE) {
                     const int pos = d.len - qn + v / G;
@@ -2163,7 +2163,7 @@ __device__ void consumer_fma(const Params& p, const Smem& sm, int warp, int lane
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int v = row0 + i;
-            sl[i] = (has_alibi && v < GE) ? __ldg(p.alibi + d.kvh * G + v % G) : 0.f;
+            sl[i] = (has_alibi && v < GE) ? p.alibi[d.kvh * G + v % G] : 0.f;
             int lo = d.tok_begin, hi = d.tok_end - 1;
             if (C::kMQ && v < GE) {
                 const int pos = d.len - qn + v / G;
@@ -2589,7 +2589,7 @@ __global__ void __launch_bounds__(WARPS * 32) pa_reduce_kernel(const Params p) {
         // statistics: sequence frame -> absolute ALiBi positions (every read of
         // max_logits above happened before the barrier)
         if (p.alibi) {
-            const float shift = __ldg(p.alibi + h) * (float)(len - 1);
+            const float shift = p.alibi[h] * (float)(len - 1);
             for (int q = p0 + tid; q < P; q += NT) ml[q] += shift;
         }
     }
@@ -2733,7 +2733,7 @@ __device__ __forceinline__ void merge_stats_row(const Params& p, int64_t srow, i
     // statistics: sequence frame -> absolute ALiBi positions; unused partitions
     // padded (every read of this row's statistics is above, in this warp)
     __syncwarp();
-    const float shift = p.alibi ? __ldg(p.alibi + h) * (float)(len - 1) : 0.f;
+    const float shift = p.alibi ? p.alibi[h] * (float)(len - 1) : 0.f;
     for (int q = lane; q < p.max_parts; q += 32) {
         if (q >= p0 && q < P) {
             if (p.alibi) ml[q] += shift;
@@ -2887,7 +2887,7 @@ __device__ __forceinline__ void diff_merge_row(const Params& p, int64_t row, int
     // statistics: sequence frame -> absolute ALiBi positions; unused partitions
     // padded (every read of this row's statistics is above, in this warp)
     __syncwarp();
-    const float shift = p.alibi ? __ldg(p.alibi + h) * (float)(len - 1) : 0.f;
+    const float shift = p.alibi ? p.alibi[h] * (float)(len - 1) : 0.f;
     for (int q = lane; q < 2 * p.max_parts; q += 32) {
         const int map = q >= p.max_parts, at = q - map * p.max_parts;
         if (at >= p0 && at < P) {
@@ -3067,7 +3067,7 @@ __global__ void __launch_bounds__(WARPS * 32) pa_diff_reduce_kernel(const Params
     }
     // statistics: sequence frame -> absolute ALiBi positions, unused partitions
     // padded (every read of them above happened before the barrier)
-    const float shift = p.alibi ? __ldg(p.alibi + h) * (float)(len - 1) : 0.f;
+    const float shift = p.alibi ? p.alibi[h] * (float)(len - 1) : 0.f;
     for (int q = tid; q < p.max_parts; q += HALF) {
         if (q >= p0 && q < P) {
             if (p.alibi) ml[q] += shift;

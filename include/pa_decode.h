@@ -164,7 +164,8 @@ typedef struct pa_decode_args {
     /* Sliding window, in keys visible to the query including its own token:
      * 0 (or < 0) = off, so a zero-initialised struct has no window; otherwise
      * the query, at position seq_lens[s] - 1, attends the keys
-     * t >= seq_lens[s] - sliding_window.  This is window_left + 1 for the
+     * t >= seq_lens[s] - sliding_window (what the slots before them hold does
+     * not matter).  This is window_left + 1 for the
      * window_left of AttnDispatchConfig in attn_dispatch.py (-1 there = off).
      * Partitions with no key in the window are skipped (unused: max_logits
      * -inf, exp_sums 0). */
@@ -188,8 +189,10 @@ typedef struct pa_decode_args {
      * seq_lens[s] - qn + i and attends the keys t <= that position (causal),
      * within its own sliding window, so its result is the single-token decode
      * of the sequence cut after that position; a token at a negative position
-     * sees no key and gets a zero row.  qn > max_query_len is reported as
-     * PA_DEVERR_SEQ_LEN and clamped. */
+     * sees no key and gets a zero row.  (That of finite values: a value of the
+     * cache that is infinite or NaN reaches the rows of all the sequence's tokens
+     * in the call once one of them sees it, as a product with weight zero.)
+     * qn > max_query_len is reported as PA_DEVERR_SEQ_LEN and clamped. */
     const int32_t* query_start;
     int32_t num_query_tokens;  /* rows of query / out / workspace */
     int32_t max_query_len;     /* >= every qn, >= 1; max_query_len * group <= 16 */

@@ -1053,56 +1053,47 @@ __device__ __forceinline__ uint32_t v_frag_off(int lane, int mt) {
     }
 }
 
-// Zero the V entries of tokens >= valid in a staged 16-bit page so that the
-// P.V product never sees unused slots (which may hold anything, even NaN).
-template <int LAYOUT, int HEAD>
-__device__ __forceinline__ void zero_v_tail16(uint32_t vpage, int valid, int lane) {
+// Zero the V entries of tokens [t0, t1) in a staged page.  Split: [d][16 tokens].  NHD:
+// swizzled blocks of 16 token rows of up to 128 bytes (the swizzle permutes 16-byte
+// chunks within a row, so a row stays one token's).
+template <class C, int LAYOUT, int HEAD>
+__device__ __forceinline__ void zero_v(uint32_t vpage, int t0, int t1, int lane) {
+    constexpr int E = C::kKvElem;
     if constexpr (LAYOUT == kSplit) {
         for (int d = lane; d < HEAD; d += 32)
-            for (int t = valid; t < kBS; ++t)
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(vpage + (uint32_t)(d * kBS + t) * 2),
-                             "h"((unsigned short)0)
-                             : "memory");
+            for (int t = t0; t < t1; ++t) {
+                const uint32_t a = vpage + (uint32_t)((d * kBS + t) * E);
+                if constexpr (E == 4)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(0u) : "memory");
+                else if constexpr (E == 2)
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((unsigned short)0) : "memory");
+                else
+                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "h"((unsigned short)0) : "memory");
+            }
     } else {
-        const int rows = (kBS - valid) * (HEAD / 64);
-        for (int i = lane; i < rows * 8; i += 32) {
-            const int rowi = i >> 3, chunk = i & 7;
-            const int tok = valid + rowi / (HEAD / 64), half = rowi % (HEAD / 64);
-            const uint32_t a = vpage + (uint32_t)(half * 2048 + tok * 128 + chunk * 16);
+        constexpr int ROW = HEAD * E < 128 ? HEAD * E : 128;  // bytes of a row of a block
+        constexpr int CH = ROW / 16, BLOCKS = HEAD * E / ROW;
+        const int n = (t1 - t0) * CH;
+        for (int i = lane; i < n * BLOCKS; i += 32) {
+            const int b = i / n, c = i - b * n;
+            const uint32_t a = vpage + (uint32_t)(b * kBS * ROW + t0 * ROW + c * 16);
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
         }
     }
 }
 
-// Zero the fp32 V entries of tokens >= valid in a staged page: split [d][16
-// tokens], or NHD as HEAD / 32 swizzled blocks of 16 token rows x 128 bytes
-// (the swizzle permutes 16-byte chunks within a row, so a row stays one token's).
-template <int LAYOUT, int HEAD>
-__device__ __forceinline__ void zero_v_tail32(uint32_t vpage, int valid, int lane) {
-    if constexpr (LAYOUT == kSplit) {
-        for (int d = lane; d < HEAD; d += 32)
-            for (int t = valid; t < kBS; ++t)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(vpage + (uint32_t)(d * kBS + t) * 4), "r"(0u)
-                             : "memory");
-    } else {
-        const int rows = (kBS - valid) * (HEAD / 32);
-        for (int i = lane; i < rows * 8; i += 32) {
-            const int rowi = i >> 3, chunk = i & 7;
-            const int tok = valid + rowi / (HEAD / 32), bx = rowi % (HEAD / 32);
-            const uint32_t a = vpage + (uint32_t)(bx * 2048 + tok * 128 + chunk * 16);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
-        }
+// Zero the V entries of a page's tokens that no row of the tile sees, before the window
+// and behind the end (where a slot may hold anything): their weight is zero, but the
+// P.V product of zero and an infinity or a NaN is none.
+template <class C, int LAYOUT, int HEAD>
+__device__ __forceinline__ void zero_unseen(uint32_t vpage, int tok0, const TileDesc& d, int lane) {
+    const int first = max(d.tok_begin - tok0, 0), valid = min(kBS, d.tok_end - tok0);
+    if (first > 0 || valid < kBS) {
+        zero_v<C, LAYOUT, HEAD>(vpage, 0, first, lane);
+        zero_v<C, LAYOUT, HEAD>(vpage, valid, kBS, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
     }
-}
-
-// Zero the fp8 V entries of tokens >= valid in a staged split page [d][16 tokens].
-template <int HEAD>
-__device__ __forceinline__ void zero_v_tail8(uint32_t vpage, int valid, int lane) {
-    for (int d = lane; d < HEAD; d += 32)
-        for (int t = valid; t < kBS; ++t)
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(vpage + (uint32_t)(d * kBS + t)),
-                         "h"((unsigned short)0)
-                         : "memory");
 }
 
 template <class C, typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC>
@@ -1232,13 +1223,8 @@ __device__ void consumer_mma(const Params& p, const Smem& sm, int warp, int lane
             const uint32_t kp = sm.ring + st * C::kStageBytes;
             const uint32_t vp = kp + C::kPageBytes;
             const int tok0 = page0 + j * kBS;
-            const int valid = min(kBS, d.tok_end - tok0);  // slots >= valid: past the sequence
             const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;  // some key masked
-            if (valid < kBS) {
-                zero_v_tail16<LAYOUT, HEAD>(vp, valid, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
+            zero_unseen<C, LAYOUT, HEAD>(vp, tok0, d, lane);
 
             // S^T[token][head] = K . Q^T
             // two accumulator chains (even / odd k-steps) for MMA latency hiding
@@ -1451,19 +1437,6 @@ __device__ __forceinline__ uint32_t v8_frag_off(int lane, int mt) {
     }
 }
 
-// fp8 NHD value page: zero the rows of tokens >= valid (whole rows: the
-// swizzle only permutes chunks inside a row).
-template <int HEAD>
-__device__ __forceinline__ void zero_v_tail8_nhd(uint32_t vpage, int valid, int lane) {
-    constexpr int ROW = HEAD > 128 ? 128 : HEAD;  // bytes of a row of a block
-#pragma unroll
-    for (int b = 0; b < HEAD / ROW; ++b)
-        for (int i = lane; i < (kBS - valid) * ROW / 4; i += 32)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(vpage + (uint32_t)(b * kBS * ROW + valid * ROW + 4 * i)),
-                         "r"(0u)
-                         : "memory");
-}
-
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -1614,16 +1587,8 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
             const uint32_t kp = sm.ring + st * C::kStageBytes;
             const uint32_t vp = kp + C::kPageBytes;
             const int tok0 = page0 + j * kBS;
-            const int valid = min(kBS, d.tok_end - tok0);  // slots >= valid: past the sequence
             const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;  // some key masked
-            if (valid < kBS) {
-                if constexpr (LAYOUT == kNHD)
-                    zero_v_tail8_nhd<HEAD>(vp, valid, lane);
-                else
-                    zero_v_tail8<HEAD>(vp, valid, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
+            zero_unseen<C, LAYOUT, HEAD>(vp, tok0, d, lane);
 
             // S^T[row][head]: key page [d/16][token][16 bytes] (split) or [token][d]
             // with swizzled 16-byte chunks (NHD)
@@ -1916,13 +1881,8 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
             const uint32_t kp = sm.ring + st * C::kStageBytes;
             const uint32_t vp = kp + C::kPageBytes;
             const int tok0 = page0 + j * kBS;
-            const int valid = min(kBS, d.tok_end - tok0);
             const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;
-            if (valid < kBS) {
-                zero_v_tail32<LAYOUT, HEAD>(vp, valid, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
+            zero_unseen<C, LAYOUT, HEAD>(vp, tok0, d, lane);
 
             // S^T[token][row] = K . Q^T; the four 8 x 4 blocks (tokens 0-7 /
             // 8-15, head dims 8kk..+3 / +4..+7) of a k-step are its A fragment,
@@ -2222,7 +2182,6 @@ __device__ void consumer_fma(const Params& p, const Smem& sm, int warp, int lane
             const uint32_t kp = sm.ring + st * C::kStageBytes;
             const uint32_t vp = kp + C::kPageBytes;
             const int tok0 = page0 + j * kBS;
-            const int valid = min(kBS, d.tok_end - tok0);
             const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;
 
             float s[4][4];  // [token j][column i]
@@ -2297,11 +2256,7 @@ __device__ void consumer_fma(const Params& p, const Smem& sm, int warp, int lane
                 *sm.abort = 1;
                 return;
             }
-            if (valid < kBS) {
-                zero_v_tail32<LAYOUT, HEAD>(vp, valid, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
+            zero_unseen<C, LAYOUT, HEAD>(vp, tok0, d, lane);
 
             uint32_t vlast = 0;  // the page's last read
             float o[DV][8];      // the page's sum

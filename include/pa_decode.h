@@ -360,7 +360,8 @@ pa_status pa_plan(const pa_decode_args* args, pa_launch_plan* plan);
  *     out[row][h] = out_scale * o                                                without
  * with softcap, alibi_slopes, sliding_window, fp8 caches and query_start as in
  * pa_decode, applied to both maps' logits.  Sums, statistics and the norm are
- * fp32; the output is rounded once.  A row that sees no key gets zeros.
+ * fp32 (so |o| has to stay below 1e18 with norm); the output is rounded once.  A row
+ * that sees no key gets zeros.
  * (The pages have no counterpart.)
  *
  * `decode` describes the call as for pa_decode, with these differences, where
@@ -374,8 +375,12 @@ pa_status pa_plan(const pa_decode_args* args, pa_launch_plan* plan);
  *   exp_sums, max_logits [rows][num_heads][2][P], tmp_out [rows][num_heads][2][P][2 * head_size]
  *                (pa_workspace_elems with 2 * num_heads heads of 2 * head_size): room
  *                for the maps' partitions, which the library makes as long as suits
- *                the batch (pa_diff_plan tells); what it holds after the call is unspecified
- *   max_query_len * (num_heads / num_kv_heads) <= 8  (one tile holds both maps' rows)
+ *                the batch (partition_tokens of pa_diff_plan).  After a v2 call the fronts
+ *                of exp_sums and max_logits hold the maps' statistics,
+ *                [rows][num_heads][2][ceil(max_seq_len / partition_tokens)], as
+ *                pa_decode leaves them; the rest of the workspace is unspecified
+ *   max_query_len * (num_heads / num_kv_heads) <= 8  (a tile holds both maps of each row
+ *                in the 16 columns that pa_decode has for 16 rows)
  *   max_seq_len  at most 2^30
  *   num_query_tokens may pass query_start[num_seqs] (a padded batch): the rows of
  *                out behind the last token stay as they were; 0 is a no-op

@@ -231,7 +231,7 @@ struct Cfg {
     // ones of value heads of 128: warps in pairs of page streams, one n-tile each;
     // every page is consumed by two warps.  (fp8: the pair would convert every
     // value twice; one warp with both n-tiles, five warps and fifteen stages: 32 x
-    // 4096 e4m3 with four tokens 65 -> 57 us.)
+    // 4096 e4m3 with four tokens 65 -> 57 us, both with one term of P.)
     static constexpr bool kPairs = NT == 2 && (DIFF ? (KV == kKvSame || HEAD > 128) : (KV == kKvSame && !kF32));
     static constexpr int kMergeRows = kPairs ? 8 : kMaxG;  // merge-buffer rows per warp
     static constexpr int kPageWarps = kPairs ? 2 : 1;      // warps that release each page
@@ -1446,7 +1446,7 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 // Consumer for fp8 caches (split layout).  The tensor-core inputs are fp16 for
 // both query types: fp8 -> fp16 is exact; a bf16 query is converted once per
 // tile (values beyond the fp16 range are clamped and PA_DEVERR_QUERY_RANGE is
-// set); P is packed to fp16 (11 significant bits, no second term needed).
+// set); P is packed to fp16 (11 significant bits; two terms in a differential call).
 // Every lane fetches four fp8 values with one 32-bit shared load.  For that
 // the reduction index of each MMA is permuted identically on both operands:
 //   Q.K^T  k-index 2cq+j <-> head dim 4cq+j, 2cq+8+j <-> 4cq+2+j  (per 16-dim step)
@@ -2057,7 +2057,8 @@ __device__ void consumer_tf32(const Params& p, const Smem& sm, int warp, int lan
 // instructions of a warp at value heads of 128.  (As three tf32 products each it
 // is 96 m16n8k8 MMAs of some fifty cycles.  GPU time with those and so: 32 x 4096,
 // groups of four, 87 and 81.4 us, of eight 116 and 119; heads of 256 247 and 162,
-// of eight, 16 sequences, 135 and 131; two short sequences 17.4 and 15.0.  And
+// of eight, 16 sequences, 135 and 131; two short sequences, call after call, 17.4 and
+// 15.1 (14.4 in a graph).  And
 // every product is rounded once.)  What bounds it is what shared memory returns
 // to registers, 128 bytes a cycle: per page of a warp 128 + 192 cycles, so packed
 // fp32 pairs, which need P or V twice, cost more than they save (86.7).  Column

@@ -203,9 +203,9 @@ cudaError_t launch_family(const Params& p, const LaunchArgs& la) {
 // ---------------------------------------------------------------- differential
 //
 // Measured (GPU time per call, against the KV bytes at the copy rate of 6.8 TB/s):
-// 32 x 4096, keys of 64, values of 128, fp16 43.9 us (39.6), fp32 81.4 (79); 4 x
-// 100000 bf16, groups of seven, 122.9 (120.6), e4m3 76 (60.3); 32 x 4096 e4m3 with
-// four tokens 60.3 (39.6); 64 ragged sequences, keys of 128, values of 256, bf16
+// 32 x 4096, keys of 64, values of 128, fp16 44.4 us (39.6), fp32 81.4 (79); 4 x
+// 100000 bf16, groups of seven, 122.9 (120.6), e4m3 83 (60.3); 32 x 4096 e4m3 with
+// four tokens 63.2, with a softcap 68.7 (39.6); 64 ragged sequences, keys of 128, values of 256, bf16
 // 152 (140.6), fp32 of those heads 32 x 4096 164 (158).  16-bit caches, and fp32 ones
 // up to four rows, are bound by memory, fp8 and fp32 ones of more rows by the
 // consumers' chain of a page.

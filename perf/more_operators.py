@@ -20,6 +20,8 @@ DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16,
           "e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2, "e2m1": torch.uint8}
 LEVELS = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
 DEVICE = "cuda"
+# scales of 4-bit caches of values about 1: their largest over 6 * 448, as numbers of 32 bits
+K_SCALE, V_SCALE = float(np.float32(0.0019)), float(np.float32(0.0023))
 
 
 # ------------------------------------------------------------------ cases
@@ -203,7 +205,7 @@ def _prepare_append(case, rng, gen):
         key, value = _normal((tokens, h, d), dtype, gen), _normal((tokens, h, d), dtype, gen)
     old = lambda: torch.randint(0, 256, (blocks, h, 9 * d), generator=gen, device=DEVICE, dtype=torch.uint8)  # noqa: E731
     return dict(op="append", key=key, value=value, slots=_int(slots), key_cache=old(), value_cache=old(),
-                k_scale=0.0019, v_scale=0.0023)
+                k_scale=K_SCALE, v_scale=V_SCALE)
 
 
 def _prepare_attention(case, rng, gen):
@@ -217,7 +219,7 @@ def _prepare_attention(case, rng, gen):
     table, blocks = _table(lens, _pages(case["longest"]), rng)
     rows = int(new.sum())
     layout = case["layout"] if weights else "nhd"
-    scale = {"same": 1.0, "e2m1": 0.0019}.get(kv, 2.0 ** -6)
+    scale = {"same": 1.0, "e2m1": K_SCALE}.get(kv, 2.0 ** -6)
     ks, vs = _cache_shapes(blocks, hk, d, hk, d, layout, DTYPES[case["dtype"] if kv == "same" else kv].itemsize)
     fill = lambda shape: (_codes((blocks, hk, d), gen, scale) if kv == "e2m1" else  # noqa: E731
                           _normal(shape, dtype if kv == "same" else DTYPES[kv], gen, scale))
@@ -272,7 +274,7 @@ def _prepare_compact(case, rng, gen):
     table, blocks = _table(lens, _pages(top), rng)
     dtype, layout = DTYPES[case["dtype"]], case["layout"]
     ks, vs = _cache_shapes(blocks, case["k_heads"], case["k_size"], hk, case["v_size"], layout, dtype.itemsize)
-    fill = lambda shape, size: (_codes((blocks, hk, size), gen, 0.0019) if case["dtype"] == "e2m1" else  # noqa: E731
+    fill = lambda shape, size: (_codes((blocks, hk, size), gen, K_SCALE) if case["dtype"] == "e2m1" else  # noqa: E731
                                 _normal(shape, dtype, gen))
     # a choice as the selection makes it: the first and the last tokens, and some of those between
     live = torch.from_numpy(lens).to(DEVICE)[:, None, None]

@@ -95,6 +95,12 @@ pa_status pa_build_tables(const pa_tables_args* args, void* stream);
  * the cache is skipped and reported (PA_DEVERR_SLOT).  The slots of a call are
  * distinct (of a slot given twice each element is that of one of its rows).
  * Slots that no row names keep their bytes.
+ * 4-bit caches (PA_KV_FP4_E2M1, 16-bit rows of 64 or 128, NHD): of each 16 successive
+ * elements x of a row, with g = k_scale or v_scale,
+ *     scale = e4m3(max|x| / (6 g)),   code = e2m1(x / (g scale)),
+ * the real quotients rounded once, half to even, beyond the largest value: that value
+ * (an infinity too).  A scale that comes out zero makes all 16 codes zero; a NaN among the
+ * elements makes the scale NaN and the codes zero.
  *
  * Keys and values have head counts and sizes of their own: num_kv_heads of
  * head_size for pa_decode, twice the heads for the keys and twice the size for
@@ -108,14 +114,14 @@ typedef struct pa_append_args {
     const int32_t* slots; /* [num_tokens] */
     int64_t key_stride, key_head_stride, value_stride, value_head_stride; /* elements */
     int32_t num_tokens;  /* at most 2^30 */
-    int32_t num_key_heads, key_head_size;     /* head sizes: 64, 128 or 256 */
+    int32_t num_key_heads, key_head_size;     /* head sizes: 64, 128 or 256 (4-bit: not 256) */
     int32_t num_value_heads, value_head_size;
     int32_t num_blocks;  /* pages in each cache, below 2^27 */
     int32_t block_size;  /* must be PA_BLOCK_SIZE */
     int32_t dtype;       /* pa_dtype of key and value */
     int32_t layout;      /* pa_layout */
     int32_t kv_dtype;    /* pa_kv_dtype of the caches */
-    float k_scale, v_scale; /* fp8 caches; values <= 0 mean 1.0, a reciprocal beyond fp32 is refused */
+    float k_scale, v_scale; /* fp8 and 4-bit caches; values <= 0 mean 1.0, a reciprocal beyond fp32 is refused */
     int32_t* dev_error;  /* optional: PA_DEVERR_* bits */
 } pa_append_args;
 

@@ -73,7 +73,8 @@ typedef enum pa_dtype { PA_DTYPE_F32 = 0, PA_DTYPE_F16 = 1, PA_DTYPE_BF16 = 2 } 
 typedef enum pa_kv_dtype {
     PA_KV_SAME = 0,      /* same as dtype */
     PA_KV_FP8_E4M3 = 3,  /* OCP fp8 E4M3 (bias 7, no infinities); f16/bf16 query */
-    PA_KV_FP8_E5M2 = 4   /* OCP fp8 E5M2 (bias 15); f16/bf16 query */
+    PA_KV_FP8_E5M2 = 4,  /* OCP fp8 E5M2 (bias 15); f16/bf16 query */
+    PA_KV_FP4_E2M1 = 5   /* 4 bits and a scale per 16 elements (below); f16/bf16 query */
 } pa_kv_dtype;
 
 /*
@@ -86,6 +87,14 @@ typedef enum pa_kv_dtype {
  *  PA_LAYOUT_NHD:   key_cache and value_cache [num_blocks][num_kv_heads][block_size][head_size]
  *                   (dispatch_decode argument comments of attn_dispatch.py).
  * All arrays are dense, row-major, without padding.
+ *
+ * 4-bit caches (PA_KV_FP4_E2M1, with PA_LAYOUT_NHD): key_cache and value_cache
+ * [num_blocks][num_kv_heads][9 * head_size] bytes.  A page of one head is 16 rows of
+ * head_size / 2 bytes, element 2i of the token's head in the low half of byte i and
+ * 2i + 1 in the high half (e2m1: a sign, 0 0.5 1 1.5 2 3 4 6), then 16 rows of
+ * head_size / 16 e4m3 scales, one for every 16 successive elements:
+ *     K(t)[i] = k_scale * scale(t, i / 16) * code(t, i),   V likewise with v_scale.
+ * A scale that is NaN makes its 16 elements NaN.
  */
 typedef enum pa_layout { PA_LAYOUT_SPLIT = 0, PA_LAYOUT_NHD = 1 } pa_layout;
 
@@ -102,7 +111,7 @@ typedef enum pa_mode { PA_MODE_AUTO = 0, PA_MODE_V1 = 1, PA_MODE_V2 = 2 } pa_mod
 #define PA_DEVERR_BLOCK_ID   1  /* a block table entry outside [0, num_blocks); page 0 read instead */
 #define PA_DEVERR_SEQ_LEN    2  /* seq_lens[s] < 0 or > max_seq_len; clamped into [0, max_seq_len] */
 #define PA_DEVERR_TIMEOUT    4  /* an internal pipeline wait exceeded its limit; results invalid   */
-#define PA_DEVERR_QUERY_RANGE 8 /* fp8 caches with a bf16 query: |q| > 65504 clamped (fp16 MMAs)  */
+#define PA_DEVERR_QUERY_RANGE 8 /* fp8 or 4-bit caches with a bf16 query: |q| > 65504 clamped (fp16 MMAs)  */
 #define PA_DEVERR_POOL       16 /* pa_build_tables: too few free pages, or a pool state that cannot be */
 #define PA_DEVERR_SLOT       32 /* pa_append_kv: a slot past the cache; skipped */
 
@@ -174,7 +183,7 @@ typedef struct pa_decode_args {
      * key layout packs x = 16 elements per 16 bytes. */
     int32_t kv_dtype;
     /* Dequantisation scales of fp8 caches: K = k_scale * fp8(K), V = v_scale *
-     * fp8(V); values <= 0 mean 1.0 (so a zero-initialised struct has none). */
+     * fp8(V), and of 4-bit ones on top of their block scales; values <= 0 mean 1.0 (so a zero-initialised struct has none). */
     float k_scale;
     float v_scale;
     /* Several query tokens per sequence (speculative / multi-token decode, the

@@ -27,7 +27,7 @@ __all__ = ["pa_decode", "pa_decode_static_workspace", "alloc_workspace", "max_nu
 
 _LAYOUTS = {"split": _abi.PA_LAYOUT_SPLIT, "nhd": _abi.PA_LAYOUT_NHD}
 _MODES = {"auto": _abi.PA_MODE_AUTO, "v1": _abi.PA_MODE_V1, "v2": _abi.PA_MODE_V2}
-_KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP8_E5M2}
+_KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP8_E5M2, "e2m1": _abi.PA_KV_FP4_E2M1}
 
 
 class PaDecodeError(RuntimeError):
@@ -138,7 +138,9 @@ def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num
     window_left follows AttnDispatchConfig (-1 = no window; the query sees the
     keys t >= seq_len - 1 - window_left) and becomes sliding_window = window_left + 1.
     kv_dtype "e4m3" / "e5m2" marks fp8 caches (raw uint8 tensors) holding K / k_scale
-    and V / v_scale; the query dtype sets the compute and output type.
+    and V / v_scale, "e2m1" 4-bit ones ([num_blocks, num_kv_heads, 9 * head_size]
+    bytes, layout "nhd"; include/pa_decode.h); the query dtype sets the compute and
+    output type.
     query_start ([num_seqs + 1] int32 offsets) gives several query tokens per
     sequence: query / out rows are query tokens, and max_query_len (>= every
     sequence's token count) is required with it.  seq_lens_host (a host copy of
@@ -161,8 +163,10 @@ def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num
         if query_start.dtype.itemsize != 4 or query_start.numel() != num_seqs + 1:
             raise ValueError("query_start must be int32 [num_seqs + 1]")
     num_blocks = key_cache.shape[0]
-    kv_bytes = 1 if kv_dtype in ("e4m3", "e5m2") else query.element_size()
+    kv_bytes = query.element_size() if kv_dtype is None else 1
     page = num_kv_heads * block_size * head_size  # elements of one block of one cache
+    if kv_dtype == "e2m1":  # bytes: half of one for each element, one for every 16
+        page = num_kv_heads * 9 * head_size
     for name, c in (("key_cache", key_cache), ("value_cache", value_cache)):
         if c.element_size() != kv_bytes:
             raise ValueError(f"{name} has {c.element_size()}-byte elements, kv_dtype "

@@ -13,11 +13,11 @@ import torch
 from . import _abi
 
 _LAYOUT = {"split": _abi.PA_LAYOUT_SPLIT, "nhd": _abi.PA_LAYOUT_NHD}
-_KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP8_E5M2}
+_KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP8_E5M2, "e2m1": _abi.PA_KV_FP4_E2M1}
 _DTYPE = {torch.float32: _abi.PA_DTYPE_F32, torch.float16: _abi.PA_DTYPE_F16,
           torch.bfloat16: _abi.PA_DTYPE_BF16}
 # cache element types of each kv_dtype (None: the rows' own)
-_CACHE = {"e4m3": (torch.uint8, torch.float8_e4m3fn), "e5m2": (torch.uint8, torch.float8_e5m2)}
+_CACHE = {"e4m3": (torch.uint8, torch.float8_e4m3fn), "e5m2": (torch.uint8, torch.float8_e5m2), "e2m1": (torch.uint8,)}
 _TABLES = _abi.packer(_abi.PaTablesArgs)
 _APPEND = _abi.packer(_abi.PaAppendArgs)
 _PAGE = _abi.PA_BLOCK_SIZE
@@ -126,8 +126,9 @@ def _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_
         raise ValueError("the head dims of key and value must be contiguous")
     if value.get_device() != device:
         raise ValueError("key and value must be on one device")
-    for name, cache, page in (("key_cache", key_cache, k_heads * k_size * _PAGE),
-                              ("value_cache", value_cache, v_heads * v_size * _PAGE)):
+    per = 9 if kv_dtype == "e2m1" else _PAGE  # elements of the cache (e2m1: bytes) per element of a row
+    for name, cache, page in (("key_cache", key_cache, k_heads * k_size * per),
+                              ("value_cache", value_cache, v_heads * v_size * per)):
         if cache.dtype not in types:
             raise ValueError(f"{name} is {cache.dtype}, kv_dtype {kv_dtype or 'same as key'} needs {types[0]}")
         if cache.numel() != blocks * page or not cache.is_contiguous() or cache.get_device() != device:
@@ -160,7 +161,10 @@ def pa_append_kv(key, value, key_cache, value_cache, slots, *, layout: str = "sp
     a multiple of 16 bytes, as in a slice of a fused projection), slots [tokens]
     int32 from pa_build_tables (negative: skip), caches in the split or NHD
     layout; kv_dtype "e4m3" / "e5m2" quantises to fp8 caches (torch's fp8 types or
-    raw uint8) holding K / k_scale and V / v_scale (the fp32 quotients, rounded).
+    raw uint8) holding K / k_scale and V / v_scale (the fp32 quotients, rounded), "e2m1"
+    to 4-bit caches (uint8 [blocks, heads, 9 * head size], layout "nhd", head sizes of
+    64 and 128; fp16 or bf16 rows): a scale for every 16 elements, which their largest
+    magnitude sets, and the nearest codes (include/pa_cache.h).
     """
     args = _pack_append(key, value, key_cache, value_cache, slots, layout, kv_dtype, k_scale, v_scale, dev_error)
     _call("pa_append_kv", args, stream, key.get_device())

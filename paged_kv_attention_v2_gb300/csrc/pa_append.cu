@@ -423,7 +423,8 @@ extern "C" pa_status pa_append_kv(const pa_append_args* a, void* stream) {
         return PA_ERR_INVALID_ARG;
     if (a->dtype != PA_DTYPE_F32 && a->dtype != PA_DTYPE_F16 && a->dtype != PA_DTYPE_BF16) return PA_ERR_INVALID_ARG;
     if (a->layout != PA_LAYOUT_SPLIT && a->layout != PA_LAYOUT_NHD) return PA_ERR_INVALID_ARG;
-    if (a->kv_dtype != PA_KV_SAME && a->kv_dtype != PA_KV_FP8_E4M3 && a->kv_dtype != PA_KV_FP8_E5M2)
+    if (a->kv_dtype != PA_KV_SAME && a->kv_dtype != PA_KV_FP8_E4M3 && a->kv_dtype != PA_KV_FP8_E5M2 &&
+        a->kv_dtype != PA_KV_FP4_E2M1)
         return PA_ERR_INVALID_ARG;
     if (!std::isfinite(a->k_scale) || !std::isfinite(a->v_scale)) return PA_ERR_INVALID_ARG;
     if (a->kv_dtype != PA_KV_SAME && a->dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;
@@ -431,6 +432,8 @@ extern "C" pa_status pa_append_kv(const pa_append_args* a, void* stream) {
     if (a->num_tokens > 1 << 30) return PA_ERR_UNSUPPORTED;  // rows rounded up to blocks in 32 bits
     if (!size_ok(a->key_head_size) || !size_ok(a->value_head_size)) return PA_ERR_UNSUPPORTED;
     if ((int64_t)a->num_key_heads + a->num_value_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (a->kv_dtype == PA_KV_FP4_E2M1 && (a->layout != PA_LAYOUT_NHD || a->key_head_size > 128 || a->value_head_size > 128))
+        return PA_ERR_UNSUPPORTED;
     if (a->num_tokens == 0) return PA_OK;
     if (!a->key || !a->value || !a->key_cache || !a->value_cache || !a->slots) return PA_ERR_INVALID_ARG;
     const int e = a->dtype == PA_DTYPE_F32 ? 4 : 2;
@@ -461,6 +464,7 @@ extern "C" pa_status pa_append_kv(const pa_append_args* a, void* stream) {
     p.v = scale_of(a->v_scale);
     if (!std::isfinite(p.k.inv) || !std::isfinite(p.v.inv)) return PA_ERR_INVALID_ARG;
     p.dev_error = a->dev_error;
+    if (a->kv_dtype == PA_KV_FP4_E2M1) return pa::append4(a, stream) ? PA_OK : PA_ERR_LAUNCH;
 
     bool ok;
     const int kv = a->kv_dtype;

@@ -224,6 +224,10 @@ pa_status dispatch(Prepared& pr, pa::LaunchOut* out) {
         }
         return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
     }
+    if (pr.kv == PA_KV_FP4_E2M1) {
+        e = pr.la.dtype == PA_DTYPE_F16 ? pa::launch_f16_fp4(pr.p, pr.la) : pa::launch_bf16_fp4(pr.p, pr.la);
+        return e == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    }
     switch (pr.la.dtype) {
     case PA_DTYPE_F32: e = pa::launch_f32(pr.p, pr.la); break;
     case PA_DTYPE_F16: e = pr.kv == PA_KV_SAME ? pa::launch_f16(pr.p, pr.la) : pa::launch_f16_fp8(pr.p, pr.la, kvk); break;
@@ -347,8 +351,10 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
         !std::isfinite(a->v_scale))
         return PA_ERR_INVALID_ARG;
     const int kv = a->kv_dtype;
-    if (kv != PA_KV_SAME && kv != PA_KV_FP8_E4M3 && kv != PA_KV_FP8_E5M2) return PA_ERR_INVALID_ARG;
+    if (kv != PA_KV_SAME && kv != PA_KV_FP8_E4M3 && kv != PA_KV_FP8_E5M2 && kv != PA_KV_FP4_E2M1) return PA_ERR_INVALID_ARG;
     if (kv != PA_KV_SAME && a->dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;
+    // 4-bit caches: one layout, no differential heads
+    if (kv == PA_KV_FP4_E2M1 && (df || a->layout != PA_LAYOUT_NHD)) return PA_ERR_UNSUPPORTED;
     if (a->block_size != PA_BLOCK_SIZE) return PA_ERR_UNSUPPORTED;
     if (a->head_size != 64 && a->head_size != 128) return PA_ERR_UNSUPPORTED;
     const int group = a->num_heads / a->num_kv_heads;
@@ -610,8 +616,8 @@ pa_status pa_decode(const pa_decode_args* a, void* stream) {
     Prepared pr;
     const pa_status st = prepare(a, stream, pr);
     if (st != PA_OK || pr.empty) return st;
-    // NHD pages come through tensor maps
-    if (a->layout == PA_LAYOUT_NHD) {
+    // NHD pages come through tensor maps (4-bit ones do not)
+    if (a->layout == PA_LAYOUT_NHD && pr.kv != PA_KV_FP4_E2M1) {
         const int64_t rows = (int64_t)a->num_blocks * a->num_kv_heads * PA_BLOCK_SIZE;
         if (rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;  // tensor-map row coordinate is int32
         const bool ok = pr.kv != PA_KV_SAME

@@ -8,7 +8,12 @@
 
 #include <atomic>
 
+#include "pa_cache.h"
+
 namespace pa {
+
+// pa_append_kv into 4-bit caches (pa_append4.cu), arguments checked; false: CUDA reported an error.
+bool append4(const pa_append_args* a, void* stream);
 
 constexpr int kHostDevices = 64;
 

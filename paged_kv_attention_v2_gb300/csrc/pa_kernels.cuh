@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "pa_decode.h"
+#include "pa_fp4.cuh"
 #include "pa_ptx.cuh"
 
 namespace pa {
@@ -38,6 +39,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKvSame = 0;      // same 16-bit / 32-bit type as the query
 constexpr int kKvE4M3 = 1;      // fp8 E4M3
 constexpr int kKvE5M2 = 2;      // fp8 E5M2
+constexpr int kKvE2M1 = 3;      // 4-bit E2M1, an E4M3 scale per 16 elements
 
 // Shape of the partition kernel.  Ring stages per cache type, one 16-token
 // page of K and V each.  One n-tile of 16-bit or fp32 pages: five consumer
@@ -49,6 +51,7 @@ constexpr int kKvE5M2 = 2;      // fp8 E5M2
 constexpr int kStages16 = 10;      // 16-bit caches, one n-tile
 constexpr int kStages16x2 = 10;    // 16-bit caches, two n-tiles (paired page streams)
 constexpr int kStagesFp8 = 12;     // fp8 caches (three CTAs per SM fit)
+constexpr int kStagesFp4 = 24;     // 4-bit caches
 constexpr int kStagesF32 = 5;      // fp32 caches, one n-tile (two CTAs per SM)
 constexpr int kStagesF32x2 = 8;    // fp32 caches, two n-tiles (one CTA per SM)
 constexpr int kStagesFp8x2Diff = 15; // fp8 caches, two n-tiles of a differential call (five warps)
@@ -219,7 +222,8 @@ struct Cfg {
     static constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
     static constexpr int kElem = sizeof(T);                // query / output element
     static constexpr int kKvElem = KV == kKvSame ? (int)sizeof(T) : 1;
-    static constexpr int kPageBytes = kBS * HEAD * kKvElem;  // one page of K (or of V)
+    static constexpr bool kFp4 = KV == kKvE2M1;  // codes of HEAD / 2 bytes a token, then scales of HEAD / 16
+    static constexpr int kPageBytes = kFp4 ? kBS * (HEAD / 2 + HEAD / 16) : kBS * HEAD * kKvElem;  // one page of K (or of V)
     // One page of K and one of V per ring stage.  (Two pages per fp8 NHD stage
     // halve its barrier rounds, max reductions and rescales, but their 8 KB
     // stages leave room for two CTAs per SM, against three with one-page
@@ -247,8 +251,10 @@ struct Cfg {
     static constexpr int kThreads = (NC + 1) * 32;
     // NHD pages arrive through tensor maps with the 128-byte swizzle (3-D for
     // 16-bit and fp32, 2-D for fp8)
-    static constexpr bool kTensorMap = LAYOUT == kNHD;
-    static_assert(KV == kKvSame || !kF32, "fp8 caches: 16-bit query");
+    // (4-bit pages are read in place by bulk copies)
+    static constexpr bool kTensorMap = LAYOUT == kNHD && !kFp4;
+    static_assert(KV == kKvSame || !kF32, "fp8 and 4-bit caches: 16-bit query");
+    static_assert(kPageBytes % 16 == 0, "bulk copy size");
 
     static constexpr int oRing = 0;
     static constexpr int oQ = oRing + STAGES * kStageBytes;
@@ -1756,6 +1762,287 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
     }
 }
 
+// Consumer for 4-bit caches.  Tensor-core inputs are fp16 for both query types, as in the
+// fp8 consumer, with code x block scale in fp16 (exact) and k_scale, v_scale folded
+// into the logit scale and the epilogue.
+//
+// A page is read as it lies in memory, without a transposition: the reduction index of an
+// MMA and the rows of its result may be in any order, and here they follow the page.
+//   Q.K^T  lane (r, cq) holds HEAD / 4 successive head dims of its tokens (rows r and r + 8),
+//          from HEAD cq / 4 on, so that it needs the scales of those blocks only; k-step j takes four
+//          of them from every lane, and the query's fragments are laid out the same way.
+//   P.V    row r of the m-tiles stands for HEAD / 8 successive head dims, from HEAD r / 8 on
+//          (m-tile mt: HEAD r / 8 + 2 mt in row r, the next one in row r + 8): for each of its four
+//          tokens a lane needs the one scale of that run.  The codes of two tokens are
+//          paired before they are converted, four instructions for sixteen of them.
+// Row i of S^T is token tau(i): rows 2q, 2q + 1 and 2q + 8, 2q + 9 are tokens 4q .. 4q + 3,
+// the first two and the last two in swapped order for odd q, so that the lanes of a value
+// load meet in both halves of the banks (two to a bank instead of four).
+template <class C, typename T, int HEAD, int NT, int STAGES, int NC>
+__device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int lane) {
+    constexpr bool QBF = C::kBF16;
+    constexpr int KT = HEAD / 16;
+    constexpr int KW = HEAD / 32;             // 32-bit words of codes a lane holds of a token's key
+    constexpr int VW = HEAD / 64;             // of a token's value
+    constexpr uint32_t kScales = kBS * HEAD / 2;  // where a page's scales begin
+    const int G = p.group;
+    const int r = lane >> 2, cq = lane & 3;
+    // tokens of S^T rows r and r + 8, and of this lane's value words
+    const int tlo = ((r >> 1) << 2) + ((r & 1) ^ (r >> 1 & 1)), thi = tlo + 2;
+    const int tv = (cq << 2) + (cq & 1), tv1 = (cq << 2) + (~cq & 1);  // k-indices 2cq, 2cq + 1 (+ 8: two tokens on)
+    const bool has_alibi = p.alibi != nullptr;
+    const bool has_cap = p.softcap > 0.f;
+    uint32_t gbase = 0;
+    uint32_t mphase = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k % C::kTD;
+        if (!warp_wait(sm.td_full + slot * 8, (k / C::kTD) & 1, sm.abort, sm.wait_ns)) {
+            report(p, PA_DEVERR_TIMEOUT);
+            *sm.abort = 1;
+            return;
+        }
+        const TileDesc d = sm.desc[slot];
+        if (d.flags & kTileStop) return;
+        const int qn = C::kMQ ? d.qn : 1;
+        const int GE = qn * G;  // rows of N: query token v / G, head kvh * G + v % G
+
+        // Q as fp16 B fragments: k-step j of lane cq is head dims HEAD cq / 4 + 4j .. + 3.
+        uint32_t qb[NT][KT][2];
+        bool q_clamped = false;
+        const uint32_t qs = sm.q + slot * C::kQBytes;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int v = nt * 8 + r;
+#pragma unroll
+            for (int j = 0; j < KT; ++j) {
+                uint32_t w0 = 0, w1 = 0;
+                if (v < GE) {
+                    const uint32_t a = qs + (uint32_t)((v * HEAD + cq * (HEAD / 4) + 4 * j) * 2);
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(a));
+                    if constexpr (QBF) {
+                        float2 f0 = unpack2<true>(w0), f1 = unpack2<true>(w1);
+                        const float lim = 65504.f;
+                        q_clamped |= fabsf(f0.x) > lim || fabsf(f0.y) > lim || fabsf(f1.x) > lim || fabsf(f1.y) > lim;
+                        w0 = pack2<false>(fminf(fmaxf(f0.x, -lim), lim), fminf(fmaxf(f0.y, -lim), lim));
+                        w1 = pack2<false>(fminf(fmaxf(f1.x, -lim), lim), fminf(fmaxf(f1.y, -lim), lim));
+                    }
+                }
+                qb[nt][j][0] = w0;
+                qb[nt][j][1] = w1;
+            }
+        }
+        if (q_clamped) report(p, PA_DEVERR_QUERY_RANGE);
+        const uint32_t qlast = last_query_word<C, KT>(qb[NT - 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);
+
+        float sl[NT][2];
+        int klo[NT][2], khi[NT][2];  // key range of each of this lane's rows (see consumer_mma_fp8)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = nt * 8 + 2 * cq + e;
+                sl[nt][e] = (has_alibi && v < GE) ? p.alibi[d.kvh * G + v % G] : 0.f;
+                int lo = d.tok_begin, hi = d.tok_end - 1;
+                if (C::kMQ && v < GE) {
+                    const int pos = d.len - qn + v / G;
+                    hi = min(hi, pos);
+                    lo = max(lo, window_lo_at(p, pos));
+                }
+                klo[nt][e] = lo;
+                khi[nt][e] = hi;
+            }
+        const int hi_all = C::kMQ ? min(d.tok_end - 1, d.len - qn) : d.tok_end - 1;
+        const int lo_all = C::kMQ ? max(d.tok_begin, window_lo_at(p, d.len - 1)) : d.tok_begin;
+        const int origin = d.tok_end - 1;
+
+        float m[NT][2], l[NT][2], mx[NT][2];  // reference max, sum, this lane's running max
+        float acc[KT][NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = mx[nt][0] = mx[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < KT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+        }
+
+        const int npages = tile_pages(d.tok_begin, d.tok_end);
+        const int page0 = d.tok_begin / kBS * kBS;
+        uint32_t st = (gbase + (uint32_t)warp) % STAGES, ph = ((gbase + (uint32_t)warp) / STAGES) & 1;
+        for (int j = warp; j < npages; j += NC, advance_stage<STAGES, NC>(st, ph)) {
+            if (!warp_wait(sm.full + st * 8, ph, sm.abort, sm.wait_ns)) {
+                report(p, PA_DEVERR_TIMEOUT);
+                *sm.abort = 1;
+                return;
+            }
+            const uint32_t kp = sm.ring + st * C::kStageBytes;
+            const uint32_t vp = kp + C::kPageBytes;
+            const int tok0 = page0 + j * kBS;
+            const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;  // some key masked
+
+            // the whole page to registers, and the stage back to the producer
+            uint32_t kw[2][KW], ks[2];   // rows r and r + 8
+            uint32_t vw[4][VW], vs[4];   // k-indices 2cq, 2cq + 1, 2cq + 8, 2cq + 9
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = h ? thi : tlo;
+                const uint32_t a = kp + (uint32_t)(t * (HEAD / 2) + cq * (HEAD / 8));
+                const uint32_t b = kp + kScales + (uint32_t)(t * (HEAD / 16) + cq * (HEAD / 64));
+                if constexpr (HEAD == 128) {
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(kw[h][0]), "=r"(kw[h][1]), "=r"(kw[h][2]), "=r"(kw[h][3])
+                                 : "r"(a));
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(ks[h]) : "r"(b));
+                } else {
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(kw[h][0]), "=r"(kw[h][1]) : "r"(a));
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ks[h]) : "r"(b));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = (i & 1 ? tv1 : tv) + (i >> 1) * 2;
+                const uint32_t a = vp + (uint32_t)(t * (HEAD / 2) + r * (HEAD / 16));
+                const uint32_t b = vp + kScales + (uint32_t)(t * (HEAD / 16) + (HEAD == 128 ? r : r >> 1));
+                if constexpr (HEAD == 128)
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(a));
+                else
+                    vw[i][0] = lds32(a);
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(vs[i]) : "r"(b));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vs[3], p.zero);
+
+            float s[NT][4], s2[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+            {
+                uint32_t f[2][2];  // scale pairs {s, s} of this lane's one or two blocks of each row
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t c = e4m3x2_to_f16(ks[h]);
+                    f[h][0] = __byte_perm(c, c, 0x1010);
+                    f[h][1] = HEAD == 128 ? __byte_perm(c, c, 0x3232) : f[h][0];
+                }
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    uint32_t x[4], y[4];
+                    e2m1x8_to_f16(kw[0][w], x);
+                    e2m1x8_to_f16(kw[1][w], y);
+                    const int b = HEAD == 128 ? w >> 1 : 0;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t a0 = hmul2(x[2 * u], f[0][b]), a1 = hmul2(y[2 * u], f[1][b]);
+                        const uint32_t a2 = hmul2(x[2 * u + 1], f[0][b]), a3 = hmul2(y[2 * u + 1], f[1][b]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t(&q)[2] = qb[nt][2 * w + u];
+                            if (u)
+                                mma_16816<false>(s2[nt], a0, a1, a2, a3, q[0], q[1]);
+                            else
+                                mma_16816<false>(s[nt], a0, a1, a2, a3, q[0], q[1]);
+                        }
+                    }
+                }
+            }
+
+            uint32_t pb[NT][2];
+            float z[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = (s[nt][e] + s2[nt][e]) * p.scale;
+                    if (has_cap) v = soft_cap<false>(p, v);
+                    if (has_alibi) v += sl[nt][e & 1] * (float)(tok0 + ((e >> 1) ? thi : tlo) - origin);
+                    z[nt][e] = v;
+                }
+                if (edge) {
+                    const int t0 = tok0 + tlo, t1 = tok0 + thi;
+                    if (t0 < klo[nt][0] || t0 > khi[nt][0]) z[nt][0] = -INFINITY;
+                    if (t0 < klo[nt][1] || t0 > khi[nt][1]) z[nt][1] = -INFINITY;
+                    if (t1 < klo[nt][0] || t1 > khi[nt][0]) z[nt][2] = -INFINITY;
+                    if (t1 < klo[nt][1] || t1 > khi[nt][1]) z[nt][3] = -INFINITY;
+                }
+            }
+            if (edge) {  // slots that no row of the tile sees may hold anything: a scale of zero (codes are finite)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = tok0 + (i & 1 ? tv1 : tv) + (i >> 1) * 2;
+                    if (t < d.tok_begin || t >= d.tok_end) vs[i] = 0;
+                }
+            }
+            softmax_page<NT, KT, C::kMQ>(z, m, mx, l, acc, edge);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                pb[nt][0] = movmatrix_trans(pack2<false>(z[nt][0], z[nt][1]));
+                pb[nt][1] = movmatrix_trans(pack2<false>(z[nt][2], z[nt][3]));
+            }
+
+            const uint32_t f01 = e4m3x2_to_f16(vs[0] | vs[1] << 8), f23 = e4m3x2_to_f16(vs[2] | vs[3] << 8);
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                uint32_t c01[2], c23[2];
+                pair_codes(vw[0][w], vw[1][w], c01[0], c01[1]);
+                pair_codes(vw[2][w], vw[3][w], c23[0], c23[1]);
+                uint32_t a0[4], a1[4], a2[4], a3[4];
+                e2m1x8_to_f16(c01[0], a0);  // head dim 2 mt of the run, tokens of k-indices 2cq, 2cq + 1
+                e2m1x8_to_f16(c01[1], a1);  // the next head dim
+                e2m1x8_to_f16(c23[0], a2);
+                e2m1x8_to_f16(c23[1], a3);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t b0 = hmul2(a0[u], f01), b1 = hmul2(a1[u], f01);
+                    const uint32_t b2 = hmul2(a2[u], f23), b3 = hmul2(a3[u], f23);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816<false>(acc[4 * w + u][nt], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+                }
+            }
+        }
+
+        settle_max<NT, KT>(m, mx, l, acc);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], o);
+                l[nt][1] += __shfl_xor_sync(0xffffffffu, l[nt][1], o);
+            }
+        }
+        float* mw = sm.merge + warp * C::kMergeRows * C::kMergeStride;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h0 = nt * 8 + 2 * cq;
+#pragma unroll
+            for (int mt = 0; mt < KT; ++mt) {
+                const int d0 = r * (HEAD / 8) + 2 * mt;
+                *reinterpret_cast<float2*>(mw + h0 * C::kMergeStride + d0) = make_float2(acc[mt][nt][0], acc[mt][nt][2]);
+                *reinterpret_cast<float2*>(mw + (h0 + 1) * C::kMergeStride + d0) = make_float2(acc[mt][nt][1], acc[mt][nt][3]);
+            }
+            if (r == 0) {
+                sm.ml[warp * C::kMergeRows + h0] = make_float2(m[nt][0], l[nt][0]);
+                sm.ml[warp * C::kMergeRows + h0 + 1] = make_float2(m[nt][1], l[nt][1]);
+            }
+        }
+        if (!consumer_sync(sm, mphase, lane)) {
+            report(p, PA_DEVERR_TIMEOUT);
+            *sm.abort = 1;
+            return;
+        }
+        if (!tile_finish<C, T, HEAD, NC>(p, d, sm, warp, lane, mphase)) {
+            report(p, PA_DEVERR_TIMEOUT);
+            *sm.abort = 1;
+            return;
+        }
+        gbase += (uint32_t)npages;
+    }
+}
+
 // fp32 inputs: tensor cores with each fp32 operand carried as two tf32 terms
 // (hi + lo) and three MMAs per product (hi.hi + hi.lo + lo.hi), which keeps
 // each product to ~2^-20 relative, well inside the fp32 result's error budget.
@@ -2431,6 +2718,8 @@ __global__ void __launch_bounds__((NC + 1) * 32,
     } else {
         if constexpr (KV == kKvSame)
             consumer_mma<C, T, HEAD, NT, LAYOUT, STAGES, NC>(p, sm, warp, lane);
+        else if constexpr (KV == kKvE2M1)
+            consumer_mma_fp4<C, T, HEAD, NT, STAGES, NC>(p, sm, warp, lane);
         else
             consumer_mma_fp8<C, T, HEAD, NT, LAYOUT, STAGES, NC, KV>(p, sm, warp, lane);
     }

@@ -53,6 +53,7 @@ cudaError_t launch_main(const Params& p_in, const LaunchArgs& la, bool* fused) {
                            : WIDE && KV != kKvSame ? (NT == 1 ? kStagesFp8Wide : kStagesFp8Widex2)
                            : WIDE         ? (NT == 1 ? kStages16Wide : kStages16Widex2)
                            : F32          ? (NT == 1 ? kStagesF32 : kStagesF32x2)
+                           : KV == kKvE2M1 ? kStagesFp4
                            : KV != kKvSame ? kStagesFp8
                                            : (NT == 1 ? kStages16 : kStages16x2);
     constexpr int NC = FP8X2         ? kConsumerWarps5
@@ -200,6 +201,23 @@ cudaError_t launch_family(const Params& p, const LaunchArgs& la) {
     return la.head_size == 128 ? launch_reduce<T, 128, false>(p, la) : launch_reduce<T, 64, false>(p, la);
 }
 
+// 4-bit caches: one layout.
+template <typename T, int HEAD, bool MQ>
+cudaError_t launch_fp4_head(const Params& p, const LaunchArgs& la) {
+    bool fused = false;
+    const cudaError_t e = la.group_tiles == 2 ? launch_main<T, HEAD, 2, kNHD, kKvE2M1, MQ>(p, la, &fused)
+                                              : launch_main<T, HEAD, 1, kNHD, kKvE2M1, MQ>(p, la, &fused);
+    if (e != cudaSuccess || p.v1 || fused || la.query) return e;
+    return launch_reduce<T, HEAD, MQ>(p, la);
+}
+
+template <typename T>
+cudaError_t launch_family_fp4(const Params& p, const LaunchArgs& la) {
+    if (la.head_size == 128)
+        return p.query_start ? launch_fp4_head<T, 128, true>(p, la) : launch_fp4_head<T, 128, false>(p, la);
+    return p.query_start ? launch_fp4_head<T, 64, true>(p, la) : launch_fp4_head<T, 64, false>(p, la);
+}
+
 // ---------------------------------------------------------------- differential
 //
 // Measured (GPU time per call, against the KV bytes at the copy rate of 6.8 TB/s):
@@ -270,5 +288,7 @@ cudaError_t launch_f16(const Params& p, const LaunchArgs& la);
 cudaError_t launch_bf16(const Params& p, const LaunchArgs& la);
 cudaError_t launch_f16_fp8(const Params& p, const LaunchArgs& la, int kv);   // kv: kKvE4M3 / kKvE5M2
 cudaError_t launch_bf16_fp8(const Params& p, const LaunchArgs& la, int kv);
+cudaError_t launch_f16_fp4(const Params& p, const LaunchArgs& la);
+cudaError_t launch_bf16_fp4(const Params& p, const LaunchArgs& la);
 
 }  // namespace pa

@@ -21,6 +21,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
     return h;
 }
 
+// A bf16x2 pair as f16x2, beyond 65504: that number.
+__device__ __forceinline__ uint32_t bf16x2_to_f16(uint32_t w) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(__uint_as_float(w & 0xffff0000u)), "f"(__uint_as_float(w << 16)));
+    return d;
+}
+
 // Products of f16x2 pairs (a code times a scale: at most six significant bits, between
 // 2^-10 and 2688, so exact).
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {

@@ -51,7 +51,8 @@ constexpr int kKvE2M1 = 3;      // 4-bit E2M1, an E4M3 scale per 16 elements
 constexpr int kStages16 = 10;      // 16-bit caches, one n-tile
 constexpr int kStages16x2 = 10;    // 16-bit caches, two n-tiles (paired page streams)
 constexpr int kStagesFp8 = 12;     // fp8 caches (three CTAs per SM fit)
-constexpr int kStagesFp4 = 24;     // 4-bit caches
+constexpr int kStagesFp4 = 16, kConsumerWarpsFp4 = 4, kCtasFp4 = 3;    // 4-bit caches, one n-tile
+constexpr int kStagesFp4x2 = 24, kConsumerWarpsFp4x2 = 4, kCtasFp4x2 = 2; // two n-tiles
 constexpr int kStagesF32 = 5;      // fp32 caches, one n-tile (two CTAs per SM)
 constexpr int kStagesF32x2 = 8;    // fp32 caches, two n-tiles (one CTA per SM)
 constexpr int kStagesFp8x2Diff = 15; // fp8 caches, two n-tiles of a differential call (five warps)
@@ -275,6 +276,9 @@ struct Cfg {
     // both warps of a pair released it.  Across tiles the tile-end barrier of
     // the consumer warps gives the same guarantee.
     static_assert(STAGES % (NC / kPageWarps) == 0, "ring stages must be a multiple of the page streams");
+    // (4-bit pages, one n-tile: two successive pages at a time go to a warp.)
+    static constexpr int kPagesAtOnce = kFp4 && NT == 1 ? 2 : 1;
+    static_assert(STAGES % (NC * kPagesAtOnce) == 0 || !kFp4, "ring stages must be a multiple of the pages of a round");
     static_assert(STAGES <= 32, "one producer lane per stage");
     static_assert(kQBytes % 16 == 0, "bulk copy size");
 };
@@ -983,6 +987,54 @@ __device__ __forceinline__ void softmax_page(float (&z)[NT][4], float (&m)[NT][2
         l[nt][0] += z[nt][0] + z[nt][2];
         l[nt][1] += z[nt][1] + z[nt][3];
     }
+}
+
+// The same for PP pages at once: one vote and at most one rescale for all of them.
+template <int PP, int NT, int KT, bool MQ>
+__device__ __forceinline__ void softmax_pages(float (&z)[PP][NT][4], float (&m)[NT][2], float (&mx)[NT][2], float (&l)[NT][2],
+                                              float (&acc)[KT][NT][4], bool edge) {
+    bool need = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float a = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+#pragma unroll
+            for (int g = 1; g < PP; ++g) a = fmaxf(a, fmaxf(z[g][nt][e], z[g][nt][e + 2]));
+            mx[nt][e] = fmaxf(mx[nt][e], a);
+            need |= a - m[nt][e] > kLazyMax;  // -inf - -inf: false
+        }
+    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mn = mx[nt][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                const float mr = (MQ && mn == -INFINITY) ? 0.f : mn;  // (see softmax_page)
+                const float al = exp2f((m[nt][e] - mr) * kLog2e);
+                m[nt][e] = mn;
+                l[nt][e] *= al;
+#pragma unroll
+                for (int mt = 0; mt < KT; ++mt) {
+                    acc[mt][nt][e] *= al;
+                    acc[mt][nt][e + 2] *= al;
+                }
+            }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float mr = (MQ && edge && m[nt][e] == -INFINITY) ? 0.f : m[nt][e];
+#pragma unroll
+            for (int g = 0; g < PP; ++g) {
+                z[g][nt][e] = exp2f((z[g][nt][e] - mr) * kLog2e);
+                z[g][nt][e + 2] = exp2f((z[g][nt][e + 2] - mr) * kLog2e);
+                l[nt][e] += z[g][nt][e] + z[g][nt][e + 2];
+            }
+        }
 }
 
 // End of a warp's pages of a tile: move the reference of each head to the
@@ -1808,7 +1860,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
 
         // Q as fp16 B fragments: k-step j of lane cq is head dims HEAD cq / 4 + 4j .. + 3.
         uint32_t qb[NT][KT][2];
-        bool q_clamped = false;
+        uint32_t q_top = 0;  // bf16: largest magnitudes, as 16-bit patterns
         const uint32_t qs = sm.q + slot * C::kQBytes;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -1820,18 +1872,17 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                     const uint32_t a = qs + (uint32_t)((v * HEAD + cq * (HEAD / 4) + 4 * j) * 2);
                     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(a));
                     if constexpr (QBF) {
-                        float2 f0 = unpack2<true>(w0), f1 = unpack2<true>(w1);
-                        const float lim = 65504.f;
-                        q_clamped |= fabsf(f0.x) > lim || fabsf(f0.y) > lim || fabsf(f1.x) > lim || fabsf(f1.y) > lim;
-                        w0 = pack2<false>(fminf(fmaxf(f0.x, -lim), lim), fminf(fmaxf(f0.y, -lim), lim));
-                        w1 = pack2<false>(fminf(fmaxf(f1.x, -lim), lim), fminf(fmaxf(f1.y, -lim), lim));
+                        q_top = __vmaxu2(q_top, __vmaxu2(w0 & 0x7fff7fffu, w1 & 0x7fff7fffu));
+                        w0 = bf16x2_to_f16(w0);
+                        w1 = bf16x2_to_f16(w1);
                     }
                 }
                 qb[nt][j][0] = w0;
                 qb[nt][j][1] = w1;
             }
         }
-        if (q_clamped) report(p, PA_DEVERR_QUERY_RANGE);
+        // beyond 65504 (the largest bf16 number below 65536 is 65280), clamped; a NaN stays one
+        if (QBF && ((q_top & 0xffffu) - 0x4780u < 0x3801u || (q_top >> 16) - 0x4780u < 0x3801u)) report(p, PA_DEVERR_QUERY_RANGE);
         const uint32_t qlast = last_query_word<C, KT>(qb[NT - 1]);
         __syncwarp();
         if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);
@@ -1871,136 +1922,159 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
 
         const int npages = tile_pages(d.tok_begin, d.tok_end);
         const int page0 = d.tok_begin / kBS * kBS;
-        uint32_t st = (gbase + (uint32_t)warp) % STAGES, ph = ((gbase + (uint32_t)warp) / STAGES) & 1;
-        for (int j = warp; j < npages; j += NC, advance_stage<STAGES, NC>(st, ph)) {
-            if (!warp_wait(sm.full + st * 8, ph, sm.abort, sm.wait_ns)) {
-                report(p, PA_DEVERR_TIMEOUT);
-                *sm.abort = 1;
-                return;
-            }
-            const uint32_t kp = sm.ring + st * C::kStageBytes;
-            const uint32_t vp = kp + C::kPageBytes;
+        constexpr int PP = C::kPagesAtOnce;  // successive pages of this warp, worked on together
+        uint32_t st = (gbase + (uint32_t)(warp * PP)) % STAGES, ph = ((gbase + (uint32_t)(warp * PP)) / STAGES) & 1;
+        for (int j = warp * PP; j < npages; j += NC * PP, advance_stage<STAGES, NC * PP>(st, ph)) {
             const int tok0 = page0 + j * kBS;
-            const bool edge = tok0 < lo_all || tok0 + kBS - 1 > hi_all;  // some key masked
+            const bool edge = tok0 < lo_all || tok0 + PP * kBS - 1 > hi_all;  // some key masked
 
-            // the whole page to registers, and the stage back to the producer
-            uint32_t kw[2][KW], ks[2];   // rows r and r + 8
-            uint32_t vw[4][VW], vs[4];   // k-indices 2cq, 2cq + 1, 2cq + 8, 2cq + 9
+            // the whole pages to registers, and the stages back to the producer
+            uint32_t kw[PP][2][KW], ks[PP][2];   // rows r and r + 8
+            uint32_t vw[PP][4][VW], vs[PP][4];   // k-indices 2cq, 2cq + 1, 2cq + 8, 2cq + 9
+            uint32_t sp = st, pp = ph;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = h ? thi : tlo;
-                const uint32_t a = kp + (uint32_t)(t * (HEAD / 2) + cq * (HEAD / 8));
-                const uint32_t b = kp + kScales + (uint32_t)(t * (HEAD / 16) + cq * (HEAD / 64));
-                if constexpr (HEAD == 128) {
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(kw[h][0]), "=r"(kw[h][1]), "=r"(kw[h][2]), "=r"(kw[h][3])
-                                 : "r"(a));
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(ks[h]) : "r"(b));
-                } else {
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(kw[h][0]), "=r"(kw[h][1]) : "r"(a));
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ks[h]) : "r"(b));
+            for (int g = 0; g < PP; ++g) {
+                // the tile's last page may have no partner: it stands in for it, all of it masked
+                if (g > 0 && j + g < npages) {
+                    sp = sp + 1 == STAGES ? 0 : sp + 1;
+                    pp ^= sp == 0;
+                }
+                if (!warp_wait(sm.full + sp * 8, pp, sm.abort, sm.wait_ns)) {
+                    report(p, PA_DEVERR_TIMEOUT);
+                    *sm.abort = 1;
+                    return;
+                }
+                const uint32_t kp = sm.ring + sp * C::kStageBytes;
+                const uint32_t vp = kp + C::kPageBytes;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = h ? thi : tlo;
+                    const uint32_t a = kp + (uint32_t)(t * (HEAD / 2) + cq * (HEAD / 8));
+                    const uint32_t b = kp + kScales + (uint32_t)(t * (HEAD / 16) + cq * (HEAD / 64));
+                    if constexpr (HEAD == 128) {
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(kw[g][h][0]), "=r"(kw[g][h][1]), "=r"(kw[g][h][2]), "=r"(kw[g][h][3])
+                                     : "r"(a));
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(ks[g][h]) : "r"(b));
+                    } else {
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(kw[g][h][0]), "=r"(kw[g][h][1]) : "r"(a));
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ks[g][h]) : "r"(b));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = (i & 1 ? tv1 : tv) + (i >> 1) * 2;
+                    const uint32_t a = vp + (uint32_t)(t * (HEAD / 2) + r * (HEAD / 16));
+                    const uint32_t b = vp + kScales + (uint32_t)(t * (HEAD / 16) + (HEAD == 128 ? r : r >> 1));
+                    if constexpr (HEAD == 128)
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[g][i][0]), "=r"(vw[g][i][1]) : "r"(a));
+                    else
+                        vw[g][i][0] = lds32(a);
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(vs[g][i]) : "r"(b));
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = (i & 1 ? tv1 : tv) + (i >> 1) * 2;
-                const uint32_t a = vp + (uint32_t)(t * (HEAD / 2) + r * (HEAD / 16));
-                const uint32_t b = vp + kScales + (uint32_t)(t * (HEAD / 16) + (HEAD == 128 ? r : r >> 1));
-                if constexpr (HEAD == 128)
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(a));
-                else
-                    vw[i][0] = lds32(a);
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(vs[i]) : "r"(b));
-            }
             __syncwarp();
-            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vs[3], p.zero);
+            if (lane == 0) {
+                mbar_arrive_after(sm.empty + st * 8, vs[PP - 1][3], p.zero);
+                if (sp != st) mbar_arrive_after(sm.empty + sp * 8, vs[PP - 1][3], p.zero);
+            }
 
-            float s[NT][4], s2[NT][4];
+            float z[PP][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int g = 0; g < PP; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-            {
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[g][nt][e] = 0.f;
+#pragma unroll
+            for (int g = 0; g < PP; ++g) {
                 uint32_t f[2][2];  // scale pairs {s, s} of this lane's one or two blocks of each row
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t c = e4m3x2_to_f16(ks[h]);
+                    const uint32_t c = e4m3x2_to_f16(ks[g][h]);
                     f[h][0] = __byte_perm(c, c, 0x1010);
                     f[h][1] = HEAD == 128 ? __byte_perm(c, c, 0x3232) : f[h][0];
                 }
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
                     uint32_t x[4], y[4];
-                    e2m1x8_to_f16(kw[0][w], x);
-                    e2m1x8_to_f16(kw[1][w], y);
+                    e2m1x8_to_f16(kw[g][0][w], x);
+                    e2m1x8_to_f16(kw[g][1][w], y);
                     const int b = HEAD == 128 ? w >> 1 : 0;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const uint32_t a0 = hmul2(x[2 * u], f[0][b]), a1 = hmul2(y[2 * u], f[1][b]);
                         const uint32_t a2 = hmul2(x[2 * u + 1], f[0][b]), a3 = hmul2(y[2 * u + 1], f[1][b]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint32_t(&q)[2] = qb[nt][2 * w + u];
-                            if (u)
-                                mma_16816<false>(s2[nt], a0, a1, a2, a3, q[0], q[1]);
-                            else
-                                mma_16816<false>(s[nt], a0, a1, a2, a3, q[0], q[1]);
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_16816<false>(z[g][nt], a0, a1, a2, a3, qb[nt][2 * w + u][0], qb[nt][2 * w + u][1]);
                     }
                 }
             }
-
-            uint32_t pb[NT][2];
-            float z[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int g = 0; g < PP; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = (s[nt][e] + s2[nt][e]) * p.scale;
-                    if (has_cap) v = soft_cap<false>(p, v);
-                    if (has_alibi) v += sl[nt][e & 1] * (float)(tok0 + ((e >> 1) ? thi : tlo) - origin);
-                    z[nt][e] = v;
-                }
-                if (edge) {
-                    const int t0 = tok0 + tlo, t1 = tok0 + thi;
-                    if (t0 < klo[nt][0] || t0 > khi[nt][0]) z[nt][0] = -INFINITY;
-                    if (t0 < klo[nt][1] || t0 > khi[nt][1]) z[nt][1] = -INFINITY;
-                    if (t1 < klo[nt][0] || t1 > khi[nt][0]) z[nt][2] = -INFINITY;
-                    if (t1 < klo[nt][1] || t1 > khi[nt][1]) z[nt][3] = -INFINITY;
-                }
-            }
-            if (edge) {  // slots that no row of the tile sees may hold anything: a scale of zero (codes are finite)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = tok0 + (i & 1 ? tv1 : tv) + (i >> 1) * 2;
-                    if (t < d.tok_begin || t >= d.tok_end) vs[i] = 0;
-                }
-            }
-            softmax_page<NT, KT, C::kMQ>(z, m, mx, l, acc, edge);
+                    for (int e = 0; e < 4; ++e) z[g][nt][e] *= p.scale;
+            if (has_cap || has_alibi) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                pb[nt][0] = movmatrix_trans(pack2<false>(z[nt][0], z[nt][1]));
-                pb[nt][1] = movmatrix_trans(pack2<false>(z[nt][2], z[nt][3]));
-            }
-
-            const uint32_t f01 = e4m3x2_to_f16(vs[0] | vs[1] << 8), f23 = e4m3x2_to_f16(vs[2] | vs[3] << 8);
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-                uint32_t c01[2], c23[2];
-                pair_codes(vw[0][w], vw[1][w], c01[0], c01[1]);
-                pair_codes(vw[2][w], vw[3][w], c23[0], c23[1]);
-                uint32_t a0[4], a1[4], a2[4], a3[4];
-                e2m1x8_to_f16(c01[0], a0);  // head dim 2 mt of the run, tokens of k-indices 2cq, 2cq + 1
-                e2m1x8_to_f16(c01[1], a1);  // the next head dim
-                e2m1x8_to_f16(c23[0], a2);
-                e2m1x8_to_f16(c23[1], a3);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t b0 = hmul2(a0[u], f01), b1 = hmul2(a1[u], f01);
-                    const uint32_t b2 = hmul2(a2[u], f23), b3 = hmul2(a3[u], f23);
+                for (int g = 0; g < PP; ++g)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma_16816<false>(acc[4 * w + u][nt], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (has_cap) z[g][nt][e] = soft_cap<false>(p, z[g][nt][e]);
+                            if (has_alibi) z[g][nt][e] += sl[nt][e & 1] * (float)(tok0 + g * kBS + ((e >> 1) ? thi : tlo) - origin);
+                        }
+            }
+            if (edge) {
+#pragma unroll
+                for (int g = 0; g < PP; ++g) {
+                    const int t0 = tok0 + g * kBS + tlo, t1 = tok0 + g * kBS + thi;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (t0 < klo[nt][0] || t0 > khi[nt][0]) z[g][nt][0] = -INFINITY;
+                        if (t0 < klo[nt][1] || t0 > khi[nt][1]) z[g][nt][1] = -INFINITY;
+                        if (t1 < klo[nt][0] || t1 > khi[nt][0]) z[g][nt][2] = -INFINITY;
+                        if (t1 < klo[nt][1] || t1 > khi[nt][1]) z[g][nt][3] = -INFINITY;
+                    }
+                    // slots that no row of the tile sees may hold anything: a scale of zero (codes are finite)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = tok0 + g * kBS + (i & 1 ? tv1 : tv) + (i >> 1) * 2;
+                        if (t < d.tok_begin || t >= d.tok_end) vs[g][i] = 0;
+                    }
+                }
+            }
+            softmax_pages<PP, NT, KT, C::kMQ>(z, m, mx, l, acc, edge);
+#pragma unroll
+            for (int g = 0; g < PP; ++g) {
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    pb[nt][0] = movmatrix_trans(pack2<false>(z[g][nt][0], z[g][nt][1]));
+                    pb[nt][1] = movmatrix_trans(pack2<false>(z[g][nt][2], z[g][nt][3]));
+                }
+                const uint32_t f01 = e4m3x2_to_f16(vs[g][0] | vs[g][1] << 8), f23 = e4m3x2_to_f16(vs[g][2] | vs[g][3] << 8);
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    uint32_t c01[2], c23[2];
+                    pair_codes(vw[g][0][w], vw[g][1][w], c01[0], c01[1]);
+                    pair_codes(vw[g][2][w], vw[g][3][w], c23[0], c23[1]);
+                    uint32_t a0[4], a1[4], a2[4], a3[4];
+                    e2m1x8_to_f16(c01[0], a0);  // head dim 2 mt of the run, tokens of k-indices 2cq, 2cq + 1
+                    e2m1x8_to_f16(c01[1], a1);  // the next head dim
+                    e2m1x8_to_f16(c23[0], a2);
+                    e2m1x8_to_f16(c23[1], a3);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t b0 = hmul2(a0[u], f01), b1 = hmul2(a1[u], f01);
+                        const uint32_t b2 = hmul2(a2[u], f23), b3 = hmul2(a3[u], f23);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_16816<false>(acc[4 * w + u][nt], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+                    }
                 }
             }
         }
@@ -2647,7 +2721,8 @@ __device__ void consumer_fma(const Params& p, const Smem& sm, int warp, int lane
 // Value heads of 256 hold one CTA per SM.
 template <typename T, int HEAD, int NT, int LAYOUT, int STAGES, int NC, int KV, bool MQ, bool DIFF>
 __global__ void __launch_bounds__((NC + 1) * 32,
-                                  (HEAD > 128 || (std::is_same<T, float>::value && NT > 1))
+                                  KV == kKvE2M1 ? (NT == 1 ? kCtasFp4 : kCtasFp4x2)
+                                  : (HEAD > 128 || (std::is_same<T, float>::value && NT > 1))
                                       ? 1
                                       : ((NT > 1 || std::is_same<T, float>::value) ? 2 : (KV != kKvSame ? 3 : 1)))
     pa_partition_kernel(const Params p, const __grid_constant__ CUtensorMap tmk,

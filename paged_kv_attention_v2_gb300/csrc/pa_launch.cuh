@@ -53,13 +53,14 @@ cudaError_t launch_main(const Params& p_in, const LaunchArgs& la, bool* fused) {
                            : WIDE && KV != kKvSame ? (NT == 1 ? kStagesFp8Wide : kStagesFp8Widex2)
                            : WIDE         ? (NT == 1 ? kStages16Wide : kStages16Widex2)
                            : F32          ? (NT == 1 ? kStagesF32 : kStagesF32x2)
-                           : KV == kKvE2M1 ? kStagesFp4
+                           : KV == kKvE2M1 ? (NT == 1 ? kStagesFp4 : kStagesFp4x2)
                            : KV != kKvSame ? kStagesFp8
                                            : (NT == 1 ? kStages16 : kStages16x2);
     constexpr int NC = FP8X2         ? kConsumerWarps5
                        : F32X2       ? kConsumerWarpsF32x2Diff
                        : WIDE && F32 ? (NT == 1 ? kConsumerWarpsF32Wide : kConsumerWarpsF32Widex2)
                        : WIDE && KV != kKvSame ? (NT == 1 ? kConsumerWarpsFp8Wide : kConsumerWarpsFp8Widex2)
+                       : KV == kKvE2M1 ? (NT == 1 ? kConsumerWarpsFp4 : kConsumerWarpsFp4x2)
                        : WIDE ? (NT == 1 ? kConsumerWarps16Wide : kConsumerWarps16Widex2)
                               : ((KV == kKvSame && NT == 1) ? kConsumerWarps5 : kConsumerWarps);
     using C = Cfg<T, HEAD, NT, LAYOUT, STAGES, NC, KV, MQ, DIFF>;

@@ -28,6 +28,7 @@ __all__ = ["pa_decode", "pa_decode_static_workspace", "alloc_workspace", "max_nu
 _LAYOUTS = {"split": _abi.PA_LAYOUT_SPLIT, "nhd": _abi.PA_LAYOUT_NHD}
 _MODES = {"auto": _abi.PA_MODE_AUTO, "v1": _abi.PA_MODE_V1, "v2": _abi.PA_MODE_V2}
 _KV = {None: _abi.PA_KV_SAME, "e4m3": _abi.PA_KV_FP8_E4M3, "e5m2": _abi.PA_KV_FP8_E5M2, "e2m1": _abi.PA_KV_FP4_E2M1}
+_DECODE = _abi.packer(_abi.PaDecodeArgs)
 
 
 class PaDecodeError(RuntimeError):
@@ -87,12 +88,6 @@ def plan_for(out, query, key_cache, value_cache, block_tables, seq_lens, **kw) -
         return plan(args)
 
 
-def _dtype_code(t):
-    import torch
-    return {torch.float32: _abi.PA_DTYPE_F32, torch.float16: _abi.PA_DTYPE_F16,
-            torch.bfloat16: _abi.PA_DTYPE_BF16}[t.dtype]
-
-
 def alloc_workspace(num_seqs: int, num_heads: int, head_size: int, max_seq_len: int, device,
                     num_kv_heads: int | None = None, num_query_tokens: int | None = None,
                     tile_counters: bool = False):
@@ -119,7 +114,58 @@ def alloc_workspace(num_seqs: int, num_heads: int, head_size: int, max_seq_len: 
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
+
+
+def _pack(out, query, key_cache, value_cache, block_tables, seq_lens, num_kv_heads, scale, max_seq_len,
+          block_size=PA_BLOCK_SIZE, alibi_slopes=None, softcap=0.0, layout="split", mode="auto", exp_sums=None,
+          max_logits=None, tmp_out=None, dev_error=None, event_begin=None, event_end=None, partition_counters=None,
+          window_left=-1, kv_dtype=None, k_scale=1.0, v_scale=1.0, query_start=None, max_query_len=None,
+          seq_lens_host=None, tile_counters=None, metadata_ready=False):
+    """The packed argument struct, and the host lengths that its pointer needs alive."""
+    num_rows, num_heads, head_size = query.shape
+    num_seqs = seq_lens.shape[0]
+    if out.shape != query.shape:
+        raise ValueError(f"out shape {tuple(out.shape)} != query shape {tuple(query.shape)}")
+    if query_start is None:
+        if num_rows != num_seqs:
+            raise ValueError(f"query has {num_rows} rows for {num_seqs} sequences")
+    else:
+        if max_query_len is None:
+            raise ValueError("max_query_len is required with query_start")
+        if query_start.dtype.itemsize != 4 or query_start.numel() != num_seqs + 1:
+            raise ValueError("query_start must be int32 [num_seqs + 1]")
+    num_blocks = key_cache.shape[0]
+    kv_bytes = query.element_size() if kv_dtype is None else 1
+    page = num_kv_heads * block_size * head_size  # elements of one block of one cache
+    if kv_dtype == "e2m1":  # bytes: half of one for each element, one for every 16
+        page = num_kv_heads * 9 * head_size
+    for name, c in (("key_cache", key_cache), ("value_cache", value_cache)):
+        if c.element_size() != kv_bytes:
+            raise ValueError(f"{name} has {c.element_size()}-byte elements, kv_dtype "
+                             f"{kv_dtype or 'same as query'} needs {kv_bytes}")
+        if c.numel() != num_blocks * page:
+            raise ValueError(f"{name} holds {c.numel()} elements, expected "
+                             f"num_blocks {num_blocks} x {page}")
+    host_lens = None
+    if seq_lens_host is not None:
+        import numpy as np
+        src = seq_lens_host.numpy() if hasattr(seq_lens_host, "numpy") else seq_lens_host
+        host_lens = np.ascontiguousarray(src, dtype=np.int32)
+        if host_lens.shape != (num_seqs,):
+            raise ValueError("seq_lens_host must hold num_seqs lengths")
+    several = query_start is not None
+    return _DECODE.pack(
+        out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), num_seqs, num_heads, num_kv_heads, head_size, num_blocks, block_size, max_seq_len,
+        block_tables.shape[1] if block_tables.dim() == 2 else 0, scale, softcap, _ptr(alibi_slopes),
+        _DTYPES[query.dtype], _LAYOUTS[layout], _MODES[mode], _ptr(exp_sums), _ptr(max_logits), _ptr(tmp_out),
+        _ptr(dev_error), 0 if event_begin is None else event_begin.cuda_event,
+        0 if event_end is None else event_end.cuda_event, _ptr(partition_counters),
+        int(window_left) + 1 if window_left >= 0 else 0, _KV[kv_dtype], k_scale, v_scale, _ptr(query_start),
+        num_rows if several else 0, int(max_query_len) if several else 0,
+        0 if host_lens is None else host_lens.__array_interface__["data"][0], _ptr(tile_counters),
+        1 if metadata_ready else 0), host_lens
 
 
 def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: int,
@@ -150,58 +196,24 @@ def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num
     the dynamic tile schedule.  metadata_ready promises that no earlier kernel
     in the stream writes block_tables, seq_lens or query_start (the kernel may
     read them before it waits for that kernel)."""
-    num_rows, num_heads, head_size = query.shape
-    num_seqs = seq_lens.shape[0]
-    if tuple(out.shape) != tuple(query.shape):
-        raise ValueError(f"out shape {tuple(out.shape)} != query shape {tuple(query.shape)}")
-    if query_start is None:
-        if num_rows != num_seqs:
-            raise ValueError(f"query has {num_rows} rows for {num_seqs} sequences")
-    else:
-        if max_query_len is None:
-            raise ValueError("max_query_len is required with query_start")
-        if query_start.dtype.itemsize != 4 or query_start.numel() != num_seqs + 1:
-            raise ValueError("query_start must be int32 [num_seqs + 1]")
-    num_blocks = key_cache.shape[0]
-    kv_bytes = query.element_size() if kv_dtype is None else 1
-    page = num_kv_heads * block_size * head_size  # elements of one block of one cache
-    if kv_dtype == "e2m1":  # bytes: half of one for each element, one for every 16
-        page = num_kv_heads * 9 * head_size
-    for name, c in (("key_cache", key_cache), ("value_cache", value_cache)):
-        if c.element_size() != kv_bytes:
-            raise ValueError(f"{name} has {c.element_size()}-byte elements, kv_dtype "
-                             f"{kv_dtype or 'same as query'} needs {kv_bytes}")
-        if c.numel() != num_blocks * page:
-            raise ValueError(f"{name} holds {c.numel()} elements, expected "
-                             f"num_blocks {num_blocks} x {page}")
-    host_lens = None
-    if seq_lens_host is not None:
-        import numpy as np
-        src = seq_lens_host.numpy() if hasattr(seq_lens_host, "numpy") else seq_lens_host
-        host_lens = np.ascontiguousarray(np.asarray(src, dtype=np.int32))
-        if host_lens.shape != (num_seqs,):
-            raise ValueError("seq_lens_host must hold num_seqs lengths")
-    a = _abi.PaDecodeArgs(
-        out=_ptr(out), query=_ptr(query), key_cache=_ptr(key_cache),
-        value_cache=_ptr(value_cache), block_tables=_ptr(block_tables), seq_lens=_ptr(seq_lens),
-        num_seqs=num_seqs, num_heads=num_heads, num_kv_heads=num_kv_heads, head_size=head_size,
-        num_blocks=num_blocks, block_size=block_size, max_seq_len=max_seq_len,
-        max_blocks_per_seq=block_tables.shape[1] if block_tables.dim() == 2 else 0,
-        scale=scale, softcap=softcap, alibi_slopes=_ptr(alibi_slopes), dtype=_dtype_code(query),
-        layout=_LAYOUTS[layout], mode=_MODES[mode], exp_sums=_ptr(exp_sums),
-        max_logits=_ptr(max_logits), tmp_out=_ptr(tmp_out), dev_error=_ptr(dev_error),
-        event_main_begin=None if event_begin is None else event_begin.cuda_event,
-        event_main_end=None if event_end is None else event_end.cuda_event,
-        partition_counters=_ptr(partition_counters),
-        sliding_window=int(window_left) + 1 if window_left >= 0 else 0,
-        kv_dtype=_KV[kv_dtype], k_scale=float(k_scale), v_scale=float(v_scale),
-        query_start=_ptr(query_start), num_query_tokens=num_rows if query_start is not None else 0,
-        max_query_len=int(max_query_len) if query_start is not None else 0,
-        seq_lens_host=None if host_lens is None else host_lens.ctypes.data,
-        tile_counters=_ptr(tile_counters), metadata_ready=1 if metadata_ready else 0,
-    )
-    a._keep_host_lens = host_lens  # the pointer above stays valid as long as the struct lives
+    packed, host_lens = _pack(
+        out, query, key_cache, value_cache, block_tables, seq_lens, num_kv_heads, scale, max_seq_len, block_size,
+        alibi_slopes, softcap, layout, mode, exp_sums, max_logits, tmp_out, dev_error, event_begin, event_end,
+        partition_counters, window_left, kv_dtype, k_scale, v_scale, query_start, max_query_len, seq_lens_host,
+        tile_counters, metadata_ready)
+    a = _abi.PaDecodeArgs.from_buffer_copy(packed)
+    a._keep_host_lens = host_lens  # the pointer inside stays valid as long as the struct lives
     return a
+
+
+def _launch(name: str, tensors, kw, stream) -> None:
+    """Call `name` on the packed arguments, with the tensors' device current (the library
+    sizes its grid for, and caches attributes of, the current device)."""
+    for t in tensors:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} needs contiguous tensors")
+    packed, _host = _pack(*tensors, **kw)
+    _call(name, packed, stream, tensors[1].get_device())
 
 
 def pa_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *, stream=None,
@@ -215,19 +227,7 @@ def pa_decode(out, query, key_cache, value_cache, block_tables, seq_lens, *, str
     [num_heads] fp32, v2 workspace from alloc_workspace().  Raises PaDecodeError
     with the library's status on failure.
     """
-    import torch
-    for t in (out, query, key_cache, value_cache, block_tables, seq_lens):
-        if not t.is_contiguous():
-            raise ValueError("pa_decode needs contiguous tensors")
-    args = make_args(out, query, key_cache, value_cache, block_tables, seq_lens, **kw)
-    if stream is None:
-        stream = torch.cuda.current_stream(query.device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    # the library sizes its grid for (and caches attributes of) the current device
-    with torch.cuda.device(query.device):
-        st = library().pa_decode(ctypes.byref(args), ctypes.c_void_p(handle))
-    if st != _abi.PA_OK:
-        raise PaDecodeError(st)
+    _launch("pa_decode", (out, query, key_cache, value_cache, block_tables, seq_lens), kw, stream)
 
 
 def decode_args_call(args: _abi.PaDecodeArgs, stream_handle: int) -> int:
@@ -241,20 +241,8 @@ def pa_decode_static_workspace(out, query, key_cache, value_cache, block_tables,
     array, for callers that cannot allocate device memory (see the C header).
     Workspace arguments and `mode` are ignored.  Raises PaDecodeError, e.g.
     PA_ERR_WORKSPACE when the batch needs more than PA_STATIC_WORKSPACE_FLOATS."""
-    import torch
-    for t in (out, query, key_cache, value_cache, block_tables, seq_lens):
-        if not t.is_contiguous():
-            raise ValueError("pa_decode_static_workspace needs contiguous tensors")
-    args = make_args(out, query, key_cache, value_cache, block_tables, seq_lens, **kw)
-    if stream is None:
-        stream = torch.cuda.current_stream(query.device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    # the array used is the current device's: make the tensors' device current
-    with torch.cuda.device(query.device):
-        st = library().pa_decode_static_workspace(ctypes.byref(args), ctypes.c_void_p(handle))
-    if st != _abi.PA_OK:
-        raise PaDecodeError(st)
+    _launch("pa_decode_static_workspace", (out, query, key_cache, value_cache, block_tables, seq_lens), kw, stream)
 
 
-from .cache import pa_append_kv, pa_build_tables  # noqa: E402
+from .cache import _call, _DTYPE as _DTYPES, pa_append_kv, pa_build_tables  # noqa: E402
 from .diff import alloc_diff_workspace, diff_plan, pa_diff_decode  # noqa: E402

@@ -193,7 +193,8 @@ def load(path: Path | None = None):
             f"{p} is missing: build it with `python -m paged_kv_attention_v2_gb300.build` "
             "(or __graft_entry__.build()); there is no fallback implementation")
     lib = ctypes.CDLL(str(p))
-    lib.pa_decode.argtypes = [ctypes.POINTER(PaDecodeArgs), ctypes.c_void_p]
+    # argument structs come as structures (byref) or as packed bytes
+    lib.pa_decode.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.pa_decode.restype = ctypes.c_int
     lib.pa_max_num_partitions.argtypes = [ctypes.c_int32]
     lib.pa_max_num_partitions.restype = ctypes.c_int32
@@ -210,13 +211,12 @@ def load(path: Path | None = None):
     lib.pa_status_str.argtypes = [ctypes.c_int32]
     lib.pa_status_str.restype = ctypes.c_char_p
     lib.pa_version.restype = ctypes.c_int32
-    lib.pa_decode_static_workspace.argtypes = [ctypes.POINTER(PaDecodeArgs), ctypes.c_void_p]
+    lib.pa_decode_static_workspace.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.pa_decode_static_workspace.restype = ctypes.c_int
     lib.pa_plan.argtypes = [ctypes.POINTER(PaDecodeArgs), ctypes.POINTER(PaLaunchPlan)]
     lib.pa_plan.restype = ctypes.c_int
     lib.pa_debug_withhold_page.argtypes = [ctypes.c_int32, ctypes.c_int64]
     lib.pa_debug_withhold_page.restype = ctypes.c_int
-    # argument structs of these come as structures (byref) or as packed bytes
     lib.pa_diff_decode.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.pa_diff_decode.restype = ctypes.c_int
     lib.pa_diff_plan.argtypes = [ctypes.POINTER(PaDiffArgs), ctypes.POINTER(PaLaunchPlan)]

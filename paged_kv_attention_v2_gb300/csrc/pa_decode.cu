@@ -146,6 +146,21 @@ bool make_nhd_map_fp8(CUtensorMap* map, const void* base, int64_t rows, int head
     return r == CUDA_SUCCESS;
 }
 
+// 4-bit cache: pages of one head as rows, of which a copy gathers four.
+bool make_fp4_map(CUtensorMap* map, const void* base, int64_t pages, int head_size) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t bytes = 9 * (cuuint64_t)head_size;
+    cuuint64_t dims[2] = {bytes / 8, (cuuint64_t)pages};
+    cuuint64_t strides[1] = {bytes};
+    cuuint32_t box[2] = {(cuuint32_t)(bytes / 8), 1};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
 // Test hook of pa_debug_withhold_page (process-wide).
@@ -616,8 +631,14 @@ pa_status pa_decode(const pa_decode_args* a, void* stream) {
     Prepared pr;
     const pa_status st = prepare(a, stream, pr);
     if (st != PA_OK || pr.empty) return st;
-    // NHD pages come through tensor maps (4-bit ones do not)
-    if (a->layout == PA_LAYOUT_NHD && pr.kv != PA_KV_FP4_E2M1) {
+    // NHD pages come through tensor maps
+    if (pr.kv == PA_KV_FP4_E2M1) {
+        const int64_t pages = (int64_t)a->num_blocks * a->num_kv_heads;
+        if (pages > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+        if (!make_fp4_map(&pr.tmk, a->key_cache, pages, a->head_size) ||
+            !make_fp4_map(&pr.tmv, a->value_cache, pages, a->head_size))
+            return PA_ERR_LAUNCH;
+    } else if (a->layout == PA_LAYOUT_NHD) {
         const int64_t rows = (int64_t)a->num_blocks * a->num_kv_heads * PA_BLOCK_SIZE;
         if (rows > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;  // tensor-map row coordinate is int32
         const bool ok = pr.kv != PA_KV_SAME

@@ -51,8 +51,8 @@ constexpr int kKvE2M1 = 3;      // 4-bit E2M1, an E4M3 scale per 16 elements
 constexpr int kStages16 = 10;      // 16-bit caches, one n-tile
 constexpr int kStages16x2 = 10;    // 16-bit caches, two n-tiles (paired page streams)
 constexpr int kStagesFp8 = 12;     // fp8 caches (three CTAs per SM fit)
-constexpr int kStagesFp4 = 16, kConsumerWarpsFp4 = 4, kCtasFp4 = 3;    // 4-bit caches, one n-tile
-constexpr int kStagesFp4x2 = 24, kConsumerWarpsFp4x2 = 4, kCtasFp4x2 = 2; // two n-tiles
+constexpr int kStagesFp4 = 4, kConsumerWarpsFp4 = 4, kCtasFp4 = 3;     // 4-bit caches, one n-tile; four pages a stage
+constexpr int kStagesFp4x2 = 6, kConsumerWarpsFp4x2 = 4, kCtasFp4x2 = 2;  // two n-tiles
 constexpr int kStagesF32 = 5;      // fp32 caches, one n-tile (two CTAs per SM)
 constexpr int kStagesF32x2 = 8;    // fp32 caches, two n-tiles (one CTA per SM)
 constexpr int kStagesFp8x2Diff = 15; // fp8 caches, two n-tiles of a differential call (five warps)
@@ -230,7 +230,11 @@ struct Cfg {
     // stages leave room for two CTAs per SM, against three with one-page
     // stages: measured, long100k_fp8 NHD 83.1 -> 75.9 µs and gqa4k_fp8 NHD
     // 34.2 -> 32.7 µs for the one-page stages.)
-    static constexpr int kStageBytes = 2 * kPageBytes;  // K page, then V page
+    // 4-bit pages come four at a time (one gather of four rows for K, one for V): issuing a bulk copy costs the
+    // producer the same whatever its size, and for pages of 1152 bytes that bound the stream (32 x 4096 with
+    // nothing done to the pages: 26 us, of 11 for the bytes).
+    static constexpr int kStagePages = kFp4 ? 4 : 1;
+    static constexpr int kStageBytes = 2 * kStagePages * kPageBytes;  // K page, then V page
     static constexpr int kMaxG = NT * 8;                   // MMA columns: rows (heads x query tokens) handled
     // 16-bit caches with two n-tiles, and differential kernels with two but fp8
     // ones of value heads of 128: warps in pairs of page streams, one n-tile each;
@@ -239,7 +243,9 @@ struct Cfg {
     // 4096 e4m3 with four tokens 65 -> 57 us, both with one term of P.)
     static constexpr bool kPairs = NT == 2 && (DIFF ? (KV == kKvSame || HEAD > 128) : (KV == kKvSame && !kF32));
     static constexpr int kMergeRows = kPairs ? 8 : kMaxG;  // merge-buffer rows per warp
-    static constexpr int kPageWarps = kPairs ? 2 : 1;      // warps that release each page
+    static constexpr int kPagesAtOnce = kFp4 && NT == 1 ? 2 : 1;  // 4-bit pages, one n-tile: two successive pages to a warp
+    static constexpr int kPageWarps = kPairs ? 2 : 1;      // warps that work on each page
+    static constexpr int kStageWarps = kFp4 ? kStagePages / kPagesAtOnce : kPageWarps;  // warps that release each stage
     // Differential fp32: K and V of a stage have barriers of their own.  A warp
     // holds its stage through a page's whole work, and there are no more stages
     // than warps: the key half is refilled while P.V runs, the value half during
@@ -248,12 +254,16 @@ struct Cfg {
     static constexpr bool kHalves = DIFF && kF32;
     static constexpr int kQBytes = kRows * HEAD * kElem;
     static constexpr int kTD = 2;                          // tile descriptor ring depth
-    static constexpr int kMergeStride = HEAD + 4;          // floats; +4 breaks bank conflicts
+    // 4-bit pages: a warp's stores go to eight runs of HEAD / 8 columns, four floats further apart than
+    // those are long (fewer bank conflicts).
+    static constexpr int kRun = HEAD / 8, kRunPad = kFp4 ? 4 : 0;
+    static constexpr int merge_col(int d) { return d + d / kRun * kRunPad; }
+    static constexpr int kMergeStride = HEAD + 8 * kRunPad + 4;  // floats; +4 breaks bank conflicts
     static constexpr int kThreads = (NC + 1) * 32;
     // NHD pages arrive through tensor maps with the 128-byte swizzle (3-D for
     // 16-bit and fp32, 2-D for fp8)
-    // (4-bit pages are read in place by bulk copies)
-    static constexpr bool kTensorMap = LAYOUT == kNHD && !kFp4;
+    // (4-bit: without a swizzle, pages as rows of a 2-D tensor)
+    static constexpr bool kTensorMap = LAYOUT == kNHD;
     static_assert(KV == kKvSame || !kF32, "fp8 and 4-bit caches: 16-bit query");
     static_assert(kPageBytes % 16 == 0, "bulk copy size");
 
@@ -266,7 +276,8 @@ struct Cfg {
     static constexpr int oAbort = oBar + ((kHalves ? 4 : 2) * STAGES + 2 * kTD + 1) * 8;
     static constexpr int kSmemBytes = oAbort + 16 + 1024;  // + slack for 1024-B alignment
 
-    static_assert(kPageBytes % 1024 == 0 || !kTensorMap, "swizzled pages need 1024-B alignment");
+    static_assert(kPageBytes % 1024 == 0 || !kTensorMap || kFp4, "swizzled pages need 1024-B alignment");
+    static_assert(kStagePages * kPageBytes % 128 == 0, "tensor copies need 128-B alignment");
     // Within a tile, page j goes to page stream j % (NC / kPageWarps) (one
     // warp, or two with paired streams, each releasing it) and to ring stage
     // (base + j) % STAGES.  With STAGES a multiple of the streams every page of
@@ -275,10 +286,8 @@ struct Cfg {
     // cannot tell phase n from phase n + 2): the stage is refilled only once
     // both warps of a pair released it.  Across tiles the tile-end barrier of
     // the consumer warps gives the same guarantee.
-    static_assert(STAGES % (NC / kPageWarps) == 0, "ring stages must be a multiple of the page streams");
-    // (4-bit pages, one n-tile: two successive pages at a time go to a warp.)
-    static constexpr int kPagesAtOnce = kFp4 && NT == 1 ? 2 : 1;
-    static_assert(STAGES % (NC * kPagesAtOnce) == 0 || !kFp4, "ring stages must be a multiple of the pages of a round");
+    static_assert(kFp4 || STAGES % (NC / kPageWarps) == 0, "ring stages must be a multiple of the page streams");
+    static_assert(!kFp4 || (NC % kStageWarps == 0 && STAGES % (NC / kStageWarps) == 0), "4-bit: of the stages of a round of the warps");
     static_assert(STAGES <= 32, "one producer lane per stage");
     static_assert(kQBytes % 16 == 0, "bulk copy size");
 };
@@ -548,10 +557,48 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
         for (int pc = 0; pc < cur.npages && ok; pc += 32) {
             const int n = min(32, cur.npages - pc);
             int ids_next = 0;  // block ids of the next 32 pages (this tile or the next one)
+            auto load_next = [&]() {
+                if (pc + 32 < cur.npages) {
+                    ids_next = load_ids(cur, pc + 32);
+                } else {
+                    if (!have_nxt) {
+                        nxt = next_tile();
+                        have_nxt = true;
+                    }
+                    ids_next = load_ids(nxt, 0);
+                }
+            };
+            if constexpr (C::kFp4) {
+                // Two stages of four pages at a time, one a lane.  A tile's last page stands in for those that
+                // its last stage lacks.
+                const int nq = (n + 3) / 4;
+                for (int q0 = 0; q0 < nq && ok; q0 += 2) {
+                    const int nb = min(2, nq - q0);
+                    int y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i] = __shfl_sync(0xffffffffu, ids, min(4 * (q0 + lane) + i, n - 1)) * Hkv + cur.kvh;
+                    bool lok = true;
+                    if (lane < nb) {
+                        const uint32_t gg = g + (uint32_t)lane;
+                        const uint32_t st = gg % STAGES, ph = (gg / STAGES) & 1;
+                        lok = mbar_wait(sm.empty + st * 8, ph ^ 1, sm.abort, sm.wait_ns);
+                        if (lok && !(p.withhold_page && blockIdx.x == 0 && gg == 0)) {  // (test hook)
+                            const uint32_t fb = sm.full + st * 8, dk = sm.ring + st * C::kStageBytes;
+                            mbar_arrive_expect_tx(fb, C::kStageBytes);
+                            gather4_g2s_hint(dk, tmk, y[0], y[1], y[2], y[3], fb, kvpol);
+                            gather4_g2s_hint(dk + C::kStageBytes / 2, tmv, y[0], y[1], y[2], y[3], fb, kvpol);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, lok);
+                    g += (uint32_t)nb;
+                    if (q0 == 0) load_next();  // first copies out: load the next ids while they stream
+                }
+            }
             // Issue in batches of up to STAGES pages, one stage per lane: the
             // stages of a batch are distinct, so each lane waits for exactly the
             // previous use of its own stage.
-            for (int b0 = 0; b0 < n && ok; b0 += STAGES) {
+            for (int b0 = 0; !C::kFp4 && b0 < n && ok; b0 += STAGES) {
                 const int nb = min(STAGES, n - b0);
                 const int blk = __shfl_sync(0xffffffffu, ids, (b0 + lane) & 31);
                 bool lok = true;
@@ -616,17 +663,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* tmk
                     ok = __all_sync(0xffffffffu, lok);
                 }
                 g += (uint32_t)nb;
-                if (b0 == 0) {  // first batch out: load the next ids while the rest streams
-                    if (pc + 32 < cur.npages) {
-                        ids_next = load_ids(cur, pc + 32);
-                    } else {
-                        if (!have_nxt) {
-                            nxt = next_tile();
-                            have_nxt = true;
-                        }
-                        ids_next = load_ids(nxt, 0);
-                    }
-                }
+                if (b0 == 0) load_next();  // first batch out: load the next ids while the rest streams
             }
             ids = check_ids(ids_next);
         }
@@ -804,7 +841,7 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
             if (idx < n) {
                 e[it][w] = sm.ml[(w0 + w) * C::kMergeRows + hl];
                 a[it][w] = *reinterpret_cast<const float4*>(
-                    sm.merge + ((w0 + w) * C::kMergeRows + hl) * C::kMergeStride + 4 * d4);
+                    sm.merge + ((w0 + w) * C::kMergeRows + hl) * C::kMergeStride + C::merge_col(4 * d4));
             } else {
                 e[it][w] = make_float2(-INFINITY, 0.f);
                 a[it][w] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1922,30 +1959,33 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
 
         const int npages = tile_pages(d.tok_begin, d.tok_end);
         const int page0 = d.tok_begin / kBS * kBS;
-        constexpr int PP = C::kPagesAtOnce;  // successive pages of this warp, worked on together
-        uint32_t st = (gbase + (uint32_t)(warp * PP)) % STAGES, ph = ((gbase + (uint32_t)(warp * PP)) / STAGES) & 1;
-        for (int j = warp * PP; j < npages; j += NC * PP, advance_stage<STAGES, NC * PP>(st, ph)) {
+        constexpr int PP = C::kPagesAtOnce;      // successive pages of this warp, worked on together
+        constexpr int PER = C::kStageWarps;      // warps to a stage
+        const int nstages = (npages + C::kStagePages - 1) / C::kStagePages;
+        uint32_t st = (gbase + (uint32_t)(warp / PER)) % STAGES, ph = ((gbase + (uint32_t)(warp / PER)) / STAGES) & 1;
+        for (int q = warp / PER; q < nstages; q += NC / PER, advance_stage<STAGES, NC / PER>(st, ph)) {
+            const int first = warp % PER * PP, j = q * C::kStagePages + first;  // this warp's pages of the stage, and of the tile
             const int tok0 = page0 + j * kBS;
             const bool edge = tok0 < lo_all || tok0 + PP * kBS - 1 > hi_all;  // some key masked
+            if (!warp_wait(sm.full + st * 8, ph, sm.abort, sm.wait_ns)) {
+                report(p, PA_DEVERR_TIMEOUT);
+                *sm.abort = 1;
+                return;
+            }
+            if (j >= npages) {  // the tile's last stage may have none for this warp
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sm.empty + st * 8);
+                continue;
+            }
 
-            // the whole pages to registers, and the stages back to the producer
+            // the whole pages to registers, and the stage back to the producer (a page that the tile's last stage
+            // lacks is another one in its place, all of it masked)
             uint32_t kw[PP][2][KW], ks[PP][2];   // rows r and r + 8
             uint32_t vw[PP][4][VW], vs[PP][4];   // k-indices 2cq, 2cq + 1, 2cq + 8, 2cq + 9
-            uint32_t sp = st, pp = ph;
 #pragma unroll
             for (int g = 0; g < PP; ++g) {
-                // the tile's last page may have no partner: it stands in for it, all of it masked
-                if (g > 0 && j + g < npages) {
-                    sp = sp + 1 == STAGES ? 0 : sp + 1;
-                    pp ^= sp == 0;
-                }
-                if (!warp_wait(sm.full + sp * 8, pp, sm.abort, sm.wait_ns)) {
-                    report(p, PA_DEVERR_TIMEOUT);
-                    *sm.abort = 1;
-                    return;
-                }
-                const uint32_t kp = sm.ring + sp * C::kStageBytes;
-                const uint32_t vp = kp + C::kPageBytes;
+                const uint32_t kp = sm.ring + st * C::kStageBytes + (first + g) * C::kPageBytes;
+                const uint32_t vp = kp + C::kStageBytes / 2;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int t = h ? thi : tlo;
@@ -1974,10 +2014,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                 }
             }
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive_after(sm.empty + st * 8, vs[PP - 1][3], p.zero);
-                if (sp != st) mbar_arrive_after(sm.empty + sp * 8, vs[PP - 1][3], p.zero);
-            }
+            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vs[PP - 1][3], p.zero);
 
             float z[PP][NT][4];
 #pragma unroll
@@ -2094,7 +2131,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
             const int h0 = nt * 8 + 2 * cq;
 #pragma unroll
             for (int mt = 0; mt < KT; ++mt) {
-                const int d0 = r * (HEAD / 8) + 2 * mt;
+                const int d0 = C::merge_col(r * (HEAD / 8) + 2 * mt);
                 *reinterpret_cast<float2*>(mw + h0 * C::kMergeStride + d0) = make_float2(acc[mt][nt][0], acc[mt][nt][2]);
                 *reinterpret_cast<float2*>(mw + (h0 + 1) * C::kMergeStride + d0) = make_float2(acc[mt][nt][1], acc[mt][nt][3]);
             }
@@ -2113,7 +2150,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
             *sm.abort = 1;
             return;
         }
-        gbase += (uint32_t)npages;
+        gbase += (uint32_t)nstages;
     }
 }
 
@@ -2754,7 +2791,7 @@ __global__ void __launch_bounds__((NC + 1) * 32,
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(sm.full + s * 8, 1);
-            mbar_init(sm.empty + s * 8, C::kPageWarps);
+            mbar_init(sm.empty + s * 8, C::kStageWarps);
             if constexpr (C::kHalves) {
                 mbar_init(sm.full_v + s * 8, 1);
                 mbar_init(sm.empty_v + s * 8, C::kPageWarps);

@@ -139,6 +139,17 @@ __device__ __forceinline__ void tensor4d_g2s_hint(uint32_t dst, const CUtensorMa
         : "memory");
 }
 
+// Four rows (y0 .. y3) of a 2-D tensor at column 0, one after the other in shared memory, through a
+// tensor map whose box is one row; completing on an mbarrier, with an L2 cache policy.
+__device__ __forceinline__ void gather4_g2s_hint(uint32_t dst, const CUtensorMap* map, int y0, int y1, int y2, int y3,
+                                                 uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar), "l"(pol)
+        : "memory");
+}
+
 // Bulk prefetch of global memory into L2 (a hint: no completion, no data
 // returned).  src 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {

@@ -90,8 +90,12 @@ cudaError_t launch_main(const Params& p_in, const LaunchArgs& la, bool* fused) {
     // The dynamic schedule keeps every resident CTA: its tiles go to whichever
     // CTA is free, so no CTA waits on a fixed share.
     if (!p_in.tile_ctr) {
-        const int64_t rounds = (la.tiles_upper + grid - 1) / grid;
-        grid = (la.tiles_upper + rounds - 1) / rounds;
+        const int64_t rounds = (la.tiles_upper + grid - 1) / grid, cut = (la.tiles_upper + rounds - 1) / rounds;
+        // 4-bit caches: bound by the SMs' issue slots, not by a CTA's stream.  The CTAs of an SM share those, so
+        // what counts is the tiles of the busiest SM; a cut that leaves some SMs a CTA more than others
+        // can raise them (1024 tiles: 342 CTAs x 3, nine on some SMs; 456 CTAs: seven).
+        const int64_t sms = la.sm_count;
+        if (KV != kKvE2M1 || (cut + sms - 1) / sms * rounds <= (la.tiles_upper + sms - 1) / sms) grid = cut;
     }
     Params p = p_in;
     p.fused = (!p.v1 && p.counters && p.max_parts <= PA_FUSED_MAX_PARTITIONS &&

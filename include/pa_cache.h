@@ -128,6 +128,126 @@ typedef struct pa_append_args {
 /* num_tokens == 0 is a no-op. */
 pa_status pa_append_kv(const pa_append_args* args, void* stream);
 
+/*
+ * A cache that is short of room: the tokens that attention has used least go.  Between two
+ * decode steps,
+ *     pa_add_weights     query, keys, statistics of the decode -> a score of every token
+ *     pa_select_tokens   scores, budgets                       -> which tokens stay
+ *     pa_compact_kv      those                                 -> cache pages without the others
+ *     pa_build_tables    with keep_lens = the new lengths: their pages go back to the pool
+ * Scores are fp32, [num_blocks][num_kv_heads][16]: a page of them for every page of the
+ * cache, found through the same block tables, and each kv head keeps tokens of its own.
+ */
+
+/*
+ * Adds to the score of every token the attention weights that it had in a decode:
+ *     scores(t, kv head) = decay * scores(t, kv head) + sum over the kv head's query heads h and
+ *                          the sequence's query tokens of softmax(z)(t),
+ * with the logits z of pa_decode (scale, softcap, alibi_slopes, sliding_window,
+ * query_start as there).  exp_sums and max_logits are the statistics that pa_decode left in
+ * PA_MODE_V2 for the same arguments (v1 leaves none), in the same shapes.  The tokens of this step, the
+ * last query_start[s+1] - query_start[s] of the sequence (without query_start the last one),
+ * are set to their weights and not added to, so a slot's former score does not matter; decay 0
+ * sets every token (the scores of a prompt, by its last tokens).  Tokens outside the window
+ * only fade.  Sums are fp32, in an order that does not depend on the run.  Places behind a
+ * sequence's end keep their scores; a page whose block id is out of range is skipped
+ * (PA_DEVERR_BLOCK_ID).
+ */
+typedef struct pa_weights_args {
+    float* scores;               /* [num_blocks][num_kv_heads][16], updated in place */
+    const void* query;           /* [rows][num_heads][head_size], dtype; 16-byte aligned */
+    const void* key_cache;       /* as pa_decode */
+    const int32_t* block_tables; /* [num_seqs][max_blocks_per_seq] */
+    const int32_t* seq_lens;     /* [num_seqs], in [0, max_seq_len]; this step's tokens among them */
+    const float* exp_sums;       /* [rows][num_heads][pa_max_num_partitions(max_seq_len)] */
+    const float* max_logits;
+    const float* alibi_slopes;   /* [num_heads] or NULL */
+    const int32_t* query_start;  /* [num_seqs + 1] or NULL */
+    int32_t* dev_error;          /* optional: PA_DEVERR_* bits */
+    int32_t num_seqs;
+    int32_t num_heads, num_kv_heads; /* max_query_len * (num_heads / num_kv_heads) <= 16 */
+    int32_t head_size;           /* 64 or 128 */
+    int32_t num_blocks;
+    int32_t block_size;          /* must be PA_BLOCK_SIZE */
+    int32_t max_seq_len;         /* as the decode had it, at most 2^30 */
+    int32_t max_blocks_per_seq;
+    int32_t num_query_tokens, max_query_len; /* with query_start */
+    int32_t sliding_window;      /* as pa_decode: 0 = off */
+    int32_t dtype;               /* pa_dtype of the query */
+    int32_t layout;              /* pa_layout */
+    int32_t kv_dtype;            /* pa_kv_dtype */
+    float scale, softcap, k_scale;
+    float decay;                 /* >= 0; 1: plain sums */
+} pa_weights_args;
+
+/* num_seqs == 0 or max_seq_len == 0 is a no-op. */
+pa_status pa_add_weights(const pa_weights_args* args, void* stream);
+
+/*
+ * The tokens that stay: of the n = seq_lens[s] tokens of sequence s, for each kv head,
+ * new_seq_lens[s] = min(n, budgets[s]) of them, namely the last `recent`, the first `sink`
+ * (both as far as the budget goes, the last ones first) and of the others those with the
+ * largest scores (of equal ones the lower position; a NaN counts as less than any number).
+ * kept[s][kv head][i], i < new_seq_lens[s], are their positions in ascending order; places behind
+ * stay as they were.  n <= budgets[s]: all of them.  A length or budget outside its range is
+ * clamped and reported (PA_DEVERR_SEQ_LEN); the scores of a page whose block id is out of
+ * range (PA_DEVERR_BLOCK_ID) count as NaN.
+ */
+typedef struct pa_select_args {
+    int32_t* kept;               /* [num_seqs][num_kv_heads][max_budget] */
+    int32_t* new_seq_lens;       /* [num_seqs] */
+    const float* scores;         /* [num_blocks][num_kv_heads][16] */
+    const int32_t* block_tables; /* [num_seqs][max_blocks_per_seq] */
+    const int32_t* seq_lens;     /* [num_seqs], in [0, max_seq_len]; not new_seq_lens itself */
+    const int32_t* budgets;      /* [num_seqs], in [0, max_budget] */
+    int32_t* dev_error;          /* optional: PA_DEVERR_* bits */
+    int32_t num_seqs, num_kv_heads, num_blocks;
+    int32_t block_size;          /* must be PA_BLOCK_SIZE */
+    int32_t max_seq_len;         /* at most 2^30 */
+    int32_t max_blocks_per_seq;
+    int32_t max_budget;          /* at most 2^30 */
+    int32_t sink, recent;        /* >= 0 */
+} pa_select_args;
+
+/* num_seqs == 0 is a no-op. */
+pa_status pa_select_tokens(const pa_select_args* args, void* stream);
+
+/*
+ * Moves the tokens kept[s][kv head][i], i < new_seq_lens[s], to position i of their sequence, in the
+ * pages that it has: keys, values and scores, in place and bit by bit.  The positions of a row
+ * ascend strictly, so that kept[i] >= i and nothing is overwritten before it has moved; an
+ * entry that does not (or whose page is out of range: PA_DEVERR_BLOCK_ID) is not moved
+ * (PA_DEVERR_SLOT), and what its place and its row's later ones then hold is some token's old
+ * or new contents.  Slots from new_seq_lens[s] on keep their bytes.  The block tables are not
+ * changed: pages that no token is left in go back with pa_build_tables (keep_lens =
+ * new_seq_lens).
+ *
+ * Caches as in pa_append_kv; num_key_heads and num_value_heads are multiples of
+ * num_kv_heads, whose row of `kept` key head h follows: h / (num_key_heads / num_kv_heads), and
+ * value heads likewise (differential caches: two key heads to each value head).
+ */
+typedef struct pa_compact_args {
+    void* key_cache;             /* 16-byte aligned */
+    void* value_cache;
+    float* scores;               /* [num_blocks][num_kv_heads][16] or NULL */
+    const int32_t* block_tables; /* [num_seqs][max_blocks_per_seq] */
+    const int32_t* kept;         /* [num_seqs][num_kv_heads][max_budget] */
+    const int32_t* new_seq_lens; /* [num_seqs], in [0, max_budget] */
+    int32_t* dev_error;          /* optional: PA_DEVERR_* bits */
+    int32_t num_seqs, num_kv_heads, max_budget; /* max_budget at most 2^30 */
+    int32_t num_key_heads, key_head_size; /* head sizes: 64, 128 or 256 (4-bit: not 256) */
+    int32_t num_value_heads, value_head_size;
+    int32_t num_blocks;          /* below 2^27 */
+    int32_t block_size;          /* must be PA_BLOCK_SIZE */
+    int32_t max_blocks_per_seq;  /* max_budget <= 16 * max_blocks_per_seq */
+    int32_t dtype;               /* pa_dtype of the caches with kv_dtype PA_KV_SAME */
+    int32_t layout;              /* pa_layout */
+    int32_t kv_dtype;            /* pa_kv_dtype */
+} pa_compact_args;
+
+/* num_seqs == 0 or max_budget == 0 is a no-op. */
+pa_status pa_compact_kv(const pa_compact_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

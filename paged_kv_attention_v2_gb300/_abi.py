@@ -39,7 +39,8 @@ PA_BLOCK_SIZE = 16
 EXPORTED = ("pa_decode", "pa_max_num_partitions", "pa_workspace_elems", "pa_choose_mode",
             "pa_choose_mode_for_lengths", "pa_workspace_bytes", "pa_partition_size", "pa_plan",
             "pa_status_str", "pa_version", "pa_decode_static_workspace", "pa_debug_withhold_page",
-            "pa_build_tables", "pa_append_kv", "pa_diff_decode", "pa_diff_plan")
+            "pa_build_tables", "pa_append_kv", "pa_diff_decode", "pa_diff_plan",
+            "pa_add_weights", "pa_select_tokens", "pa_compact_kv")
 
 PA_STATIC_WORKSPACE_FLOATS = 4 * 1024 * 1024
 PA_FUSED_MAX_PARTITIONS = 8
@@ -162,6 +163,85 @@ class PaAppendArgs(ctypes.Structure):
     ]
 
 
+class PaWeightsArgs(ctypes.Structure):
+    _fields_ = [
+        ("scores", ctypes.c_void_p),
+        ("query", ctypes.c_void_p),
+        ("key_cache", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("exp_sums", ctypes.c_void_p),
+        ("max_logits", ctypes.c_void_p),
+        ("alibi_slopes", ctypes.c_void_p),
+        ("query_start", ctypes.c_void_p),
+        ("dev_error", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("num_query_tokens", ctypes.c_int32),
+        ("max_query_len", ctypes.c_int32),
+        ("sliding_window", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("k_scale", ctypes.c_float),
+        ("decay", ctypes.c_float),
+    ]
+
+
+class PaSelectArgs(ctypes.Structure):
+    _fields_ = [
+        ("kept", ctypes.c_void_p),
+        ("new_seq_lens", ctypes.c_void_p),
+        ("scores", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("budgets", ctypes.c_void_p),
+        ("dev_error", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("max_budget", ctypes.c_int32),
+        ("sink", ctypes.c_int32),
+        ("recent", ctypes.c_int32),
+    ]
+
+
+class PaCompactArgs(ctypes.Structure):
+    _fields_ = [
+        ("key_cache", ctypes.c_void_p),
+        ("value_cache", ctypes.c_void_p),
+        ("scores", ctypes.c_void_p),
+        ("block_tables", ctypes.c_void_p),
+        ("kept", ctypes.c_void_p),
+        ("new_seq_lens", ctypes.c_void_p),
+        ("dev_error", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("max_budget", ctypes.c_int32),
+        ("num_key_heads", ctypes.c_int32),
+        ("key_head_size", ctypes.c_int32),
+        ("num_value_heads", ctypes.c_int32),
+        ("value_head_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+    ]
+
+
 _CODES = {ctypes.c_void_p: "P", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f"}
 
 
@@ -225,6 +305,9 @@ def load(path: Path | None = None):
     lib.pa_build_tables.restype = ctypes.c_int
     lib.pa_append_kv.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.pa_append_kv.restype = ctypes.c_int
+    for fn in (lib.pa_add_weights, lib.pa_select_tokens, lib.pa_compact_kv):
+        fn.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+        fn.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib

@@ -1,0 +1,235 @@
+// pa_compact.cu -- pa_compact_kv: the tokens that stay move to the front of their sequence's
+// pages, in place.
+//
+// Bound by memory: every token that moves is read once and written once.  As kept[i] >= i and
+// ascending, the place of token i of the result holds nothing that token i or a later one
+// still needs but itself, so a chain of chunks is safe in place when the loads of a chunk
+// come before its stores: a CTA loads a chunk of 256 tokens into registers, waits at a barrier
+// and stores it, with the next chunk's loads already on their way.  No CTA waits for another:
+// what makes enough chains of few long sequences is that the pieces of a head do not depend on
+// each other: 64 bytes of a token's row (NHD), four of the 16-byte pieces of split keys, or 16 head
+// dims of split values each make a chain of their own.
+// Which way lanes run follows the layout: along a token's row, or along the tokens where a page holds
+// [piece][token]; there successive tokens that stay are neighbours in the page, and a load takes
+// few sectors.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "pa_cache.h"
+#include "pa_host.cuh"
+#include "pa_ptx.cuh"
+
+namespace {
+
+constexpr int kBS = PA_BLOCK_SIZE;
+constexpr int kThreads = 256;
+constexpr int kChunk = kThreads;  // tokens at once
+constexpr int kAhead = 4;         // chunks whose places are in shared memory (see move_chain)
+
+// One array of the cache, in atoms: atom a of a token's head is at page + a * atom_step + token * token_step.
+struct Array {
+    uint8_t* base;
+    int64_t block_bytes;  // from a block to the next
+    int head_bytes;       // from a head's page to the next
+    int heads;            // heads to a kv head
+    int token_step, atom_step;
+    int chains;           // per head
+    int kind;             // kRow4 ..
+};
+
+enum { kRow4 = 0, kRow2, kPiece, kWide, kHalf, kByte, kWord8, kWord4 };
+
+struct CompactParams {
+    Array arrays[5];  // keys, values, 4-bit scales of both, scores
+    int first[6];     // chains of a kv head before each array's
+    const int32_t* block_tables;
+    const int32_t* kept;
+    const int32_t* new_seq_lens;
+    int32_t* dev_error;
+    int num_seqs, num_kv_heads, max_budget, num_blocks, max_blocks_per_seq;
+};
+
+struct Places {
+    int64_t src[kAhead][kChunk], dst[kAhead][kChunk];  // byte offsets of the tokens' first atoms; src < 0: stays
+};
+
+// Moves NA atoms of type V, from the first one of `page` (block 0's) on, of every token.  ROWS: lanes along
+// the atoms of a token.
+template <typename V, int NA, bool ROWS>
+__device__ __forceinline__ void move_chain(const CompactParams& p, const Array& arr, uint8_t* page, int unit, int n, Places& at) {
+    const int tid = threadIdx.x, seq = unit / p.num_kv_heads;
+    const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
+    const int32_t* kept = p.kept + (int64_t)unit * p.max_budget;
+    // Places of chunk j.  Written while the stores of chunk j - 3 may still be reading theirs, so there are four.
+    auto plan = [&](int j) {
+        const int i = j * kChunk + tid;
+        int64_t src = -1, dst = 0;
+        if (i < n) {
+            const int k = kept[i], before = i > 0 ? kept[i - 1] : -1;
+            if (k < i || k <= before || k >= p.max_blocks_per_seq * kBS) {
+                if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_SLOT);
+            } else if (k > i) {
+                const int from = table[k / kBS], to = table[i / kBS];
+                if ((unsigned)from >= (unsigned)p.num_blocks || (unsigned)to >= (unsigned)p.num_blocks) {
+                    if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
+                } else {
+                    src = from * arr.block_bytes + k % kBS * arr.token_step;
+                    dst = to * arr.block_bytes + i % kBS * arr.token_step;
+                }
+            }
+        }
+        at.src[j % kAhead][tid] = src;
+        at.dst[j % kAhead][tid] = dst;
+    };
+    auto token_of = [&](int k) { return ROWS ? tid / NA + k * (kThreads / NA) : tid; };
+    auto atom_of = [&](int k) { return ROWS ? tid % NA : k; };
+    V cur[NA], next[NA];
+    auto load = [&](int j, V(&x)[NA]) {
+#pragma unroll
+        for (int k = 0; k < NA; ++k) {
+            const int64_t s = at.src[j % kAhead][token_of(k)];
+            if (s >= 0) x[k] = *reinterpret_cast<const V*>(page + s + atom_of(k) * arr.atom_step);
+        }
+    };
+    auto store = [&](int j, const V(&x)[NA]) {
+#pragma unroll
+        for (int k = 0; k < NA; ++k) {
+            const int t = token_of(k);
+            if (at.src[j % kAhead][t] >= 0)
+                *reinterpret_cast<V*>(page + at.dst[j % kAhead][t] + atom_of(k) * arr.atom_step) = x[k];
+        }
+    };
+    const int chunks = (n + kChunk - 1) / kChunk;
+    plan(0);
+    plan(1);
+    __syncthreads();
+    load(0, cur);
+    for (int j = 0; j < chunks; ++j) {
+        load(j + 1, next);
+        plan(j + 2);
+        __syncthreads();  // every load of chunk j is done, and chunk j + 2's places are there
+        store(j, cur);
+#pragma unroll
+        for (int k = 0; k < NA; ++k) cur[k] = next[k];
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) pa_compact_kernel(const CompactParams p) {
+    __shared__ Places at;
+    const int chains = p.first[5];
+    const int unit = blockIdx.x / chains, chain = blockIdx.x - unit * chains;
+    const int seq = unit / p.num_kv_heads, kvh = unit - seq * p.num_kv_heads;
+    int which = 0;
+    while (chain >= p.first[which + 1]) ++which;
+    const Array& arr = p.arrays[which];
+    const int c = chain - p.first[which], head = kvh * arr.heads + c / arr.chains, part = c % arr.chains;
+    uint8_t* page = arr.base + (int64_t)head * arr.head_bytes;
+    pa::pdl_launch_dependents();
+    pa::pdl_wait_primary();
+    int n = p.new_seq_lens[seq];
+    if (n < 0 || n > p.max_budget) {
+        if (threadIdx.x == 0 && p.dev_error) atomicOr(p.dev_error, PA_DEVERR_SEQ_LEN);
+        n = n < 0 ? 0 : p.max_budget;
+    }
+    if (n == 0) return;
+    switch (arr.kind) {
+    case kRow4: move_chain<uint4, 4, true>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
+    case kRow2: move_chain<uint4, 2, true>(p, arr, page, unit, n, at); break;
+    case kPiece: move_chain<uint4, 4, false>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
+    case kWide: move_chain<uint32_t, 16, false>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kHalf: move_chain<uint16_t, 16, false>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kByte: move_chain<uint8_t, 16, false>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kWord8: move_chain<uint2, 1, false>(p, arr, page, unit, n, at); break;
+    default: move_chain<uint32_t, 1, false>(p, arr, page, unit, n, at); break;
+    }
+}
+
+bool size_ok(int d, bool fp4) { return d == 64 || d == 128 || (d == 256 && !fp4); }
+
+}  // namespace
+
+extern "C" pa_status pa_compact_kv(const pa_compact_args* a, void* stream) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs < 0 || a->num_kv_heads <= 0 || a->max_budget < 0 || a->num_key_heads <= 0 || a->num_value_heads <= 0 ||
+        a->num_blocks <= 0 || a->max_blocks_per_seq < 0)
+        return PA_ERR_INVALID_ARG;
+    if (a->dtype != PA_DTYPE_F32 && a->dtype != PA_DTYPE_F16 && a->dtype != PA_DTYPE_BF16) return PA_ERR_INVALID_ARG;
+    if (a->layout != PA_LAYOUT_SPLIT && a->layout != PA_LAYOUT_NHD) return PA_ERR_INVALID_ARG;
+    const int kv = a->kv_dtype;
+    if (kv != PA_KV_SAME && kv != PA_KV_FP8_E4M3 && kv != PA_KV_FP8_E5M2 && kv != PA_KV_FP4_E2M1) return PA_ERR_INVALID_ARG;
+    if (a->num_key_heads % a->num_kv_heads != 0 || a->num_value_heads % a->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    const bool fp4 = kv == PA_KV_FP4_E2M1;
+    if (kv != PA_KV_SAME && a->dtype == PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;
+    if (fp4 && a->layout != PA_LAYOUT_NHD) return PA_ERR_UNSUPPORTED;
+    if (a->block_size != PA_BLOCK_SIZE || a->num_blocks >= 1 << 27 || a->max_blocks_per_seq >= 1 << 27 || a->max_budget > 1 << 30)
+        return PA_ERR_UNSUPPORTED;
+    if (!size_ok(a->key_head_size, fp4) || !size_ok(a->value_head_size, fp4)) return PA_ERR_UNSUPPORTED;
+    if (a->num_key_heads > 65535 || a->num_value_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (a->max_budget > (int64_t)a->max_blocks_per_seq * PA_BLOCK_SIZE) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs == 0 || a->max_budget == 0) return PA_OK;
+    if (!a->key_cache || !a->value_cache || !a->block_tables || !a->kept || !a->new_seq_lens) return PA_ERR_INVALID_ARG;
+    if (!pa::aligned(a->key_cache, 16) || !pa::aligned(a->value_cache, 16) || !pa::aligned(a->scores, 4) ||
+        !pa::aligned(a->block_tables, 4) || !pa::aligned(a->kept, 4) || !pa::aligned(a->new_seq_lens, 4) ||
+        !pa::aligned(a->dev_error, 4))
+        return PA_ERR_INVALID_ARG;
+
+    CompactParams p = {};
+    const int e = kv != PA_KV_SAME ? 1 : (a->dtype == PA_DTYPE_F32 ? 4 : 2);
+    for (int v = 0; v < 2; ++v) {
+        Array& arr = p.arrays[v];
+        const int heads = v ? a->num_value_heads : a->num_key_heads, d = v ? a->value_head_size : a->key_head_size;
+        arr.base = static_cast<uint8_t*>(v ? a->value_cache : a->key_cache);
+        arr.heads = heads / a->num_kv_heads;
+        arr.head_bytes = fp4 ? 9 * d : kBS * d * e;
+        arr.block_bytes = (int64_t)heads * arr.head_bytes;
+        if (a->layout == PA_LAYOUT_NHD) {
+            const int row = fp4 ? d / 2 : d * e;
+            arr.token_step = row;
+            arr.atom_step = 16;
+            arr.chains = row < 64 ? 1 : row / 64;
+            arr.kind = row < 64 ? kRow2 : kRow4;
+        } else if (!v) {
+            arr.token_step = 16;
+            arr.atom_step = 16 * kBS;
+            arr.chains = d * e / 64;
+            arr.kind = kPiece;
+        } else {
+            arr.token_step = e;
+            arr.atom_step = e * kBS;
+            arr.chains = d / 16;
+            arr.kind = e == 4 ? kWide : (e == 2 ? kHalf : kByte);
+        }
+        if (fp4) {  // the scales behind the codes
+            Array& s = p.arrays[2 + v];
+            s = arr;
+            s.base += 8 * d;
+            s.token_step = d / 16;
+            s.chains = 1;
+            s.kind = d == 128 ? kWord8 : kWord4;
+        }
+    }
+    if (a->scores) {
+        Array& s = p.arrays[4];
+        s.base = reinterpret_cast<uint8_t*>(a->scores);
+        s.heads = 1;
+        s.head_bytes = kBS * 4;
+        s.block_bytes = (int64_t)a->num_kv_heads * s.head_bytes;
+        s.token_step = 4;
+        s.chains = 1;
+        s.kind = kWord4;
+    }
+    for (int i = 0; i < 5; ++i) p.first[i + 1] = p.first[i] + p.arrays[i].heads * p.arrays[i].chains;
+    p.block_tables = a->block_tables;
+    p.kept = a->kept;
+    p.new_seq_lens = a->new_seq_lens;
+    p.dev_error = a->dev_error;
+    p.num_seqs = a->num_seqs;
+    p.num_kv_heads = a->num_kv_heads;
+    p.max_budget = a->max_budget;
+    p.num_blocks = a->num_blocks;
+    p.max_blocks_per_seq = a->max_blocks_per_seq;
+    const int64_t grid = (int64_t)a->num_seqs * a->num_kv_heads * p.first[5];
+    if (grid > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    return pa::launch_pdl(pa_compact_kernel, dim3((unsigned)grid), kThreads, 0, stream, p) ? PA_OK : PA_ERR_LAUNCH;
+}

@@ -1,0 +1,286 @@
+// pa_select.cu -- pa_select_tokens: which tokens of a sequence stay within its budget, for
+// each kv head.
+//
+// The threshold is the k-th largest of the scores between the first and the last tokens, by
+// radix selection: scores become unsigned keys of the same order, and three histograms of
+// 11, 11 and 10 bits (2048 bins in shared memory) fix the key digit by digit.  Then each
+// thread takes a run of successive tokens, two prefix sums (of keys equal to the threshold,
+// lowest positions first, then of the tokens that stay) give every run its place, and the
+// positions come out ascending.  Everything is whole numbers: no order of atomics shows.
+//
+// One cluster of 1, 2, 4 or 8 CTAs works on a (sequence, kv head), each on a part of the tokens whose
+// keys it keeps in shared memory; the CTAs read each other's histograms there.  Little is read
+// (four bytes a token) and what bounds the call is the chain of dependent steps, so few steps
+// and short ones are what counts: a length of 100000 is 12500 keys in each of eight CTAs.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "pa_cache.h"
+#include "pa_host.cuh"
+#include "pa_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kBS = PA_BLOCK_SIZE;
+constexpr int kThreads = 512;
+constexpr int kBins = 2048;
+constexpr int kCached = 40960;  // keys that a CTA keeps (160 KB); longer parts are read again at every step
+
+struct SelectParams {
+    int32_t* kept;
+    int32_t* new_seq_lens;
+    const float* scores;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* budgets;
+    int32_t* dev_error;
+    int num_seqs, num_kv_heads, num_blocks, max_seq_len, max_blocks_per_seq, max_budget, sink, recent;
+};
+
+// Order of the scores as unsigned numbers; NaN below everything, zeros of both signs the same.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    if (x != x) return 0;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Sum of v over the threads before this one, and over all of them.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warps, uint32_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warps[warp] = x;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const uint32_t s = warps[w];
+        before += w < warp ? s : 0;
+        all += s;
+    }
+    total = all;
+    __syncthreads();
+    return before + x - v;
+}
+
+template <bool CACHED>
+__global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams p) {
+    extern __shared__ uint32_t keys[];
+    __shared__ __align__(16) uint32_t hist[3][kBins];
+    __shared__ uint32_t warps[kThreads / 32];
+    __shared__ uint32_t found[2];   // digit of the threshold, how many above it
+    __shared__ uint32_t counts[2];  // this CTA's tokens that stay for sure, and those at the threshold
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const int unit = blockIdx.x / ranks, seq = unit / p.num_kv_heads, head = unit - seq * p.num_kv_heads;
+    for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
+    pa::pdl_launch_dependents();
+    pa::pdl_wait_primary();
+    int n = p.seq_lens[seq], budget = p.budgets[seq];
+    {
+        const int n0 = n, b0 = budget;
+        n = min(max(n, 0), p.max_seq_len);
+        budget = min(max(budget, 0), p.max_budget);
+        if ((n != n0 || budget != b0) && tid == 0 && rank == 0 && head == 0 && p.dev_error)
+            atomicOr(p.dev_error, PA_DEVERR_SEQ_LEN);
+    }
+    if (tid == 0 && rank == 0 && head == 0) p.new_seq_lens[seq] = min(n, budget);
+    int32_t* kept = p.kept + (int64_t)unit * p.max_budget;
+    if (n <= budget) {
+        for (int i = rank * kThreads + tid; i < n; i += ranks * kThreads) kept[i] = i;
+        return;  // (every CTA of the cluster)
+    }
+    const int recent = min(p.recent, budget), sink = min(p.sink, budget - recent);
+    const int lo = sink, hi = n - recent;  // tokens that their scores decide on
+    uint32_t left = (uint32_t)(budget - recent - sink);
+    // this CTA's tokens, whole pages
+    const int pages = (n + kBS - 1) / kBS, per = (pages + ranks - 1) / ranks;
+    const int t0 = min(rank * per * kBS, n), t1 = min((rank + 1) * per * kBS, n), mine = t1 - t0;
+    const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
+    auto read = [&](int t) -> uint32_t {
+        const int blk = table[t / kBS];
+        if ((unsigned)blk >= (unsigned)p.num_blocks) {
+            if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
+            return 0;
+        }
+        return key_of(p.scores[((int64_t)blk * p.num_kv_heads + head) * kBS + t % kBS]);
+    };
+    auto key_at = [&](int i) { return CACHED ? keys[i] : read(t0 + i); };
+    __syncthreads();  // histograms zeroed
+
+    uint32_t prefix = 0;  // digits of the threshold that are known, at their places
+    if (left > 0) {
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+            const uint32_t known = pass == 0 ? 0 : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
+            const uint32_t digits = pass == 2 ? 0x3ffu : 0x7ffu;
+#pragma unroll 8
+            for (int i = tid; i < mine; i += kThreads) {
+                const int t = t0 + i;
+                uint32_t k;
+                if (CACHED && pass == 0) {
+                    k = t >= lo && t < hi ? read(t) : 0;
+                    keys[i] = k;
+                } else {
+                    k = t >= lo && t < hi ? key_at(i) : 0;
+                }
+                if (t >= lo && t < hi && (k & known) == prefix) atomicAdd(&hist[pass][k >> shift & digits], 1u);
+            }
+            cluster.sync();
+            // every CTA adds up all histograms: four bins a thread, the highest first
+            uint32_t c[4] = {0, 0, 0, 0}, sum = 0, total;
+            const int bin0 = kBins - 4 - 4 * tid;
+            for (int r = 0; r < ranks; ++r) {
+                const uint4 h = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[pass][bin0], r));
+                c[0] += h.w;
+                c[1] += h.z;
+                c[2] += h.y;
+                c[3] += h.x;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += c[i];
+            uint32_t above = block_scan(sum, warps, total);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (above < left && left <= above + c[i]) {
+                    found[0] = (uint32_t)(bin0 + 3 - i);
+                    found[1] = above;
+                }
+                above += c[i];
+            }
+            __syncthreads();
+            prefix |= found[0] << shift;
+            left -= found[1];
+            __syncthreads();
+        }
+    }
+    // runs of successive tokens: those that stay whatever the ties, and those at the threshold
+    const bool any = budget - recent - sink > 0;
+    int run = (mine + kThreads - 1) / kThreads;
+    run |= 1;  // odd: no two lanes of a warp in one bank
+    const int a = min(tid * run, mine), b = min(a + run, mine);
+    uint32_t sure = 0, ties = 0;
+    for (int i = a; i < b; ++i) {
+        const int t = t0 + i;
+        if (t < lo || t >= hi) {
+            ++sure;
+        } else if (any) {
+            const uint32_t k = key_at(i);
+            sure += k > prefix;
+            ties += k == prefix;
+        }
+    }
+    uint32_t all_sure, all_ties;
+    const uint32_t ties_before = block_scan(ties, warps, all_ties);
+    block_scan(sure, warps, all_sure);
+    if (tid == 0) {
+        counts[0] = all_sure;
+        counts[1] = all_ties;
+    }
+    cluster.sync();
+    uint32_t place = 0, at_threshold = 0;  // of the CTAs before this one
+    for (int r = 0; r < rank; ++r) {
+        const uint32_t* c = cluster.map_shared_rank(counts, r);
+        const uint32_t s = c[0], e = c[1];
+        const uint32_t take = at_threshold < left ? min(e, left - at_threshold) : 0;
+        place += s + take;
+        at_threshold += e;
+    }
+    uint32_t tie = at_threshold + ties_before, total;
+    const uint32_t take = any && tie < left ? min(ties, left - tie) : 0;
+    place += block_scan(sure + take, warps, total);
+    for (int i = a; i < b; ++i) {
+        const int t = t0 + i;
+        bool stays = t < lo || t >= hi;
+        if (!stays && any) {
+            const uint32_t k = key_at(i);
+            stays = k > prefix || (k == prefix && tie < left);
+            tie += k == prefix;
+        }
+        if (stays) kept[place++] = t;
+    }
+    cluster.sync();  // the counts are read by the others
+}
+
+template <bool CACHED>
+bool launch(const SelectParams& p, int ranks, size_t smem, void* stream) {
+    auto kern = pa_select_kernel<CACHED>;
+    if (smem > 16 * 1024) {
+        static std::atomic<int> ready[pa::kHostDevices];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return false;
+        if (dev >= pa::kHostDevices || !ready[dev].load()) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4) != cudaSuccess) return false;
+            if (dev < pa::kHostDevices) ready[dev].store(1);
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)p.num_seqs * p.num_kv_heads * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" pa_status pa_select_tokens(const pa_select_args* a, void* stream) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs < 0 || a->num_kv_heads <= 0 || a->num_blocks <= 0 || a->max_seq_len < 0 || a->max_blocks_per_seq < 0 ||
+        a->max_budget < 0 || a->sink < 0 || a->recent < 0)
+        return PA_ERR_INVALID_ARG;
+    if (a->block_size != PA_BLOCK_SIZE || a->max_seq_len > 1 << 30 || a->max_budget > 1 << 30) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)a->num_seqs * a->num_kv_heads * 8 > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    if (a->num_seqs == 0) return PA_OK;
+    if ((!a->kept && a->max_budget > 0) || !a->new_seq_lens || !a->scores || !a->block_tables || !a->seq_lens || !a->budgets)
+        return PA_ERR_INVALID_ARG;
+    if (a->new_seq_lens == a->seq_lens) return PA_ERR_INVALID_ARG;  // read by CTAs that start later
+    if ((int64_t)a->max_blocks_per_seq * PA_BLOCK_SIZE < a->max_seq_len) return PA_ERR_INVALID_ARG;
+    if (!pa::aligned(a->kept, 4) || !pa::aligned(a->new_seq_lens, 4) || !pa::aligned(a->scores, 4) ||
+        !pa::aligned(a->block_tables, 4) || !pa::aligned(a->seq_lens, 4) || !pa::aligned(a->budgets, 4) ||
+        !pa::aligned(a->dev_error, 4))
+        return PA_ERR_INVALID_ARG;
+    SelectParams p = {};
+    p.kept = a->kept;
+    p.new_seq_lens = a->new_seq_lens;
+    p.scores = a->scores;
+    p.block_tables = a->block_tables;
+    p.seq_lens = a->seq_lens;
+    p.budgets = a->budgets;
+    p.dev_error = a->dev_error;
+    p.num_seqs = a->num_seqs;
+    p.num_kv_heads = a->num_kv_heads;
+    p.num_blocks = a->num_blocks;
+    p.max_seq_len = a->max_seq_len;
+    p.max_blocks_per_seq = a->max_blocks_per_seq;
+    p.max_budget = a->max_budget;
+    p.sink = a->sink;
+    p.recent = a->recent;
+    int dev = 0, sms = 0;
+    if (!pa::device_and_sms(&dev, &sms)) return PA_ERR_LAUNCH;
+    // CTAs of a cluster: more while each has over 4096 tokens and they all fit at once
+    const int64_t units = (int64_t)a->num_seqs * a->num_kv_heads;
+    int ranks = 1;
+    while (ranks < 8 && a->max_seq_len > 4096 * ranks && units * ranks * 2 <= 2 * (int64_t)sms) ranks *= 2;
+    while (ranks < 8 && (a->max_seq_len + ranks - 1) / ranks + PA_BLOCK_SIZE > kCached) ranks *= 2;
+    const int64_t pages = (a->max_seq_len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE, part = (pages + ranks - 1) / ranks * PA_BLOCK_SIZE;
+    const bool ok = part <= kCached ? launch<true>(p, ranks, (size_t)part * 4, stream) : launch<false>(p, ranks, 0, stream);
+    return ok ? PA_OK : PA_ERR_LAUNCH;
+}

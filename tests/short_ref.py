@@ -110,3 +110,56 @@ def sequences(values, table, lens):
         p = values[table[s, :-(-n // BS)]]
         out.append(p.transpose(0, 2, 1, 3).reshape(-1, p.shape[1], p.shape[3])[:n])
     return out
+
+
+def select_ref(scores, table, lens, budgets, sink, recent, width, fill):
+    """(kept [sequences, heads, width], new lengths)."""
+    heads = scores.shape[1]
+    kept, new = np.full((len(lens), heads, width), fill, dtype=np.int64), np.zeros(len(lens), dtype=np.int64)
+    for s, (n, budget) in enumerate(zip(lens, budgets)):
+        new[s] = min(n, budget)
+        last = min(recent, budget)
+        first = min(sink, budget - last)
+        for h in range(heads):
+            if n <= budget:
+                kept[s, h, :n] = np.arange(n)
+                continue
+            t = np.arange(first, n - last)
+            x = scores[table[s, t // BS], h, t % BS].astype(np.float64)
+            x = np.where(np.isnan(x), -np.inf, x)
+            number = ~np.isnan(scores[table[s, t // BS], h, t % BS])
+            order = np.lexsort((t, -x, ~number))  # numbers first, the largest first, the lowest position first
+            chosen = t[order[:budget - first - last]]
+            kept[s, h, :budget] = np.sort(np.concatenate([np.arange(first), chosen, np.arange(n - last, n)]))
+    return kept, new
+
+
+def compact_ref(caches, scores, table, kept, new, layout, kv_heads, four_bits):
+    """caches (key, value: numpy bits) and scores after the tokens have moved."""
+    out = []
+    for i, c in enumerate(list(caches) + ([] if scores is None else [scores])):
+        c = c.copy()
+        if i == 2:
+            parts = [(c, 1)]
+        elif four_bits:
+            d = c.shape[2] // 9
+            parts = [(c[:, :, :8 * d].reshape(c.shape[0], c.shape[1], BS, d // 2), 1), (c[:, :, 8 * d:].reshape(c.shape[0], c.shape[1], BS, d // 16), 1)]
+        else:
+            parts = [(c, 1 if layout == "nhd" else (2 if i == 0 else 3))]
+        done = []
+        for x, kind in parts:
+            # tokens in front of what a token holds: [blocks, heads, 16, ...]
+            y = x if kind == 1 else (x.transpose(0, 1, 3, 2, 4) if kind == 2 else x.transpose(0, 1, 3, 2))
+            was, now = y.copy(), y.copy()
+            ratio = y.shape[1] // kv_heads
+            for s in range(len(new)):
+                for h in range(kv_heads):
+                    to, src = np.arange(new[s]), kept[s, h, :new[s]]
+                    for k in range(ratio):
+                        now[table[s, to // BS], h * ratio + k, to % BS] = was[table[s, src // BS], h * ratio + k, src % BS]
+            done.append(now if kind == 1 else (now.transpose(0, 1, 3, 2, 4) if kind == 2 else now.transpose(0, 1, 3, 2)))
+        if four_bits and i < 2:
+            out.append(np.ascontiguousarray(np.concatenate([p.reshape(p.shape[0], p.shape[1], -1) for p in done], 2)))
+        else:
+            out.append(np.ascontiguousarray(done[0]))
+    return out

@@ -196,7 +196,7 @@ pa_status pa_add_weights(const pa_weights_args* args, void* stream);
 typedef struct pa_select_args {
     int32_t* kept;               /* [num_seqs][num_kv_heads][max_budget] */
     int32_t* new_seq_lens;       /* [num_seqs] */
-    const float* scores;         /* [num_blocks][num_kv_heads][16] */
+    const float* scores;         /* [num_blocks][num_kv_heads][16]; 16-byte aligned */
     const int32_t* block_tables; /* [num_seqs][max_blocks_per_seq] */
     const int32_t* seq_lens;     /* [num_seqs], in [0, max_seq_len]; not new_seq_lens itself */
     const int32_t* budgets;      /* [num_seqs], in [0, max_budget] */

@@ -24,7 +24,6 @@ namespace {
 
 constexpr int kBS = PA_BLOCK_SIZE;
 constexpr int kThreads = 256;
-constexpr int kChunk = kThreads;  // tokens at once
 constexpr int kAhead = 4;         // chunks whose places are in shared memory (see move_chain)
 
 // One array of the cache, in atoms: atom a of a token's head is at page + a * atom_step + token * token_step.
@@ -38,7 +37,7 @@ struct Array {
     int kind;             // kRow4 ..
 };
 
-enum { kRow4 = 0, kRow2, kPiece, kWide, kHalf, kByte, kWord8, kWord4 };
+enum { kRow2 = 0, kRow4, kRow8, kRow16, kPiece, kWide, kHalf, kByte, kWord8, kWord4 };
 
 struct CompactParams {
     Array arrays[5];  // keys, values, 4-bit scales of both, scores
@@ -51,19 +50,23 @@ struct CompactParams {
 };
 
 struct Places {
-    int64_t src[kAhead][kChunk], dst[kAhead][kChunk];  // byte offsets of the tokens' first atoms; src < 0: stays
+    int64_t src[kAhead][kThreads], dst[kAhead][kThreads];  // byte offsets of the tokens' first atoms; src < 0: stays
 };
 
-// Moves NA atoms of type V, from the first one of `page` (block 0's) on, of every token.  ROWS: lanes along
-// the atoms of a token.
-template <typename V, int NA, bool ROWS>
+// Moves a chain: atoms of type V of every token, from the first one of `page` (block 0's) on.  LANES == 1: a
+// thread has one token of a chunk, and NA atoms of it.  Otherwise LANES threads have the atoms of a token,
+// and each of them NA tokens of a chunk.
+template <typename V, int NA, int LANES>
 __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& arr, uint8_t* page, int unit, int n, Places& at) {
+    constexpr int kChunk = LANES == 1 ? kThreads : kThreads / LANES * NA;  // tokens at once
+    static_assert(kChunk <= kThreads, "a thread to plan each token");
     const int tid = threadIdx.x, seq = unit / p.num_kv_heads;
     const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
     const int32_t* kept = p.kept + (int64_t)unit * p.max_budget;
     // Places of chunk j.  Written while the stores of chunk j - 3 may still be reading theirs, so there are four.
     auto plan = [&](int j) {
         const int i = j * kChunk + tid;
+        if (kChunk < kThreads && tid >= kChunk) return;
         int64_t src = -1, dst = 0;
         if (i < n) {
             const int k = kept[i], before = i > 0 ? kept[i - 1] : -1;
@@ -82,8 +85,8 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
         at.src[j % kAhead][tid] = src;
         at.dst[j % kAhead][tid] = dst;
     };
-    auto token_of = [&](int k) { return ROWS ? tid / NA + k * (kThreads / NA) : tid; };
-    auto atom_of = [&](int k) { return ROWS ? tid % NA : k; };
+    auto token_of = [&](int k) { return LANES > 1 ? tid / LANES + k * (kThreads / LANES) : tid; };
+    auto atom_of = [&](int k) { return LANES > 1 ? tid % LANES : k; };
     V cur[NA], next[NA];
     auto load = [&](int j, V(&x)[NA]) {
 #pragma unroll
@@ -134,14 +137,16 @@ __global__ void __launch_bounds__(kThreads) pa_compact_kernel(const CompactParam
     }
     if (n == 0) return;
     switch (arr.kind) {
-    case kRow4: move_chain<uint4, 4, true>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
-    case kRow2: move_chain<uint4, 2, true>(p, arr, page, unit, n, at); break;
-    case kPiece: move_chain<uint4, 4, false>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
-    case kWide: move_chain<uint32_t, 16, false>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kHalf: move_chain<uint16_t, 16, false>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kByte: move_chain<uint8_t, 16, false>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kWord8: move_chain<uint2, 1, false>(p, arr, page, unit, n, at); break;
-    default: move_chain<uint32_t, 1, false>(p, arr, page, unit, n, at); break;
+    case kRow2: move_chain<uint4, 2, 2>(p, arr, page, unit, n, at); break;
+    case kRow4: move_chain<uint4, 4, 4>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
+    case kRow8: move_chain<uint4, 4, 8>(p, arr, page + part * 8 * arr.atom_step, unit, n, at); break;
+    case kRow16: move_chain<uint4, 4, 16>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kPiece: move_chain<uint4, 4, 1>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
+    case kWide: move_chain<uint32_t, 16, 1>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kHalf: move_chain<uint16_t, 16, 1>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kByte: move_chain<uint8_t, 16, 1>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kWord8: move_chain<uint2, 1, 1>(p, arr, page, unit, n, at); break;
+    default: move_chain<uint32_t, 1, 1>(p, arr, page, unit, n, at); break;
     }
 }
 
@@ -175,6 +180,7 @@ extern "C" pa_status pa_compact_kv(const pa_compact_args* a, void* stream) {
         return PA_ERR_INVALID_ARG;
 
     CompactParams p = {};
+    const int kSlice = 256;
     const int e = kv != PA_KV_SAME ? 1 : (a->dtype == PA_DTYPE_F32 ? 4 : 2);
     for (int v = 0; v < 2; ++v) {
         Array& arr = p.arrays[v];
@@ -187,8 +193,9 @@ extern "C" pa_status pa_compact_kv(const pa_compact_args* a, void* stream) {
             const int row = fp4 ? d / 2 : d * e;
             arr.token_step = row;
             arr.atom_step = 16;
-            arr.chains = row < 64 ? 1 : row / 64;
-            arr.kind = row < 64 ? kRow2 : kRow4;
+            const int wide = row < kSlice ? row : kSlice;
+            arr.chains = row / wide;
+            arr.kind = wide == 32 ? kRow2 : (wide == 64 ? kRow4 : (wide == 128 ? kRow8 : kRow16));
         } else if (!v) {
             arr.token_step = 16;
             arr.atom_step = 16 * kBS;

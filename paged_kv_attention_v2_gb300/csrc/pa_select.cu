@@ -28,6 +28,7 @@ namespace {
 constexpr int kBS = PA_BLOCK_SIZE;
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
+constexpr int kQuads = 8;       // 16-byte loads of a thread in flight
 constexpr int kCached = 40960;  // keys that a CTA keeps (160 KB); longer parts are read again at every step
 
 struct SelectParams {
@@ -71,15 +72,22 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warps, uint
     return before + x - v;
 }
 
-template <bool CACHED>
+template <bool CACHED, int RANKS>
 __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams p) {
-    extern __shared__ uint32_t keys[];
+    extern __shared__ __align__(16) uint32_t keys[];
     __shared__ __align__(16) uint32_t hist[3][kBins];
     __shared__ uint32_t warps[kThreads / 32];
     __shared__ uint32_t found[2];   // digit of the threshold, how many above it
     __shared__ uint32_t counts[2];  // this CTA's tokens that stay for sure, and those at the threshold
     cg::cluster_group cluster = cg::this_cluster();
-    const int tid = threadIdx.x, ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    constexpr int ranks = RANKS;
+    const int tid = threadIdx.x, rank = RANKS == 1 ? 0 : cluster.block_rank();
+    auto sync_all = [&]() {
+        if constexpr (RANKS == 1)
+            __syncthreads();
+        else
+            cluster.sync();
+    };
     const int unit = blockIdx.x / ranks, seq = unit / p.num_kv_heads, head = unit - seq * p.num_kv_heads;
     for (int i = tid; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
     pa::pdl_launch_dependents();
@@ -115,6 +123,37 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
     };
     auto key_at = [&](int i) { return CACHED ? keys[i] : read(t0 + i); };
     __syncthreads();  // histograms zeroed
+    if (CACHED && left > 0) {
+        // the keys, four of a page at a time: the loads of a thread do not wait for each other
+        const int quads = (mine + kBS - 1) / kBS * 4;
+        for (int i0 = 0; i0 < quads; i0 += kQuads * kThreads) {
+            int blk[kQuads];
+            float4 x[kQuads];
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k) {
+                const int i = i0 + k * kThreads + tid;
+                blk[k] = i < quads ? table[t0 / kBS + i / 4] : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k) {
+                const int i = i0 + k * kThreads + tid;
+                x[k] = make_float4(NAN, NAN, NAN, NAN);
+                if (i >= quads) continue;
+                if ((unsigned)blk[k] < (unsigned)p.num_blocks)
+                    x[k] = *reinterpret_cast<const float4*>(p.scores + ((int64_t)blk[k] * p.num_kv_heads + head) * kBS + i % 4 * 4);
+                else if (p.dev_error)
+                    atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
+            }
+#pragma unroll
+            for (int k = 0; k < kQuads; ++k) {
+                const int i = i0 + k * kThreads + tid;
+                if (i < quads)
+                    *reinterpret_cast<uint4*>(keys + 4 * i) =
+                        make_uint4(key_of(x[k].x), key_of(x[k].y), key_of(x[k].z), key_of(x[k].w));
+            }
+        }
+        __syncthreads();
+    }
 
     uint32_t prefix = 0;  // digits of the threshold that are known, at their places
     if (left > 0) {
@@ -123,24 +162,19 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const uint32_t known = pass == 0 ? 0 : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
             const uint32_t digits = pass == 2 ? 0x3ffu : 0x7ffu;
-#pragma unroll 8
-            for (int i = tid; i < mine; i += kThreads) {
-                const int t = t0 + i;
-                uint32_t k;
-                if (CACHED && pass == 0) {
-                    k = t >= lo && t < hi ? read(t) : 0;
-                    keys[i] = k;
-                } else {
-                    k = t >= lo && t < hi ? key_at(i) : 0;
-                }
-                if (t >= lo && t < hi && (k & known) == prefix) atomicAdd(&hist[pass][k >> shift & digits], 1u);
+#pragma unroll 4
+            for (int i = max(lo - t0, 0) + tid; i < min(mine, hi - t0); i += kThreads) {
+                const uint32_t k = key_at(i);
+                if ((k & known) == prefix) atomicAdd(&hist[pass][k >> shift & digits], 1u);
             }
-            cluster.sync();
+            sync_all();
             // every CTA adds up all histograms: four bins a thread, the highest first
             uint32_t c[4] = {0, 0, 0, 0}, sum = 0, total;
             const int bin0 = kBins - 4 - 4 * tid;
+#pragma unroll
             for (int r = 0; r < ranks; ++r) {
-                const uint4 h = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[pass][bin0], r));
+                const uint32_t* at = &hist[pass][bin0];
+                const uint4 h = *reinterpret_cast<const uint4*>(RANKS == 1 ? at : cluster.map_shared_rank(at, r));
                 c[0] += h.w;
                 c[1] += h.z;
                 c[2] += h.y;
@@ -186,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
         counts[0] = all_sure;
         counts[1] = all_ties;
     }
-    cluster.sync();
+    sync_all();
     uint32_t place = 0, at_threshold = 0;  // of the CTAs before this one
     for (int r = 0; r < rank; ++r) {
         const uint32_t* c = cluster.map_shared_rank(counts, r);
@@ -208,12 +242,12 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
         }
         if (stays) kept[place++] = t;
     }
-    cluster.sync();  // the counts are read by the others
+    if constexpr (RANKS > 1) cluster.sync();  // the counts are read by the others
 }
 
-template <bool CACHED>
-bool launch(const SelectParams& p, int ranks, size_t smem, void* stream) {
-    auto kern = pa_select_kernel<CACHED>;
+template <bool CACHED, int RANKS>
+bool launch(const SelectParams& p, size_t smem, void* stream) {
+    auto kern = pa_select_kernel<CACHED, RANKS>;
     if (smem > 16 * 1024) {
         static std::atomic<int> ready[pa::kHostDevices];
         int dev = 0;
@@ -224,7 +258,7 @@ bool launch(const SelectParams& p, int ranks, size_t smem, void* stream) {
         }
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)p.num_seqs * p.num_kv_heads * ranks));
+    cfg.gridDim = dim3((unsigned)((int64_t)p.num_seqs * p.num_kv_heads * RANKS));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
@@ -232,10 +266,10 @@ bool launch(const SelectParams& p, int ranks, size_t smem, void* stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.x = RANKS;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = RANKS > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess;
 }
 
@@ -253,7 +287,7 @@ extern "C" pa_status pa_select_tokens(const pa_select_args* a, void* stream) {
         return PA_ERR_INVALID_ARG;
     if (a->new_seq_lens == a->seq_lens) return PA_ERR_INVALID_ARG;  // read by CTAs that start later
     if ((int64_t)a->max_blocks_per_seq * PA_BLOCK_SIZE < a->max_seq_len) return PA_ERR_INVALID_ARG;
-    if (!pa::aligned(a->kept, 4) || !pa::aligned(a->new_seq_lens, 4) || !pa::aligned(a->scores, 4) ||
+    if (!pa::aligned(a->kept, 4) || !pa::aligned(a->new_seq_lens, 4) || !pa::aligned(a->scores, 16) ||
         !pa::aligned(a->block_tables, 4) || !pa::aligned(a->seq_lens, 4) || !pa::aligned(a->budgets, 4) ||
         !pa::aligned(a->dev_error, 4))
         return PA_ERR_INVALID_ARG;
@@ -281,6 +315,11 @@ extern "C" pa_status pa_select_tokens(const pa_select_args* a, void* stream) {
     while (ranks < 8 && a->max_seq_len > 4096 * ranks && units * ranks * 2 <= 2 * (int64_t)sms) ranks *= 2;
     while (ranks < 8 && (a->max_seq_len + ranks - 1) / ranks + PA_BLOCK_SIZE > kCached) ranks *= 2;
     const int64_t pages = (a->max_seq_len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE, part = (pages + ranks - 1) / ranks * PA_BLOCK_SIZE;
-    const bool ok = part <= kCached ? launch<true>(p, ranks, (size_t)part * 4, stream) : launch<false>(p, ranks, 0, stream);
+    const size_t smem = (size_t)part * 4;
+    const bool ok = part > kCached ? launch<false, 8>(p, 0, stream)
+                    : ranks == 1   ? launch<true, 1>(p, smem, stream)
+                    : ranks == 2   ? launch<true, 2>(p, smem, stream)
+                    : ranks == 4   ? launch<true, 4>(p, smem, stream)
+                                   : launch<true, 8>(p, smem, stream);
     return ok ? PA_OK : PA_ERR_LAUNCH;
 }

@@ -5,8 +5,8 @@
 #include "pa_weights.cuh"
 
 namespace pa {
-bool launch_weights_f32(const WeightParams& p, int head_size, int64_t grid, void* stream) {
-    return launch_weights<float, kWSame>(p, head_size, grid, stream);
+bool launch_weights_f32(WeightParams& p, int head_size, int sms, void* stream) {
+    return launch_weights<float, kWSame>(p, head_size, sms, stream);
 }
 }  // namespace pa
 
@@ -71,17 +71,11 @@ extern "C" pa_status pa_add_weights(const pa_weights_args* a, void* stream) {
     const int elem = kv != PA_KV_SAME ? 1 : (a->dtype == PA_DTYPE_F32 ? 4 : 2);
     p.token_step = a->layout == PA_LAYOUT_NHD ? a->head_size * elem : 16;
     p.piece_step = a->layout == PA_LAYOUT_NHD ? 16 : 16 * PA_BLOCK_SIZE;
-    // Pages of a CTA: each one reads its rows' statistics again, so long sequences get long tiles, as
-    // long as there are some CTAs more than fit at once.
-    const int64_t pages = (a->max_seq_len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE, heads = (int64_t)a->num_seqs * a->num_kv_heads;
-    p.tile_pages = 4 * pa::kWeightWarps;
-    while (p.tile_pages < 32 * pa::kWeightWarps && heads * (pages / (2 * p.tile_pages)) >= 8 * (int64_t)sms) p.tile_pages *= 2;
-    p.tiles = (int)((pages + p.tile_pages - 1) / p.tile_pages);
-    const int64_t grid = heads * p.tiles;
-    if (grid > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    // (grid: at least 2048 tokens a tile, checked for any tile size)
+    if ((int64_t)a->num_seqs * a->num_kv_heads > 0x7fffffffLL / (1 + (a->max_seq_len >> 11)) / 2) return PA_ERR_UNSUPPORTED;
     const int kvk = kv == PA_KV_SAME ? pa::kWSame : kv == PA_KV_FP8_E4M3 ? pa::kWE4M3 : kv == PA_KV_FP8_E5M2 ? pa::kWE5M2 : pa::kWE2M1;
-    const bool ok = a->dtype == PA_DTYPE_F32   ? pa::launch_weights_f32(p, a->head_size, grid, stream)
-                    : a->dtype == PA_DTYPE_F16 ? pa::launch_weights_f16(p, a->head_size, kvk, grid, stream)
-                                               : pa::launch_weights_bf16(p, a->head_size, kvk, grid, stream);
+    const bool ok = a->dtype == PA_DTYPE_F32   ? pa::launch_weights_f32(p, a->head_size, sms, stream)
+                    : a->dtype == PA_DTYPE_F16 ? pa::launch_weights_f16(p, a->head_size, kvk, sms, stream)
+                                               : pa::launch_weights_bf16(p, a->head_size, kvk, sms, stream);
     return ok ? PA_OK : PA_ERR_LAUNCH;
 }

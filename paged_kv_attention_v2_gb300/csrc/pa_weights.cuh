@@ -17,6 +17,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "pa_cache.h"
@@ -228,6 +229,11 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     const int seq = unit / p.tiles, tile = unit - seq * p.tiles;
     pdl_launch_dependents();
     pdl_wait_primary();
+    const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
+    // the first two pages' ids, with the lengths: which of them there are is seen below
+    int page = tile * p.tile_pages + warp;
+    int blk = page < p.max_blocks_per_seq ? table[page] : -1;
+    int blk_next = page + kWeightWarps < p.max_blocks_per_seq ? table[page + kWeightWarps] : -1;
     int len = p.seq_lens[seq];
     if (len < 0 || len > p.max_seq_len) {
         if (threadIdx.x == 0 && tile == 0 && kvh == 0) weights_report(p, PA_DEVERR_SEQ_LEN);
@@ -249,10 +255,8 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     const int seen0 = p.window_left >= 0 ? max(0, len - qn - p.window_left) : 0;
 
     const int64_t head_page = (int64_t)p.num_kv_heads;
-    const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
-    auto block_of = [&](int page) {
+    auto check = [&](int page, int blk) {
         if (page >= page1) return -1;
-        const int blk = table[page];
         if ((unsigned)blk >= (unsigned)p.num_blocks) {
             if (lane == 0) weights_report(p, PA_DEVERR_BLOCK_ID);
             return -1;
@@ -268,7 +272,8 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     };
     Page cur, next;
     float old_cur = 0.f, old_next = 0.f;
-    int page = page0 + warp, blk = block_of(page), blk_next = block_of(page + kWeightWarps);
+    blk = check(page, blk);
+    blk_next = check(page + kWeightWarps, blk_next);
     load(page, blk, cur, old_cur);
 
     uint32_t q[NT][Page::kQWords], top = 0;
@@ -311,22 +316,22 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     }
     __syncthreads();
     float lev[NT][2], slope[NT][2];
-    int klo[NT][2], khi[NT][2];
+    bool there[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int v = nt * 8 + 2 * cq + e;
-            lev[nt][e] = level[v];
+            there[nt][e] = v < GE;
+            lev[nt][e] = level[v] * kLog2;
             slope[nt][e] = p.alibi && v < GE ? p.alibi[kvh * G + v % G] : 0.f;
-            const int pos = len - qn + v / G;
-            khi[nt][e] = v < GE ? pos : -1;  // (no key: rows that there are none)
-            klo[nt][e] = p.window_left >= 0 ? pos - p.window_left : 0;
         }
+    // tokens [all0, all1) are seen by every row
+    const int all0 = p.window_left >= 0 ? max(0, len - 1 - p.window_left) : 0, all1 = len - qn + 1;
 
     for (; page < page1; page += kWeightWarps) {
         load(page + kWeightWarps, blk_next, next, old_next);
-        const int blk_after = block_of(page + 2 * kWeightWarps);
+        const int after = page + 2 * kWeightWarps, blk_after = after < page1 ? table[after] : -1;
         if (blk >= 0) {
             const int tok = page * BS;
             float sum[2] = {0.f, 0.f};
@@ -336,14 +341,35 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = tok + r + 8 * (e >> 1), c = e & 1;
-                        float v = z[nt][e] * p.scale;
-                        if (p.softcap > 0.f) v = p.softcap * tanhf(v * p.inv_softcap);
-                        if (p.alibi) v = fmaf(slope[nt][c], (float)(t - (len - 1)), v);
-                        const float w = exp2f((v - lev[nt][c]) * kLog2);
-                        sum[e >> 1] += t >= klo[nt][c] && t <= khi[nt][c] ? w : 0.f;
-                    }
+                    for (int e = 0; e < 4; ++e) z[nt][e] *= p.scale;
+                if (p.softcap > 0.f || p.alibi) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (p.softcap > 0.f) z[nt][e] = p.softcap * tanhf(z[nt][e] * p.inv_softcap);
+                            if (p.alibi) z[nt][e] = fmaf(slope[nt][e & 1], (float)(tok + r + 8 * (e >> 1) - (len - 1)), z[nt][e]);
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[nt][e] = there[nt][e & 1] ? exp2f(fmaf(z[nt][e], kLog2, -lev[nt][e & 1])) : 0.f;
+                if (tok < all0 || tok + BS > all1) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = tok + r + 8 * (e >> 1), pos = len - qn + (nt * 8 + 2 * cq + (e & 1)) / G;
+                            if (t > pos || (p.window_left >= 0 && t < pos - p.window_left)) z[nt][e] = 0.f;
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    sum[0] += z[nt][0] + z[nt][1];
+                    sum[1] += z[nt][2] + z[nt][3];
+                }
 #pragma unroll
                 for (int o = 1; o < 4; o <<= 1) {
                     sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
@@ -361,26 +387,52 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
         cur = next;
         old_cur = old_next;
         blk = blk_next;
-        blk_next = blk_after;
+        blk_next = check(after, blk_after);
     }
 }
 
+// Tiles: as many as fit on the GPU at once, each a whole number of rounds of a CTA's warps (a tile's first
+// page comes some three dependent loads after its CTA starts, and its rows' statistics are read again),
+// but of at most kTilePages pages, as sequences of a batch differ in length.
+constexpr int kTilePages = 128;
+
+template <typename T, int HEAD, int KV, int NT>
+bool launch_weights_rows(WeightParams& p, int sms, void* stream) {
+    auto kern = pa_weights_kernel<T, HEAD, KV, NT>;
+    static std::atomic<int> resident[kHostDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    int occ = dev < kHostDevices ? resident[dev].load() : 0;
+    if (occ <= 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kWeightWarps * 32, 0) != cudaSuccess || occ < 1) return false;
+        if (dev < kHostDevices) resident[dev].store(occ);
+    }
+    const int64_t pages = (p.max_seq_len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE, units = (int64_t)p.num_seqs * p.num_kv_heads;
+    int64_t per = (int64_t)sms * occ / units;  // tiles of a sequence's head
+    if (per < (pages + kTilePages - 1) / kTilePages) per = (pages + kTilePages - 1) / kTilePages;
+    int64_t tile = (pages + per - 1) / per;
+    tile = (tile + kWeightWarps - 1) / kWeightWarps * kWeightWarps;
+    p.tile_pages = (int)tile;
+    p.tiles = (int)((pages + tile - 1) / tile);
+    const int64_t grid = units * p.tiles;
+    if (grid > 0x7fffffffLL) return false;
+    return launch_pdl(kern, dim3((unsigned)grid), kWeightWarps * 32, 0, stream, p);
+}
+
 template <typename T, int HEAD, int KV>
-bool launch_weights_head(const WeightParams& p, int64_t grid, void* stream) {
-    const dim3 g((unsigned)grid);
-    return p.max_q_len * p.group <= 8
-               ? launch_pdl(pa_weights_kernel<T, HEAD, KV, 1>, g, kWeightWarps * 32, 0, stream, p)
-               : launch_pdl(pa_weights_kernel<T, HEAD, KV, 2>, g, kWeightWarps * 32, 0, stream, p);
+bool launch_weights_head(WeightParams& p, int sms, void* stream) {
+    return p.max_q_len * p.group <= 8 ? launch_weights_rows<T, HEAD, KV, 1>(p, sms, stream)
+                                      : launch_weights_rows<T, HEAD, KV, 2>(p, sms, stream);
 }
 
 template <typename T, int KV>
-bool launch_weights(const WeightParams& p, int head_size, int64_t grid, void* stream) {
-    return head_size == 128 ? launch_weights_head<T, 128, KV>(p, grid, stream) : launch_weights_head<T, 64, KV>(p, grid, stream);
+bool launch_weights(WeightParams& p, int head_size, int sms, void* stream) {
+    return head_size == 128 ? launch_weights_head<T, 128, KV>(p, sms, stream) : launch_weights_head<T, 64, KV>(p, sms, stream);
 }
 
 // One translation unit per query type; kv: kWSame .. kWE2M1
-bool launch_weights_f32(const WeightParams& p, int head_size, int64_t grid, void* stream);
-bool launch_weights_f16(const WeightParams& p, int head_size, int kv, int64_t grid, void* stream);
-bool launch_weights_bf16(const WeightParams& p, int head_size, int kv, int64_t grid, void* stream);
+bool launch_weights_f32(WeightParams& p, int head_size, int sms, void* stream);
+bool launch_weights_f16(WeightParams& p, int head_size, int kv, int sms, void* stream);
+bool launch_weights_bf16(WeightParams& p, int head_size, int kv, int sms, void* stream);
 
 }  // namespace pa

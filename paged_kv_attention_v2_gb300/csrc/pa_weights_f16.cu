@@ -2,12 +2,12 @@
 #include "pa_weights.cuh"
 
 namespace pa {
-bool launch_weights_f16(const WeightParams& p, int head_size, int kv, int64_t grid, void* stream) {
+bool launch_weights_f16(WeightParams& p, int head_size, int kv, int sms, void* stream) {
     switch (kv) {
-    case kWSame: return launch_weights<__half, kWSame>(p, head_size, grid, stream);
-    case kWE4M3: return launch_weights<__half, kWE4M3>(p, head_size, grid, stream);
-    case kWE5M2: return launch_weights<__half, kWE5M2>(p, head_size, grid, stream);
-    default: return launch_weights<__half, kWE2M1>(p, head_size, grid, stream);
+    case kWSame: return launch_weights<__half, kWSame>(p, head_size, sms, stream);
+    case kWE4M3: return launch_weights<__half, kWE4M3>(p, head_size, sms, stream);
+    case kWE5M2: return launch_weights<__half, kWE5M2>(p, head_size, sms, stream);
+    default: return launch_weights<__half, kWE2M1>(p, head_size, sms, stream);
     }
 }
 }  // namespace pa

@@ -53,12 +53,12 @@ struct Places {
     int64_t src[kAhead][kThreads], dst[kAhead][kThreads];  // byte offsets of the tokens' first atoms; src < 0: stays
 };
 
-// Moves a chain: atoms of type V of every token, from the first one of `page` (block 0's) on.  LANES == 1: a
-// thread has one token of a chunk, and NA atoms of it.  Otherwise LANES threads have the atoms of a token,
-// and each of them NA tokens of a chunk.
-template <typename V, int NA, int LANES>
+// Moves a chain: LANES * NA atoms of type V of every token, from the first one of `page` (block 0's) on.  LANES
+// neighbouring threads have successive atoms of a token, each of them NA of those, LANES apart, of each of NT
+// tokens of a chunk.
+template <typename V, int NA, int LANES, int NT>
 __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& arr, uint8_t* page, int unit, int n, Places& at) {
-    constexpr int kChunk = LANES == 1 ? kThreads : kThreads / LANES * NA;  // tokens at once
+    constexpr int kChunk = kThreads / LANES * NT;  // tokens at once
     static_assert(kChunk <= kThreads, "a thread to plan each token");
     const int tid = threadIdx.x, seq = unit / p.num_kv_heads;
     const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
@@ -85,22 +85,28 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
         at.src[j % kAhead][tid] = src;
         at.dst[j % kAhead][tid] = dst;
     };
-    auto token_of = [&](int k) { return LANES > 1 ? tid / LANES + k * (kThreads / LANES) : tid; };
-    auto atom_of = [&](int k) { return LANES > 1 ? tid % LANES : k; };
-    V cur[NA], next[NA];
-    auto load = [&](int j, V(&x)[NA]) {
+    const int lane_token = tid / LANES, lane_atom = tid % LANES * arr.atom_step;
+    V cur[NT][NA], next[NT][NA];
+    auto load = [&](int j, V(&x)[NT][NA]) {
 #pragma unroll
-        for (int k = 0; k < NA; ++k) {
-            const int64_t s = at.src[j % kAhead][token_of(k)];
-            if (s >= 0) x[k] = *reinterpret_cast<const V*>(page + s + atom_of(k) * arr.atom_step);
+        for (int t = 0; t < NT; ++t) {
+            const int64_t s = at.src[j % kAhead][lane_token + t * (kThreads / LANES)];
+            const uint8_t* from = page + s + lane_atom;
+            if (s >= 0) {
+#pragma unroll
+                for (int k = 0; k < NA; ++k) x[t][k] = *reinterpret_cast<const V*>(from + k * LANES * arr.atom_step);
+            }
         }
     };
-    auto store = [&](int j, const V(&x)[NA]) {
+    auto store = [&](int j, const V(&x)[NT][NA]) {
 #pragma unroll
-        for (int k = 0; k < NA; ++k) {
-            const int t = token_of(k);
-            if (at.src[j % kAhead][t] >= 0)
-                *reinterpret_cast<V*>(page + at.dst[j % kAhead][t] + atom_of(k) * arr.atom_step) = x[k];
+        for (int t = 0; t < NT; ++t) {
+            const int i = lane_token + t * (kThreads / LANES);
+            uint8_t* to = page + at.dst[j % kAhead][i] + lane_atom;
+            if (at.src[j % kAhead][i] >= 0) {
+#pragma unroll
+                for (int k = 0; k < NA; ++k) *reinterpret_cast<V*>(to + k * LANES * arr.atom_step) = x[t][k];
+            }
         }
     };
     const int chunks = (n + kChunk - 1) / kChunk;
@@ -114,7 +120,9 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
         __syncthreads();  // every load of chunk j is done, and chunk j + 2's places are there
         store(j, cur);
 #pragma unroll
-        for (int k = 0; k < NA; ++k) cur[k] = next[k];
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < NA; ++k) cur[t][k] = next[t][k];
     }
 }
 
@@ -137,16 +145,16 @@ __global__ void __launch_bounds__(kThreads) pa_compact_kernel(const CompactParam
     }
     if (n == 0) return;
     switch (arr.kind) {
-    case kRow2: move_chain<uint4, 2, 2>(p, arr, page, unit, n, at); break;
-    case kRow4: move_chain<uint4, 4, 4>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
-    case kRow8: move_chain<uint4, 4, 8>(p, arr, page + part * 8 * arr.atom_step, unit, n, at); break;
-    case kRow16: move_chain<uint4, 4, 16>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kPiece: move_chain<uint4, 4, 1>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
-    case kWide: move_chain<uint32_t, 16, 1>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kHalf: move_chain<uint16_t, 16, 1>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kByte: move_chain<uint8_t, 16, 1>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kWord8: move_chain<uint2, 1, 1>(p, arr, page, unit, n, at); break;
-    default: move_chain<uint32_t, 1, 1>(p, arr, page, unit, n, at); break;
+    case kRow2: move_chain<uint4, 1, 2, 2>(p, arr, page, unit, n, at); break;
+    case kRow4: move_chain<uint4, 1, 4, 4>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
+    case kRow8: move_chain<uint4, 1, 8, 4>(p, arr, page + part * 8 * arr.atom_step, unit, n, at); break;
+    case kRow16: move_chain<uint4, 1, 16, 4>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kPiece: move_chain<uint4, 4, 1, 1>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
+    case kWide: move_chain<uint32_t, 8, 2, 2>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kHalf: move_chain<uint16_t, 8, 2, 2>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kByte: move_chain<uint8_t, 4, 4, 4>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
+    case kWord8: move_chain<uint2, 1, 1, 1>(p, arr, page, unit, n, at); break;
+    default: move_chain<uint32_t, 1, 1, 1>(p, arr, page, unit, n, at); break;
     }
 }
 

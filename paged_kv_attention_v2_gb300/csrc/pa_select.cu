@@ -26,9 +26,9 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kBS = PA_BLOCK_SIZE;
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
-constexpr int kQuads = 8;       // 16-byte loads of a thread in flight
+constexpr int kQuads = 4;       // 16-byte loads of a thread in flight
 constexpr int kCached = 40960;  // keys that a CTA keeps (160 KB); longer parts are read again at every step
 
 struct SelectParams {
@@ -51,25 +51,24 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 // Sum of v over the threads before this one, and over all of them.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warps, uint32_t& total) {
+    static_assert(kThreads == 1024, "a lane for each warp");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
+    auto warp_scan = [&](uint32_t x) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    const uint32_t x = warp_scan(v);
     if (lane == 31) warps[warp] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const uint32_t s = warps[w];
-        before += w < warp ? s : 0;
-        all += s;
-    }
-    total = all;
+    const uint32_t w = warp_scan(warps[lane]);
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const uint32_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
     __syncthreads();
-    return before + x - v;
+    return (warp > 0 ? before : 0) + x - v;
 }
 
 template <bool CACHED, int RANKS>
@@ -147,12 +146,16 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
 #pragma unroll
             for (int k = 0; k < kQuads; ++k) {
                 const int i = i0 + k * kThreads + tid;
-                if (i < quads)
-                    *reinterpret_cast<uint4*>(keys + 4 * i) =
-                        make_uint4(key_of(x[k].x), key_of(x[k].y), key_of(x[k].z), key_of(x[k].w));
+                if (i >= quads) continue;
+                const uint32_t y[4] = {key_of(x[k].x), key_of(x[k].y), key_of(x[k].z), key_of(x[k].w)};
+                *reinterpret_cast<uint4*>(keys + 4 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = t0 + 4 * i + e;
+                    if (t >= lo && t < hi) atomicAdd(&hist[0][y[e] >> 21], 1u);
+                }
             }
         }
-        __syncthreads();
     }
 
     uint32_t prefix = 0;  // digits of the threshold that are known, at their places
@@ -162,31 +165,30 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const uint32_t known = pass == 0 ? 0 : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
             const uint32_t digits = pass == 2 ? 0x3ffu : 0x7ffu;
+            if (!CACHED || pass > 0) {
 #pragma unroll 4
-            for (int i = max(lo - t0, 0) + tid; i < min(mine, hi - t0); i += kThreads) {
-                const uint32_t k = key_at(i);
-                if ((k & known) == prefix) atomicAdd(&hist[pass][k >> shift & digits], 1u);
+                for (int i = max(lo - t0, 0) + tid; i < min(mine, hi - t0); i += kThreads) {
+                    const uint32_t k = key_at(i);
+                    if ((k & known) == prefix) atomicAdd(&hist[pass][k >> shift & digits], 1u);
+                }
             }
             sync_all();
-            // every CTA adds up all histograms: four bins a thread, the highest first
-            uint32_t c[4] = {0, 0, 0, 0}, sum = 0, total;
-            const int bin0 = kBins - 4 - 4 * tid;
+            // every CTA adds up all histograms: two bins a thread, the highest first
+            static_assert(kBins == 2 * kThreads, "two bins a thread");
+            uint32_t c[2] = {0, 0}, total;
+            const int bin0 = kBins - 2 - 2 * tid;
 #pragma unroll
             for (int r = 0; r < ranks; ++r) {
                 const uint32_t* at = &hist[pass][bin0];
-                const uint4 h = *reinterpret_cast<const uint4*>(RANKS == 1 ? at : cluster.map_shared_rank(at, r));
-                c[0] += h.w;
-                c[1] += h.z;
-                c[2] += h.y;
-                c[3] += h.x;
+                const uint2 h = *reinterpret_cast<const uint2*>(RANKS == 1 ? at : cluster.map_shared_rank(at, r));
+                c[0] += h.y;
+                c[1] += h.x;
             }
+            uint32_t above = block_scan(c[0] + c[1], warps, total);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum += c[i];
-            uint32_t above = block_scan(sum, warps, total);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 if (above < left && left <= above + c[i]) {
-                    found[0] = (uint32_t)(bin0 + 3 - i);
+                    found[0] = (uint32_t)(bin0 + 1 - i);
                     found[1] = above;
                 }
                 above += c[i];
@@ -197,50 +199,79 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
             __syncthreads();
         }
     }
-    // runs of successive tokens: those that stay whatever the ties, and those at the threshold
+    // Each thread takes `run` successive tokens of every round of the CTA's: bits of those that stay whatever the
+    // ties, and of those at the threshold.  (run: 4, 12, 20 or 28, so that the 16-byte reads of eight lanes lie in
+    // all banks.)
     const bool any = budget - recent - sink > 0;
     int run = (mine + kThreads - 1) / kThreads;
-    run |= 1;  // odd: no two lanes of a warp in one bank
-    const int a = min(tid * run, mine), b = min(a + run, mine);
-    uint32_t sure = 0, ties = 0;
-    for (int i = a; i < b; ++i) {
-        const int t = t0 + i;
-        if (t < lo || t >= hi) {
-            ++sure;
-        } else if (any) {
-            const uint32_t k = key_at(i);
-            sure += k > prefix;
-            ties += k == prefix;
+    run = run > 20 ? 28 : (run > 12 ? 20 : (run > 4 ? 12 : 4));
+    const int rounds = (mine + run * kThreads - 1) / (run * kThreads);
+    auto look = [&](int round, uint32_t& sure, uint32_t& ties) {
+        const int a = (round * kThreads + tid) * run, count = min(run, mine - a);
+        sure = ties = 0;
+        for (int i = 0; i < count; i += 4) {
+            uint32_t k[4] = {0, 0, 0, 0};
+            if (CACHED && any) {
+                const uint4 v = *reinterpret_cast<const uint4*>(keys + a + i);
+                k[0] = v.x;
+                k[1] = v.y;
+                k[2] = v.z;
+                k[3] = v.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = t0 + a + i + e;
+                if (i + e >= count) continue;
+                if (t < lo || t >= hi) {
+                    sure |= 1u << (i + e);
+                } else if (any) {
+                    if (!CACHED) k[e] = read(t);
+                    sure |= (uint32_t)(k[e] > prefix) << (i + e);
+                    ties |= (uint32_t)(k[e] == prefix) << (i + e);
+                }
+            }
+        }
+    };
+    // Both counts in one scan: 28 tokens of 1024 threads are less than 2^16.
+    static_assert(28 * kThreads < 65536, "two counts to a word");
+    uint32_t sure = 0, ties = 0, before = 0, all = 0;
+    auto count = [&](int round) {
+        look(round, sure, ties);
+        before = block_scan(__popc(ties) << 16 | __popc(sure), warps, all);
+    };
+    uint32_t place = 0, at_threshold = 0;  // tokens that stay, and ties, of the CTAs before this one, then of this one's rounds
+    auto taken = [&](uint32_t n) { return at_threshold < left ? min(n, left - at_threshold) : 0u; };  // of the next n ties
+    if constexpr (RANKS > 1) {
+        uint32_t all_sure = 0, all_ties = 0;
+        for (int round = 0; round < rounds; ++round) {
+            count(round);
+            all_sure += all & 0xffffu;
+            all_ties += all >> 16;
+        }
+        if (tid == 0) {
+            counts[0] = all_sure;
+            counts[1] = all_ties;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            const uint32_t* c = cluster.map_shared_rank(counts, r);
+            const uint32_t s = c[0], e = c[1];
+            place += s + taken(e);
+            at_threshold += e;
         }
     }
-    uint32_t all_sure, all_ties;
-    const uint32_t ties_before = block_scan(ties, warps, all_ties);
-    block_scan(sure, warps, all_sure);
-    if (tid == 0) {
-        counts[0] = all_sure;
-        counts[1] = all_ties;
-    }
-    sync_all();
-    uint32_t place = 0, at_threshold = 0;  // of the CTAs before this one
-    for (int r = 0; r < rank; ++r) {
-        const uint32_t* c = cluster.map_shared_rank(counts, r);
-        const uint32_t s = c[0], e = c[1];
-        const uint32_t take = at_threshold < left ? min(e, left - at_threshold) : 0;
-        place += s + take;
-        at_threshold += e;
-    }
-    uint32_t tie = at_threshold + ties_before, total;
-    const uint32_t take = any && tie < left ? min(ties, left - tie) : 0;
-    place += block_scan(sure + take, warps, total);
-    for (int i = a; i < b; ++i) {
-        const int t = t0 + i;
-        bool stays = t < lo || t >= hi;
-        if (!stays && any) {
-            const uint32_t k = key_at(i);
-            stays = k > prefix || (k == prefix && tie < left);
-            tie += k == prefix;
+    for (int round = 0; round < rounds; ++round) {
+        if (RANKS == 1 || rounds > 1) count(round);
+        const uint32_t ties_before = before >> 16, mine_taken = taken(ties_before + __popc(ties)) - taken(ties_before);
+        for (uint32_t n = mine_taken; n > 0; --n) {  // the lowest ones
+            sure |= ties & (0u - ties);
+            ties &= ties - 1;
         }
-        if (stays) kept[place++] = t;
+        int32_t* to = kept + place + (before & 0xffffu) + taken(ties_before);
+        const int a = t0 + (round * kThreads + tid) * run;
+        for (; sure; sure &= sure - 1) *to++ = a + __ffs(sure) - 1;
+        place += (all & 0xffffu) + taken(all >> 16);
+        at_threshold += all >> 16;
     }
     if constexpr (RANKS > 1) cluster.sync();  // the counts are read by the others
 }

@@ -10,16 +10,18 @@
 //
 // Rounding.  The decision between two codes is whether |x| passes t s g, with t half-way
 // between the two: x has at most 11 significant bits, t s at most 7 and g 24, so the
-// product has up to 31 and fp32 quotients can land on the wrong side.  Two facts settle
+// product has up to 31 and fp32 quotients can land on the wrong side.  Three facts settle
 // it without 64 bits.  |x| >= T holds for the real T if and only if it holds for T
 // rounded up to fp32, and |x| > T if and only if for T rounded down, as x is an fp32
-// number itself: the comparisons of exact_codes and of the scale are exact.  And where
-// both x / (g s) (1 + 2^-20) and x / (g s) (1 - 2^-20) round to the same code, that is the
-// code, whatever the last bits of the quotient: two roundings by the hardware's
-// conversion in place of seven comparisons.  Scales of at most 12 significant bits (the
-// usual 1 or a power of two among them) meet exact ties often, and none nearer than
-// 2^-19: there the quotient by one residual step (Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990) is right wherever it matters.
+// number itself: the comparisons of exact_codes and exact_scale are exact.  A quotient
+// that is a few steps of fp32 off is on the wrong side only where T lies within a few steps
+// of a number of x's own 11 (bf16: 8) bits: with the seven t's these are four significands
+// (those of s g, 3 s g, 5 s g and 7 s g), looked at once for 16 elements, and in one
+// block of 250 (bf16: 2000) the exact comparisons are needed.  And scales g of at most 12
+// significant bits (the usual 1 or a power of two among them), whose T do lie on such
+// numbers, meet none nearer than 2^-19 but them: there the quotient by one residual step
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) is right wherever it matters.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -35,7 +37,7 @@
 namespace {
 
 constexpr int kBS = PA_BLOCK_SIZE;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Scale4 {
     float g, inv;  // the tensor's scale and its reciprocal
@@ -54,10 +56,15 @@ struct Append4Params {
     int32_t* dev_error;
 };
 
-// Two numbers rounded to e2m1 codes, the first in the low half of the byte.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-    uint16_t d;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u16.u8 %0, b;\n\t}" : "=h"(d) : "f"(hi), "f"(lo));
+// Eight numbers rounded to e2m1 codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
+    uint32_t d;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(d)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return d;
 }
 
@@ -68,21 +75,27 @@ __device__ __forceinline__ float2 e4m3_pair(uint32_t c) {
     return pa::unpack2<false>(h);
 }
 
-// e4m3(amax / (6 g)) as a code, for a finite or infinite amax >= 0.
-__device__ __forceinline__ uint32_t scale_code(float amax, const Scale4& q) {
-    const float estimate = amax * q.inv * (1.f / 6);
-    uint32_t c = __nv_cvt_float_to_fp8(estimate, __NV_SATFINITE, __NV_E4M3);  // at most one code off
+// e4m3(amax / (6 g)) as a code from one that is at most one off.  Not inlined: few blocks come here.
+__device__ __noinline__ uint32_t exact_scale(uint32_t c, float amax, float g) {
     // 6 (half-way above c) g and 6 (half-way below c) g: 7 significant bits times g
     const float2 above = e4m3_pair(c);
     const float up = 3.f * (above.x + above.y);
     const bool odd = c & 1;
-    const bool more = c < 0x7e && (odd ? amax >= __fmul_ru(up, q.g) : amax > __fmul_rd(up, q.g));
-    if (more) return c + 1;
+    if (c < 0x7e && (odd ? amax >= __fmul_ru(up, g) : amax > __fmul_rd(up, g))) return c + 1;
     if (c > 0) {
         const float2 below = e4m3_pair(c - 1);
         const float down = 3.f * (below.x + below.y);
-        if (!(odd ? amax > __fmul_rd(down, q.g) : amax >= __fmul_ru(down, q.g))) --c;
+        if (!(odd ? amax > __fmul_rd(down, g) : amax >= __fmul_ru(down, g))) --c;
     }
+    return c;
+}
+
+// The same for a finite or infinite amax >= 0.
+__device__ __forceinline__ uint32_t scale_code(float amax, const Scale4& q) {
+    const float estimate = amax * q.inv * (1.f / 6);  // a few steps of fp32 off
+    const uint32_t c = __nv_cvt_float_to_fp8(estimate, __NV_SATFINITE, __NV_E4M3), u = __float_as_uint(estimate);
+    // within 16 steps of half-way between two normal numbers, or among the subnormal ones
+    if (((u - 0x80000u + 16u) & 0xfffffu) <= 32u || estimate < 0x1p-6f) return exact_scale(c, amax, q.g);
     return c;
 }
 
@@ -109,47 +122,60 @@ __device__ __noinline__ uint2 exact_codes(const uint4 a, const uint4 b, float s,
     return make_uint2(o[0], o[1]);
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t b) {  // of pairs; a NaN stays one
+    uint32_t d;
+    if constexpr (BF16)
+        asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.NaN.f16x2 %0, x, y;\n\t}" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Codes of a block and the code of its scale.
 template <bool BF16>
 __device__ __forceinline__ uint2 quantise(const uint4 a, const uint4 b, const Scale4& q, uint32_t& scale) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    // the largest magnitude: 16-bit patterns without their signs order as the numbers, NaN last
-    uint32_t m = w[0] & 0x7fff7fffu;
+    uint32_t m = max_magnitude<BF16>(w[0], w[1]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-    const uint32_t top = max(m >> 16, m & 0xffffu);
-    if (top > (BF16 ? 0x7f80u : 0x7c00u)) {  // a NaN: so is the whole block
+    for (int i = 2; i < 8; ++i) m = max_magnitude<BF16>(m, w[i]);
+    const float2 top = pa::unpack2<BF16>(m);
+    const float amax = fmaxf(top.x, top.y);
+    if (top.x != top.x || top.y != top.y) {  // a NaN: so is the whole block
         scale = 0x7f;
         return make_uint2(0, 0);
     }
-    const float amax = pa::unpack2<BF16>(top).x;
     scale = scale_code(amax, q);
     if (scale == 0) return make_uint2(0, 0);
     const float s = e4m3_pair(scale - 1).y;
     const float p = s * q.g, inv = __frcp_rn(p);
-    if (!(p >= 0x1p-100f && p <= 0x1p100f)) return exact_codes<BF16>(a, b, s, q.g);
-    uint32_t o[2] = {0, 0};
-    if (q.brief) {
+    bool exact = !(p >= 0x1p-100f && p <= 0x1p100f);
+    float y[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 x = pa::unpack2<BF16>(w[i]);
-            const float y0 = x.x * inv, y1 = x.y * inv;
-            o[i >> 2] |= e2m1x2(fmaf(-fmaf(y0, p, -x.x), inv, y0), fmaf(-fmaf(y1, p, -x.y), inv, y1)) << (8 * (i & 3));
-        }
-        // (an infinite quotient: the residual is NaN)
-        if (!(amax * inv <= 0x1p60f)) return exact_codes<BF16>(a, b, s, q.g);
-    } else {
-        const float more = inv * (1.f + 0x1p-20f), less = inv * (1.f - 0x1p-20f);
-        uint32_t u[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 x = pa::unpack2<BF16>(w[i]);
-            o[i >> 2] |= e2m1x2(x.x * more, x.y * more) << (8 * (i & 3));
-            u[i >> 2] |= e2m1x2(x.x * less, x.y * less) << (8 * (i & 3));
-        }
-        if (o[0] != u[0] || o[1] != u[1]) return exact_codes<BF16>(a, b, s, q.g);
+    for (int i = 0; i < 8; ++i) {
+        const float2 x = pa::unpack2<BF16>(w[i]);
+        y[2 * i] = x.x;
+        y[2 * i + 1] = x.y;
     }
-    return make_uint2(o[0], o[1]);
+    if (q.brief) {
+        exact |= !(amax * inv <= 0x1p60f);  // (an infinite quotient: its residual is NaN)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = y[i] * inv;
+            y[i] = fmaf(-fmaf(v, p, -y[i]), inv, v);
+        }
+    } else {
+        // whether a border lies within 8 steps of a number of x's precision
+        constexpr uint32_t kLow = BF16 ? 0xffffu : 0x1fffu;
+#pragma unroll
+        for (int t = 1; t < 8; t += 2) exact |= ((__float_as_uint(t * p) + 8u) & kLow) <= 16u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] *= inv;
+    }
+    if (exact) return exact_codes<BF16>(a, b, s, q.g);
+    const float lo[8] = {y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
+    const float hi[8] = {y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]};
+    return make_uint2(e2m1x8(lo), e2m1x8(hi));
 }
 
 // Rows [blockIdx.x * rows, ...) of one head, ITEMS blocks of 16 a thread.

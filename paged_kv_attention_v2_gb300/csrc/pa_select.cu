@@ -340,10 +340,12 @@ extern "C" pa_status pa_select_tokens(const pa_select_args* a, void* stream) {
     p.recent = a->recent;
     int dev = 0, sms = 0;
     if (!pa::device_and_sms(&dev, &sms)) return PA_ERR_LAUNCH;
-    // CTAs of a cluster: more while each has over 4096 tokens and they all fit at once
+    // CTAs of a cluster: more while each has over 4096 tokens and all of them take at most half of the SMs (a cluster
+    // of eight wants eight free SMs of one part of the GPU: sixteen such clusters ran one after the other,
+    // 4 x 100000 36 us, in clusters of four 19)
     const int64_t units = (int64_t)a->num_seqs * a->num_kv_heads;
     int ranks = 1;
-    while (ranks < 8 && a->max_seq_len > 4096 * ranks && units * ranks * 2 <= 2 * (int64_t)sms) ranks *= 2;
+    while (ranks < 8 && a->max_seq_len > 4096 * ranks && units * ranks * 4 <= sms) ranks *= 2;
     while (ranks < 8 && (a->max_seq_len + ranks - 1) / ranks + PA_BLOCK_SIZE > kCached) ranks *= 2;
     const int64_t pages = (a->max_seq_len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE, part = (pages + ranks - 1) / ranks * PA_BLOCK_SIZE;
     const size_t smem = (size_t)part * 4;

@@ -1026,10 +1026,12 @@ __device__ __forceinline__ void softmax_page(float (&z)[NT][4], float (&m)[NT][2
     }
 }
 
-// The same for PP pages at once: one vote and at most one rescale for all of them.
+// The same for PP pages at once: one vote and at most one rescale for all of them.  Logits, m
+// and mx are in units of `unit` (> 0).
 template <int PP, int NT, int KT, bool MQ>
 __device__ __forceinline__ void softmax_pages(float (&z)[PP][NT][4], float (&m)[NT][2], float (&mx)[NT][2], float (&l)[NT][2],
-                                              float (&acc)[KT][NT][4], bool edge) {
+                                              float (&acc)[KT][NT][4], bool edge, float unit) {
+    const float to_log2 = unit * kLog2e;
     bool need = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -1039,7 +1041,7 @@ __device__ __forceinline__ void softmax_pages(float (&z)[PP][NT][4], float (&m)[
 #pragma unroll
             for (int g = 1; g < PP; ++g) a = fmaxf(a, fmaxf(z[g][nt][e], z[g][nt][e + 2]));
             mx[nt][e] = fmaxf(mx[nt][e], a);
-            need |= a - m[nt][e] > kLazyMax;  // -inf - -inf: false
+            need |= (a - m[nt][e]) * unit > kLazyMax;  // -inf - -inf: false
         }
     if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -1050,7 +1052,7 @@ __device__ __forceinline__ void softmax_pages(float (&z)[PP][NT][4], float (&m)[
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
                 const float mr = (MQ && mn == -INFINITY) ? 0.f : mn;  // (see softmax_page)
-                const float al = exp2f((m[nt][e] - mr) * kLog2e);
+                const float al = exp2f((m[nt][e] - mr) * to_log2);
                 m[nt][e] = mn;
                 l[nt][e] *= al;
 #pragma unroll
@@ -1067,8 +1069,8 @@ __device__ __forceinline__ void softmax_pages(float (&z)[PP][NT][4], float (&m)[
             const float mr = (MQ && edge && m[nt][e] == -INFINITY) ? 0.f : m[nt][e];
 #pragma unroll
             for (int g = 0; g < PP; ++g) {
-                z[g][nt][e] = exp2f((z[g][nt][e] - mr) * kLog2e);
-                z[g][nt][e + 2] = exp2f((z[g][nt][e + 2] - mr) * kLog2e);
+                z[g][nt][e] = exp2f((z[g][nt][e] - mr) * to_log2);
+                z[g][nt][e + 2] = exp2f((z[g][nt][e + 2] - mr) * to_log2);
                 l[nt][e] += z[g][nt][e] + z[g][nt][e + 2];
             }
         }
@@ -1079,7 +1081,7 @@ __device__ __forceinline__ void softmax_pages(float (&z)[PP][NT][4], float (&m)[
 // and acc once.
 template <int NT, int KT>
 __device__ __forceinline__ void settle_max(float (&m)[NT][2], float (&mx)[NT][2], float (&l)[NT][2],
-                                           float (&acc)[KT][NT][4]) {
+                                           float (&acc)[KT][NT][4], float unit = 1.f) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float mn0 = mx[nt][0], mn1 = mx[nt][1];
@@ -1089,8 +1091,8 @@ __device__ __forceinline__ void settle_max(float (&m)[NT][2], float (&mx)[NT][2]
             mn1 = fmaxf(mn1, __shfl_xor_sync(0xffffffffu, mn1, o));
         }
         // equal (also both -inf: no key seen): nothing to move
-        const float al0 = mn0 == m[nt][0] ? 1.f : exp2f((m[nt][0] - mn0) * kLog2e);
-        const float al1 = mn1 == m[nt][1] ? 1.f : exp2f((m[nt][1] - mn1) * kLog2e);
+        const float al0 = mn0 == m[nt][0] ? 1.f : exp2f((m[nt][0] - mn0) * (unit * kLog2e));
+        const float al1 = mn1 == m[nt][1] ? 1.f : exp2f((m[nt][1] - mn1) * (unit * kLog2e));
         m[nt][0] = mn0;
         m[nt][1] = mn1;
         l[nt][0] *= al0;
@@ -1881,6 +1883,10 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
     const int tv = (cq << 2) + (cq & 1), tv1 = (cq << 2) + (~cq & 1);  // k-indices 2cq, 2cq + 1 (+ 8: two tokens on)
     const bool has_alibi = p.alibi != nullptr;
     const bool has_cap = p.softcap > 0.f;
+    // Logits are kept in units of `unit`: sums of products, which the exponent's argument scales in one step,
+    // unless something else is done to them (a scale that does not keep their order is such a thing).
+    const bool special = has_cap || has_alibi || !(p.scale > 1e-30f);
+    const float unit = special ? 1.f : p.scale;
     uint32_t gbase = 0;
     uint32_t mphase = 0;
     for (int k = 0;; ++k) {
@@ -1978,14 +1984,12 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                 continue;
             }
 
-            // the whole pages to registers, and the stage back to the producer (a page that the tile's last stage
-            // lacks is another one in its place, all of it masked)
+            // (a page that the tile's last stage lacks is another one in its place, all of it masked)
             uint32_t kw[PP][2][KW], ks[PP][2];   // rows r and r + 8
             uint32_t vw[PP][4][VW], vs[PP][4];   // k-indices 2cq, 2cq + 1, 2cq + 8, 2cq + 9
 #pragma unroll
             for (int g = 0; g < PP; ++g) {
                 const uint32_t kp = sm.ring + st * C::kStageBytes + (first + g) * C::kPageBytes;
-                const uint32_t vp = kp + C::kStageBytes / 2;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int t = h ? thi : tlo;
@@ -2001,20 +2005,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ks[g][h]) : "r"(b));
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = (i & 1 ? tv1 : tv) + (i >> 1) * 2;
-                    const uint32_t a = vp + (uint32_t)(t * (HEAD / 2) + r * (HEAD / 16));
-                    const uint32_t b = vp + kScales + (uint32_t)(t * (HEAD / 16) + (HEAD == 128 ? r : r >> 1));
-                    if constexpr (HEAD == 128)
-                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[g][i][0]), "=r"(vw[g][i][1]) : "r"(a));
-                    else
-                        vw[g][i][0] = lds32(a);
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(vs[g][i]) : "r"(b));
-                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vs[PP - 1][3], p.zero);
 
             float z[PP][NT][4];
 #pragma unroll
@@ -2048,19 +2039,32 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                     }
                 }
             }
+            // the values to registers (after the keys are done with theirs), and the stage back to the producer
 #pragma unroll
-            for (int g = 0; g < PP; ++g)
+            for (int g = 0; g < PP; ++g) {
+                const uint32_t vp = sm.ring + st * C::kStageBytes + C::kStageBytes / 2 + (first + g) * C::kPageBytes;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) z[g][nt][e] *= p.scale;
-            if (has_cap || has_alibi) {
+                for (int i = 0; i < 4; ++i) {
+                    const int t = (i & 1 ? tv1 : tv) + (i >> 1) * 2;
+                    const uint32_t a = vp + (uint32_t)(t * (HEAD / 2) + r * (HEAD / 16));
+                    const uint32_t b = vp + kScales + (uint32_t)(t * (HEAD / 16) + (HEAD == 128 ? r : r >> 1));
+                    if constexpr (HEAD == 128)
+                        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vw[g][i][0]), "=r"(vw[g][i][1]) : "r"(a));
+                    else
+                        vw[g][i][0] = lds32(a);
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(vs[g][i]) : "r"(b));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_after(sm.empty + st * 8, vs[PP - 1][3], p.zero);
+            if (special) {  // (without, z stays a sum of products and unit is the logit scale)
 #pragma unroll
                 for (int g = 0; g < PP; ++g)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
+                            z[g][nt][e] *= p.scale;
                             if (has_cap) z[g][nt][e] = soft_cap<false>(p, z[g][nt][e]);
                             if (has_alibi) z[g][nt][e] += sl[nt][e & 1] * (float)(tok0 + g * kBS + ((e >> 1) ? thi : tlo) - origin);
                         }
@@ -2084,7 +2088,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                     }
                 }
             }
-            softmax_pages<PP, NT, KT, C::kMQ>(z, m, mx, l, acc, edge);
+            softmax_pages<PP, NT, KT, C::kMQ>(z, m, mx, l, acc, edge, unit);
 #pragma unroll
             for (int g = 0; g < PP; ++g) {
                 uint32_t pb[NT][2];
@@ -2116,7 +2120,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
             }
         }
 
-        settle_max<NT, KT>(m, mx, l, acc);
+        settle_max<NT, KT>(m, mx, l, acc, unit);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -2136,8 +2140,8 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                 *reinterpret_cast<float2*>(mw + (h0 + 1) * C::kMergeStride + d0) = make_float2(acc[mt][nt][1], acc[mt][nt][3]);
             }
             if (r == 0) {
-                sm.ml[warp * C::kMergeRows + h0] = make_float2(m[nt][0], l[nt][0]);
-                sm.ml[warp * C::kMergeRows + h0 + 1] = make_float2(m[nt][1], l[nt][1]);
+                sm.ml[warp * C::kMergeRows + h0] = make_float2(m[nt][0] * unit, l[nt][0]);
+                sm.ml[warp * C::kMergeRows + h0 + 1] = make_float2(m[nt][1] * unit, l[nt][1]);
             }
         }
         if (!consumer_sync(sm, mphase, lane)) {

@@ -1069,8 +1069,8 @@ __device__ __forceinline__ void softmax_pages(float (&z)[PP][NT][4], float (&m)[
             const float mr = (MQ && edge && m[nt][e] == -INFINITY) ? 0.f : m[nt][e];
 #pragma unroll
             for (int g = 0; g < PP; ++g) {
-                z[g][nt][e] = exp2f((z[g][nt][e] - mr) * to_log2);
-                z[g][nt][e + 2] = exp2f((z[g][nt][e + 2] - mr) * to_log2);
+                z[g][nt][e] = exp2_ftz((z[g][nt][e] - mr) * to_log2);
+                z[g][nt][e + 2] = exp2_ftz((z[g][nt][e + 2] - mr) * to_log2);
                 l[nt][e] += z[g][nt][e] + z[g][nt][e + 2];
             }
         }

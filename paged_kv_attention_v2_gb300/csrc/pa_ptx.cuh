@@ -326,6 +326,13 @@ __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& l
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
 }
 
+// 2^x by the hardware's approximation, below 2^-126 zero (exp2f scales those in steps of its own).
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (BF16) {

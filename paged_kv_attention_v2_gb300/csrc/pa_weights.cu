@@ -68,6 +68,10 @@ extern "C" pa_status pa_add_weights(const pa_weights_args* a, void* stream) {
     p.softcap = a->softcap > 0.f ? a->softcap : 0.f;
     p.inv_softcap = a->softcap > 0.f ? 1.f / a->softcap : 0.f;
     p.decay = a->decay;
+    const int64_t block_bytes = (int64_t)a->num_kv_heads * a->head_size *
+                                (kv == PA_KV_FP4_E2M1 ? 9 : PA_BLOCK_SIZE * (kv != PA_KV_SAME ? 1 : (a->dtype == PA_DTYPE_F32 ? 4 : 2)));
+    if (block_bytes > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    p.block_bytes = (uint32_t)block_bytes;
     const int elem = kv != PA_KV_SAME ? 1 : (a->dtype == PA_DTYPE_F32 ? 4 : 2);
     p.token_step = a->layout == PA_LAYOUT_NHD ? a->head_size * elem : 16;
     p.piece_step = a->layout == PA_LAYOUT_NHD ? 16 : 16 * PA_BLOCK_SIZE;

@@ -10,9 +10,11 @@
 // from memory to the registers of the tensor-core operand: tokens on M, rows on N, and
 // the head dims in whatever order 16-byte loads bring them, the query's fragments in the
 // same one.  Lane (r, cq) holds the 16-byte pieces cq, cq + 4, ... of the keys of tokens r
-// and r + 8, in either layout.  A warp takes pages warp, warp + kWarps, ... of the CTA's tile
-// and loads one page while it works on the one before.  Four lanes then share a
-// token's sum; no atomics, so results do not depend on the run.
+// and r + 8, in either layout.  A warp takes pages warp, warp + kWeightWarps, ... of the CTA's tile
+// and loads one page while it works on the one before.  (Two or three pages ahead cost
+// registers, so warps, and a wait for one page's loads is one for the later ones too: 32 x 4096
+// fp16 38 us; a ring of asynchronous copies in shared memory 41 to 46.)  Four lanes then
+// share a token's sum; no atomics, so results do not depend on the run.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -27,7 +29,7 @@
 
 namespace pa {
 
-constexpr int kWeightWarps = 4;
+constexpr int kWeightWarps = 8;
 
 struct WeightParams {
     float* scores;
@@ -42,6 +44,7 @@ struct WeightParams {
     int32_t* dev_error;
     int num_seqs, num_heads, num_kv_heads, group, num_blocks, max_blocks_per_seq, max_seq_len, max_parts;
     int max_q_len, num_q_rows, window_left, tile_pages, tiles;  // tiles of the longest sequence
+    uint32_t block_bytes;        // from a block of the cache to the next
     int token_step, piece_step;  // bytes between the tokens, and between the 16-byte pieces of one, in a page
     float scale, softcap, inv_softcap, decay;
 };
@@ -69,23 +72,30 @@ struct PageKeys {
     uint32_t k[2][kWords];
     uint32_t s[2];  // 4-bit: the scales of a lane's one or two blocks
 
-    // this lane's pieces of tokens r and r + 8 of the page at `page`
-    __device__ __forceinline__ void load(const uint8_t* page, const WeightParams& p, int r, int cq) {
+    // Bytes from a page's start to this lane's first piece of token r, and (4-bit) to its scales of that token.
+    static __device__ __forceinline__ int offset(const WeightParams& p, int r, int cq) {
+        return kFp4 ? r * (HEAD / 2) + cq * (HEAD / 8) : r * p.token_step + cq * p.piece_step;
+    }
+    static __device__ __forceinline__ int scale_offset(int r, int cq) {
+        return 8 * HEAD + r * (HEAD / 16) + cq * (HEAD / 64);
+    }
+
+    // this lane's pieces of tokens r and r + 8, from its own pointers
+    __device__ __forceinline__ void load(const uint8_t* at, const uint8_t* scales, const WeightParams& p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int t = r + 8 * h;
             if constexpr (kFp4) {
-                const uint8_t* a = page + t * (HEAD / 2) + cq * (HEAD / 8);
-                const uint8_t* b = page + 8 * HEAD + t * (HEAD / 16) + cq * (HEAD / 64);
+                const uint8_t* a = at + 8 * h * (HEAD / 2);
+                const uint8_t* b = scales + 8 * h * (HEAD / 16);
                 if constexpr (HEAD == 128) {
-                    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(a));
+                    const uint4 v = *reinterpret_cast<const uint4*>(a);
                     k[h][0] = v.x;
                     k[h][1] = v.y;
                     k[h][2] = v.z;
                     k[h][3] = v.w;
                     s[h] = *reinterpret_cast<const uint16_t*>(b);
                 } else {
-                    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(a));
+                    const uint2 v = *reinterpret_cast<const uint2*>(a);
                     k[h][0] = v.x;
                     k[h][1] = v.y;
                     s[h] = *b;
@@ -93,7 +103,7 @@ struct PageKeys {
             } else {
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
-                    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(page + t * p.token_step + (cq + 4 * i) * p.piece_step));
+                    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(at + 8 * h * p.token_step + 4 * i * p.piece_step));
                     k[h][4 * i] = v.x;
                     k[h][4 * i + 1] = v.y;
                     k[h][4 * i + 2] = v.z;
@@ -254,7 +264,11 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     // keys that some row sees: [seen0, len)
     const int seen0 = p.window_left >= 0 ? max(0, len - qn - p.window_left) : 0;
 
-    const int64_t head_page = (int64_t)p.num_kv_heads;
+    // this lane's places in block 0; a block further, block_bytes further
+    const uint8_t* lane_keys = static_cast<const uint8_t*>(p.key_cache) + kvh * Page::kPageBytes + Page::offset(p, r, cq);
+    const uint8_t* lane_scales = static_cast<const uint8_t*>(p.key_cache) + kvh * Page::kPageBytes + Page::scale_offset(r, cq);
+    float* lane_score = p.scores + kvh * BS + r + 8 * (cq & 1);
+    auto score_of = [&](int blk) { return lane_score + (uint64_t)(uint32_t)blk * (uint32_t)(p.num_kv_heads * BS); };
     auto check = [&](int page, int blk) {
         if (page >= page1) return -1;
         if ((unsigned)blk >= (unsigned)p.num_blocks) {
@@ -266,9 +280,9 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     // A page's keys and this lane's old score: lanes with cq 0 and 1 own tokens r and r + 8.
     auto load = [&](int page, int blk, Page& k, float& old) {
         if (blk < 0) return;
-        const int64_t at = (int64_t)blk * head_page + kvh;
-        if ((page + 1) * BS > seen0 && GE > 0) k.load(static_cast<const uint8_t*>(p.key_cache) + at * Page::kPageBytes, p, r, cq);
-        if (cq < 2 && p.decay != 0.f) old = p.scores[at * BS + r + 8 * cq];
+        const uint64_t off = (uint64_t)(uint32_t)blk * p.block_bytes;
+        if ((page + 1) * BS > seen0 && GE > 0) k.load(lane_keys + off, lane_scales + off, p);
+        if (cq < 2 && p.decay != 0.f) old = *score_of(blk);
     };
     Page cur, next;
     float old_cur = 0.f, old_next = 0.f;
@@ -329,6 +343,9 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     // tokens [all0, all1) are seen by every row
     const int all0 = p.window_left >= 0 ? max(0, len - 1 - p.window_left) : 0, all1 = len - qn + 1;
 
+    const bool special = p.softcap > 0.f || p.alibi;
+    const float to_log2 = special ? kLog2 : p.scale * kLog2;  // (scale and exponent in one step)
+
     for (; page < page1; page += kWeightWarps) {
         load(page + kWeightWarps, blk_next, next, old_next);
         const int after = page + 2 * kWeightWarps, blk_after = after < page1 ? table[after] : -1;
@@ -338,15 +355,12 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
             if (tok + BS > seen0 && GE > 0) {
                 float z[NT][4];
                 cur.products(q, z);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) z[nt][e] *= p.scale;
-                if (p.softcap > 0.f || p.alibi) {
+                if (special) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
+                            z[nt][e] *= p.scale;
                             if (p.softcap > 0.f) z[nt][e] = p.softcap * tanhf(z[nt][e] * p.inv_softcap);
                             if (p.alibi) z[nt][e] = fmaf(slope[nt][e & 1], (float)(tok + r + 8 * (e >> 1) - (len - 1)), z[nt][e]);
                         }
@@ -355,7 +369,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        z[nt][e] = there[nt][e & 1] ? exp2f(fmaf(z[nt][e], kLog2, -lev[nt][e & 1])) : 0.f;
+                        z[nt][e] = there[nt][e & 1] ? exp2_ftz(fmaf(z[nt][e], to_log2, -lev[nt][e & 1])) : 0.f;
                 if (tok < all0 || tok + BS > all1) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -381,7 +395,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
                 const float w = cq ? sum[1] : sum[0];
                 // this call's tokens have no score yet
                 const float v = p.decay == 0.f || t >= len - qn ? w : fmaf(p.decay, old_cur, w);
-                p.scores[((int64_t)blk * head_page + kvh) * BS + r + 8 * cq] = v;
+                *score_of(blk) = v;
             }
         }
         cur = next;
@@ -391,9 +405,9 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     }
 }
 
-// Tiles: as many as fit on the GPU at once, each a whole number of rounds of a CTA's warps (a tile's first
-// page comes some three dependent loads after its CTA starts, and its rows' statistics are read again),
-// but of at most kTilePages pages, as sequences of a batch differ in length.
+// Tiles: as many as fit on the GPU at once, or whole rounds of that where they would have more than kTilePages
+// pages (a tile's first page comes some three dependent loads after its CTA starts, and its
+// rows' statistics are read again, so few long ones), each a whole number of rounds of a CTA's warps.
 constexpr int kTilePages = 128;
 
 template <typename T, int HEAD, int KV, int NT>
@@ -408,8 +422,9 @@ bool launch_weights_rows(WeightParams& p, int sms, void* stream) {
         if (dev < kHostDevices) resident[dev].store(occ);
     }
     const int64_t pages = (p.max_seq_len + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE, units = (int64_t)p.num_seqs * p.num_kv_heads;
-    int64_t per = (int64_t)sms * occ / units;  // tiles of a sequence's head
-    if (per < (pages + kTilePages - 1) / kTilePages) per = (pages + kTilePages - 1) / kTilePages;
+    const int64_t fit = (int64_t)sms * occ, least = (pages + kTilePages - 1) / kTilePages;  // tiles of a sequence's head
+    int64_t per = (units * least + fit - 1) / fit * fit / units;
+    if (per < least) per = least;
     int64_t tile = (pages + per - 1) / per;
     tile = (tile + kWeightWarps - 1) / kWeightWarps * kWeightWarps;
     p.tile_pages = (int)tile;

@@ -100,7 +100,8 @@ pa_status pa_build_tables(const pa_tables_args* args, void* stream);
  *     scale = e4m3(max|x| / (6 g)),   code = e2m1(x / (g scale)),
  * the real quotients rounded once, half to even, beyond the largest value: that value
  * (an infinity too).  A scale that comes out zero makes all 16 codes zero; a NaN among the
- * elements makes the scale NaN and the codes zero.
+ * elements makes the scale NaN and the codes zero.  (Of a slot given twice, the codes of an
+ * element and its scale may be of different rows.)
  *
  * Keys and values have head counts and sizes of their own: num_kv_heads of
  * head_size for pa_decode, twice the heads for the keys and twice the size for
@@ -151,7 +152,8 @@ pa_status pa_append_kv(const pa_append_args* args, void* stream);
  * sets every token (the scores of a prompt, by its last tokens).  Tokens outside the window
  * only fade.  Sums are fp32, in an order that does not depend on the run.  Places behind a
  * sequence's end keep their scores; a page whose block id is out of range is skipped
- * (PA_DEVERR_BLOCK_ID).
+ * (PA_DEVERR_BLOCK_ID).  Each page belongs to one sequence: two that share one would both write
+ * its scores.  num_kv_heads pages of keys of one block are less than 2^31 bytes.
  */
 typedef struct pa_weights_args {
     float* scores;               /* [num_blocks][num_kv_heads][16], updated in place */

@@ -113,7 +113,7 @@ typedef enum pa_mode { PA_MODE_AUTO = 0, PA_MODE_V1 = 1, PA_MODE_V2 = 2 } pa_mod
 #define PA_DEVERR_TIMEOUT    4  /* an internal pipeline wait exceeded its limit; results invalid   */
 #define PA_DEVERR_QUERY_RANGE 8 /* fp8 or 4-bit caches with a bf16 query: |q| > 65504 clamped (fp16 MMAs)  */
 #define PA_DEVERR_POOL       16 /* pa_build_tables: too few free pages, or a pool state that cannot be */
-#define PA_DEVERR_SLOT       32 /* pa_append_kv: a slot past the cache; skipped */
+#define PA_DEVERR_SLOT       32 /* pa_append_kv: a slot past the cache; skipped.  pa_compact_kv: a position that does not ascend */
 
 typedef struct pa_decode_args {
     /* [rows][num_heads][head_size], dtype; written.  16-byte aligned.

@@ -63,21 +63,34 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
     const int tid = threadIdx.x, seq = unit / p.num_kv_heads;
     const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
     const int32_t* kept = p.kept + (int64_t)unit * p.max_budget;
-    // Places of chunk j.  Written while the stores of chunk j - 3 may still be reading theirs, so there are four.
-    auto plan = [&](int j) {
+    // Places of a chunk: each token's kept position is read one chunk before its pages' ids are looked up, so that
+    // no chunk waits for both.  Written while the stores of the chunk three before may still be reading theirs, so
+    // there are four.
+    struct Token {
+        int k, before;  // its position and the one kept before it
+    };
+    auto fetch = [&](int j) {
         const int i = j * kChunk + tid;
+        Token t = {0, -1};
+        if ((kChunk == kThreads || tid < kChunk) && i < n) {
+            t.k = kept[i];
+            if (i > 0) t.before = kept[i - 1];
+        }
+        return t;
+    };
+    auto plan = [&](int j, const Token& t) {
         if (kChunk < kThreads && tid >= kChunk) return;
+        const int i = j * kChunk + tid;
         int64_t src = -1, dst = 0;
         if (i < n) {
-            const int k = kept[i], before = i > 0 ? kept[i - 1] : -1;
-            if (k < i || k <= before || k >= p.max_blocks_per_seq * kBS) {
+            if (t.k < i || t.k <= t.before || t.k >= p.max_blocks_per_seq * kBS) {
                 if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_SLOT);
-            } else if (k > i) {
-                const int from = table[k / kBS], to = table[i / kBS];
+            } else if (t.k > i) {
+                const int from = table[t.k / kBS], to = table[i / kBS];
                 if ((unsigned)from >= (unsigned)p.num_blocks || (unsigned)to >= (unsigned)p.num_blocks) {
                     if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
                 } else {
-                    src = from * arr.block_bytes + k % kBS * arr.token_step;
+                    src = from * arr.block_bytes + t.k % kBS * arr.token_step;
                     dst = to * arr.block_bytes + i % kBS * arr.token_step;
                 }
             }
@@ -110,13 +123,17 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
         }
     };
     const int chunks = (n + kChunk - 1) / kChunk;
-    plan(0);
-    plan(1);
+    const Token first = fetch(0), second = fetch(1);
+    Token token = fetch(2);
+    plan(0, first);
+    plan(1, second);
     __syncthreads();
     load(0, cur);
     for (int j = 0; j < chunks; ++j) {
+        const Token after = fetch(j + 3);
         load(j + 1, next);
-        plan(j + 2);
+        plan(j + 2, token);
+        token = after;
         __syncthreads();  // every load of chunk j is done, and chunk j + 2's places are there
         store(j, cur);
 #pragma unroll

@@ -205,3 +205,47 @@ def test_decode_schedules_merges_and_replays():
 
 def test_a_scale_of_one_by_default():
     _decode("f16", 128, 2, 4, [100, 200], ks=1.0, vs=1.0)
+
+
+@pytest.mark.parametrize("mode,group", [("v1", 4), ("v2", 4), ("v2", 12)])
+def test_a_withheld_page_times_out(mode, group):
+    """The bounded waits of the 4-bit kernels: a page that never comes ends the call with an error."""
+    from paged_kv_attention_v2_gb300 import _abi
+    lib = _abi.load()
+    gen, size, kv_heads = torch.Generator().manual_seed(2), 128, 2
+    caches = [torch.randint(0, 256, (130, kv_heads, 9 * size), generator=gen, dtype=torch.uint8) for _ in range(2)]
+    for c in caches:
+        c[:, :, 8 * size:] = 0x38  # scales of one
+    caches = [c.to(DEV) for c in caches]
+    q = torch.randn((3, kv_heads * group, size), generator=gen).half().to(DEV)
+    out, err = torch.zeros_like(q), _int([0])
+    ws = pa.alloc_workspace(3, kv_heads * group, size, 1300, DEV)
+    call = lambda: pa.pa_decode(out, q, *caches, _int(np.arange(246).reshape(3, 82) % 130), _int([700, 1300, 90]), mode=mode,  # noqa: E731
+                                num_kv_heads=kv_heads, scale=0.05, max_seq_len=1300, layout="nhd", kv_dtype="e2m1", dev_error=err, **ws)
+    call()
+    want = out.clone()
+    assert int(err) == 0 and torch.isfinite(want).all()
+    assert lib.pa_debug_withhold_page(1, 50_000_000) == 0  # 50 ms per wait
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        assert lib.pa_debug_withhold_page(0, 0) == 0
+    assert int(err) & pa.PA_DEVERR_TIMEOUT
+    err.zero_()
+    out.zero_()
+    call()
+    assert int(err) == 0 and torch.equal(out, want)
+
+
+def test_a_query_beyond_fp16_is_clamped_and_reported():
+    c = torch.full((1, 1, 576), 0x38, dtype=torch.uint8, device=DEV)
+    ws = pa.alloc_workspace(1, 1, 64, 16, DEV)
+    for value, flagged in ((65280.0, False), (65536.0, True), (-1e30, True), (float("inf"), True)):
+        q = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device=DEV)
+        q[0, 0, 5] = value
+        out, err = torch.empty_like(q), _int([0])
+        pa.pa_decode(out, q, c, c, _int([[0]]), _int([9]), num_kv_heads=1, scale=1e-6, max_seq_len=16, layout="nhd", kv_dtype="e2m1",
+                     dev_error=err, **ws)
+        assert int(err) == (8 if flagged else 0), value  # PA_DEVERR_QUERY_RANGE
+        assert torch.isfinite(out.float()).all()

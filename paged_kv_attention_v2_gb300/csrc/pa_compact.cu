@@ -26,13 +26,14 @@ constexpr int kBS = PA_BLOCK_SIZE;
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;         // chunks whose places are in shared memory (see move_chain)
 
-// One array of the cache, in atoms: atom a of a token's head is at page + a * atom_step + token * token_step.
+// One array of the cache, in atoms: a token's are token * token_step into its page, a fixed step of the layout apart.
 struct Array {
     uint8_t* base;
     int64_t block_bytes;  // from a block to the next
     int head_bytes;       // from a head's page to the next
     int heads;            // heads to a kv head
-    int token_step, atom_step;
+    int token_step;
+    int chain_bytes;      // from a chain's first atom to the next one's
     int chains;           // per head
     int kind;             // kRow4 ..
 };
@@ -55,8 +56,8 @@ struct Places {
 
 // Moves a chain: LANES * NA atoms of type V of every token, from the first one of `page` (block 0's) on.  LANES
 // neighbouring threads have successive atoms of a token, each of them NA of those, LANES apart, of each of NT
-// tokens of a chunk.
-template <typename V, int NA, int LANES, int NT>
+// tokens of a chunk.  STEP: bytes between successive atoms.
+template <typename V, int NA, int LANES, int NT, int STEP>
 __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& arr, uint8_t* page, int unit, int n, Places& at) {
     constexpr int kChunk = kThreads / LANES * NT;  // tokens at once
     static_assert(kChunk <= kThreads, "a thread to plan each token");
@@ -98,7 +99,7 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
         at.src[j % kAhead][tid] = src;
         at.dst[j % kAhead][tid] = dst;
     };
-    const int lane_token = tid / LANES, lane_atom = tid % LANES * arr.atom_step;
+    const int lane_token = tid / LANES, lane_atom = tid % LANES * STEP;
     V cur[NT][NA], next[NT][NA];
     auto load = [&](int j, V(&x)[NT][NA]) {
 #pragma unroll
@@ -107,7 +108,7 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
             const uint8_t* from = page + s + lane_atom;
             if (s >= 0) {
 #pragma unroll
-                for (int k = 0; k < NA; ++k) x[t][k] = *reinterpret_cast<const V*>(from + k * LANES * arr.atom_step);
+                for (int k = 0; k < NA; ++k) x[t][k] = *reinterpret_cast<const V*>(from + k * LANES * STEP);
             }
         }
     };
@@ -118,7 +119,7 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
             uint8_t* to = page + at.dst[j % kAhead][i] + lane_atom;
             if (at.src[j % kAhead][i] >= 0) {
 #pragma unroll
-                for (int k = 0; k < NA; ++k) *reinterpret_cast<V*>(to + k * LANES * arr.atom_step) = x[t][k];
+                for (int k = 0; k < NA; ++k) *reinterpret_cast<V*>(to + k * LANES * STEP) = x[t][k];
             }
         }
     };
@@ -162,16 +163,16 @@ __global__ void __launch_bounds__(kThreads) pa_compact_kernel(const CompactParam
     }
     if (n == 0) return;
     switch (arr.kind) {
-    case kRow2: move_chain<uint4, 1, 2, 2>(p, arr, page, unit, n, at); break;
-    case kRow4: move_chain<uint4, 1, 4, 4>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
-    case kRow8: move_chain<uint4, 1, 8, 4>(p, arr, page + part * 8 * arr.atom_step, unit, n, at); break;
-    case kRow16: move_chain<uint4, 1, 16, 4>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kPiece: move_chain<uint4, 4, 1, 1>(p, arr, page + part * 4 * arr.atom_step, unit, n, at); break;
-    case kWide: move_chain<uint32_t, 8, 2, 2>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kHalf: move_chain<uint16_t, 8, 2, 2>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kByte: move_chain<uint8_t, 4, 4, 4>(p, arr, page + part * 16 * arr.atom_step, unit, n, at); break;
-    case kWord8: move_chain<uint2, 1, 1, 1>(p, arr, page, unit, n, at); break;
-    default: move_chain<uint32_t, 1, 1, 1>(p, arr, page, unit, n, at); break;
+    case kRow2: move_chain<uint4, 1, 2, 2, 16>(p, arr, page, unit, n, at); break;
+    case kRow4: move_chain<uint4, 1, 4, 4, 16>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kRow8: move_chain<uint4, 1, 8, 4, 16>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kRow16: move_chain<uint4, 1, 16, 4, 16>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kPiece: move_chain<uint4, 4, 1, 1, 256>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kWide: move_chain<uint32_t, 8, 2, 2, 64>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kHalf: move_chain<uint16_t, 8, 2, 2, 32>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kByte: move_chain<uint8_t, 4, 4, 4, 16>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kWord8: move_chain<uint2, 1, 1, 1, 8>(p, arr, page, unit, n, at); break;
+    default: move_chain<uint32_t, 1, 1, 1, 4>(p, arr, page, unit, n, at); break;
     }
 }
 
@@ -205,7 +206,7 @@ extern "C" pa_status pa_compact_kv(const pa_compact_args* a, void* stream) {
         return PA_ERR_INVALID_ARG;
 
     CompactParams p = {};
-    const int kSlice = 256;
+    const int kSlice = 256;  // bytes of a row to a chain (64: 102 us where 256 have 98, 32 x 16384 to 2048 bf16)
     const int e = kv != PA_KV_SAME ? 1 : (a->dtype == PA_DTYPE_F32 ? 4 : 2);
     for (int v = 0; v < 2; ++v) {
         Array& arr = p.arrays[v];
@@ -217,18 +218,18 @@ extern "C" pa_status pa_compact_kv(const pa_compact_args* a, void* stream) {
         if (a->layout == PA_LAYOUT_NHD) {
             const int row = fp4 ? d / 2 : d * e;
             arr.token_step = row;
-            arr.atom_step = 16;
             const int wide = row < kSlice ? row : kSlice;
             arr.chains = row / wide;
+            arr.chain_bytes = wide;
             arr.kind = wide == 32 ? kRow2 : (wide == 64 ? kRow4 : (wide == 128 ? kRow8 : kRow16));
         } else if (!v) {
             arr.token_step = 16;
-            arr.atom_step = 16 * kBS;
+            arr.chain_bytes = 4 * 16 * kBS;
             arr.chains = d * e / 64;
             arr.kind = kPiece;
         } else {
             arr.token_step = e;
-            arr.atom_step = e * kBS;
+            arr.chain_bytes = 16 * e * kBS;
             arr.chains = d / 16;
             arr.kind = e == 4 ? kWide : (e == 2 ? kHalf : kByte);
         }

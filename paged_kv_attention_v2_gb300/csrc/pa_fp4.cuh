@@ -28,6 +28,13 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16(uint32_t w) {
     return d;
 }
 
+// The larger magnitude of two f16x2 pairs, element by element (of NaN and a number the number).
+__device__ __forceinline__ uint32_t max_magnitude_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.f16x2 %0, x, y;\n\t}" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Products of f16x2 pairs (a code times a scale: at most six significant bits, between
 // 2^-10 and 2688, so exact).
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {

@@ -904,6 +904,59 @@ __device__ void tile_epilogue(const Params& p, const TileDesc& d, const Smem& sm
     }
 }
 
+// The same for 4-bit pages with one n-tile and four consumer warps, whose tiles are short: a lane for each (row,
+// warp) works out what that partial state counts for, once, and every warp then sums two rows (head size 64: one
+// turn of two rows) of four columns a lane.  (4 x 100000: 65.8 -> 63.9 us against the general form.)
+template <class C, typename T, int HEAD, int NC>
+__device__ __forceinline__ void tile_epilogue_short(const Params& p, const TileDesc& d, const Smem& sm, int warp, int lane) {
+    static_assert(C::kMaxG * NC == 32, "a lane for each row and warp");
+    constexpr int LPR = HEAD / 4, RPW = 32 / LPR;  // lanes to a row, rows of a warp at once
+    const int G = p.group, qn = C::kMQ ? d.qn : 1, GE = qn * G;
+    const float2 e = sm.ml[(lane & 3) * C::kMergeRows + (lane >> 2)];
+    float M = fmaxf(e.x, __shfl_xor_sync(0xffffffffu, e.x, 1));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+    const float c = e.x == -INFINITY ? 0.f : exp2f((e.x - M) * kLog2e);
+    float L = c * e.y;
+    L += __shfl_xor_sync(0xffffffffu, L, 1);
+    L += __shfl_xor_sync(0xffffffffu, L, 2);
+    const float f = L > 0.f ? c * (p.v_scale / L) : 0.f;
+#pragma unroll
+    for (int h0 = 0; h0 < C::kMaxG; h0 += NC * RPW) {
+        const int h = h0 + warp * RPW + lane / LPR, d4 = lane % LPR;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NC; ++w) {
+            const float fw = __shfl_sync(0xffffffffu, f, 4 * h + w);
+            const float4 a = *reinterpret_cast<const float4*>(sm.merge + (w * C::kMergeRows + h) * C::kMergeStride + C::merge_col(4 * d4));
+            if (h < GE) {  // (rows that there are none hold nothing to be trusted)
+                o.x = fmaf(fw, a.x, o.x);
+                o.y = fmaf(fw, a.y, o.y);
+                o.z = fmaf(fw, a.z, o.z);
+                o.w = fmaf(fw, a.w, o.w);
+            }
+        }
+        const float row_m = __shfl_sync(0xffffffffu, M, 4 * h), row_l = __shfl_sync(0xffffffffu, L, 4 * h);
+        if (h >= GE) continue;
+        const int qi = C::kMQ ? h / G : 0;
+        const int head = d.kvh * G + (h - qi * G);
+        const int64_t sh = (int64_t)(d.q0 + qi) * p.num_heads + head;
+        if (p.v1) {
+            uint2 v;
+            v.x = pack2<C::kBF16>(o.x, o.y);
+            v.y = pack2<C::kBF16>(o.z, o.w);
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + sh * HEAD + 4 * d4) = v;
+        } else {
+            const int64_t ps = sh * p.max_parts + d.part;
+            st_global_v4_hint(p.tmp_out + ps * HEAD + 4 * d4, o, l2_policy_evict_last());
+            if (d4 == 0) {
+                // relative to the sequence's last token (see tile_epilogue)
+                p.max_logits[ps] = p.alibi ? row_m + p.alibi[head] * (float)(d.tok_end - d.len) : row_m;
+                p.exp_sums[ps] = row_l;
+            }
+        }
+    }
+}
+
 template <typename T, int HEAD, bool L2ONLY>
 __device__ __forceinline__ void merge_row_warp(const Params& p, int64_t row, int h, int len, int qn, int qi,
                                                int lane);
@@ -937,7 +990,10 @@ template <class C, typename T, int HEAD, int NC>
 __device__ bool tile_finish(const Params& p, const TileDesc& d, const Smem& sm, int warp, int lane,
                             uint32_t& mphase) {
     const int tid = warp * 32 + lane;
-    tile_epilogue<C, T, HEAD, NC>(p, d, sm, tid);
+    if constexpr (C::kFp4 && C::kMaxG * NC == 32)
+        tile_epilogue_short<C, T, HEAD, NC>(p, d, sm, warp, lane);
+    else
+        tile_epilogue<C, T, HEAD, NC>(p, d, sm, tid);
     if (!consumer_sync(sm, mphase, lane)) return false;  // epilogue done, merge buffers free
     if (!p.fused || p.v1) return true;
     if (tid == 0) {
@@ -1903,7 +1959,7 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
 
         // Q as fp16 B fragments: k-step j of lane cq is head dims HEAD cq / 4 + 4j .. + 3.
         uint32_t qb[NT][KT][2];
-        uint32_t q_top = 0;  // bf16: largest magnitudes, as 16-bit patterns
+        uint32_t q_top = 0;  // bf16: largest magnitudes
         const uint32_t qs = sm.q + slot * C::kQBytes;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -1915,17 +1971,17 @@ __device__ void consumer_mma_fp4(const Params& p, const Smem& sm, int warp, int 
                     const uint32_t a = qs + (uint32_t)((v * HEAD + cq * (HEAD / 4) + 4 * j) * 2);
                     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(a));
                     if constexpr (QBF) {
-                        q_top = __vmaxu2(q_top, __vmaxu2(w0 & 0x7fff7fffu, w1 & 0x7fff7fffu));
                         w0 = bf16x2_to_f16(w0);
                         w1 = bf16x2_to_f16(w1);
+                        q_top = max_magnitude_f16x2(max_magnitude_f16x2(w0, w1), q_top);
                     }
                 }
                 qb[nt][j][0] = w0;
                 qb[nt][j][1] = w1;
             }
         }
-        // beyond 65504 (the largest bf16 number below 65536 is 65280), clamped; a NaN stays one
-        if (QBF && ((q_top & 0xffffu) - 0x4780u < 0x3801u || (q_top >> 16) - 0x4780u < 0x3801u)) report(p, PA_DEVERR_QUERY_RANGE);
+        // 65504, which no bf16 number is: one beyond it, clamped (a NaN stays one)
+        if (QBF && ((q_top & 0xffffu) == 0x7bffu || q_top >> 16 == 0x7bffu)) report(p, PA_DEVERR_QUERY_RANGE);
         const uint32_t qlast = last_query_word<C, KT>(qb[NT - 1]);
         __syncwarp();
         if (lane == 0) mbar_arrive_after(sm.td_empty + slot * 8, qlast, p.zero);

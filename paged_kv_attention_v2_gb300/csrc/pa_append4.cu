@@ -6,7 +6,9 @@
 // A thread takes one block of 16: 32 bytes in, 8 bytes of codes and one of scale out, so
 // nothing is exchanged but the scales of a row, which go out as one store.  Eight (head
 // size 64: four) lanes make up a row, and the rows of successive slots lie side by side
-// in the page.
+// in the page.  Two blocks to a thread, CTAs of 128 threads: 32768 tokens of 8 + 8 heads of
+// 128, bf16, 30.8 us (172 MB: 25.4 at the copy rate; one block 35, four 35, 256 threads
+// 32).  The bytes alone take 26.5: the rest is the quantiser's issue slots.
 //
 // Rounding.  The decision between two codes is whether |x| passes t s g, with t half-way
 // between the two: x has at most 11 significant bits, t s at most 7 and g 24, so the

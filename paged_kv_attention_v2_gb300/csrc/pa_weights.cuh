@@ -15,6 +15,8 @@
 // registers, so warps, and a wait for one page's loads is one for the later ones too: 32 x 4096
 // fp16 38 us; a ring of asynchronous copies in shared memory 41 to 46.)  Four lanes then
 // share a token's sum; no atomics, so results do not depend on the run.
+// Measured: 32 x 4096 fp16, groups of seven, 24.6 us (139 MB: 20.4 at the copy rate; bound by
+// memory), 4 x 100000 over 4-bit keys 38.5 (18.9; by issue slots).
 #pragma once
 
 #include <cuda_runtime.h>

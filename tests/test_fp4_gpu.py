@@ -121,7 +121,7 @@ def test_append_slots_outside():
 # ------------------------------------------------------------------ decode
 
 def _decode(dtype, size, kv_heads, group, lens, mode="v2", q_len=None, window=-1, cap=0.0, alibi=False, seed=0, static=False,
-            dynamic=False, counters=False, graph=False, ks=0.0019, vs=0.0023):
+            dynamic=False, counters=False, graph=False, ks=0.0019, vs=0.0023, scale=None, ready=False):
     rng, gen = np.random.default_rng(seed), torch.Generator().manual_seed(seed)
     n, heads = len(lens), kv_heads * group
     own = [-(-x // 16) for x in lens]
@@ -144,8 +144,9 @@ def _decode(dtype, size, kv_heads, group, lens, mode="v2", q_len=None, window=-1
     slopes = np.array([2.0 ** (-8 * (i + 1) / heads) for i in range(heads)], dtype=np.float32) if alibi else None
     top = max(max(lens), 1)
     out, err = torch.full((rows, heads, size), 7.0, dtype=TORCH[dtype], device=DEV), _int([0])
-    kw = dict(num_kv_heads=kv_heads, scale=size ** -0.5, max_seq_len=top, layout="nhd", kv_dtype="e2m1", k_scale=ks, v_scale=vs,
-              window_left=window, softcap=cap, alibi_slopes=None if slopes is None else torch.from_numpy(slopes).to(DEV), dev_error=err)
+    scale = size ** -0.5 if scale is None else scale
+    kw = dict(num_kv_heads=kv_heads, scale=scale, max_seq_len=top, layout="nhd", kv_dtype="e2m1", k_scale=ks, v_scale=vs,
+              metadata_ready=ready, window_left=window, softcap=cap, alibi_slopes=None if slopes is None else torch.from_numpy(slopes).to(DEV), dev_error=err)
     if q_len:
         kw.update(query_start=_int(start), max_query_len=max(q_len))
     if dynamic:
@@ -166,7 +167,7 @@ def _decode(dtype, size, kv_heads, group, lens, mode="v2", q_len=None, window=-1
             g.replay()
     torch.cuda.synchronize()
     assert int(err) == 0
-    want = attention(q.double().numpy(), k, v, lens, start, group, size ** -0.5, cap, slopes, window)
+    want = attention(q.double().numpy(), k, v, lens, start, group, scale, cap, slopes, window)
     got = out.double().cpu().numpy()
     absolute, relative = TOL[dtype]
     assert np.all(np.abs(got - want) <= absolute + relative * np.abs(want)), np.abs(got - want).max()
@@ -201,10 +202,47 @@ def test_decode_schedules_merges_and_replays():
     _decode("bf16", 128, 8, 4, [3000, 40, 1, 2000, 700], mode="auto", dynamic=True, graph=True)
     _decode("f16", 64, 2, 4, [300] * 40, mode="auto", graph=True)
     _decode("f16", 128, 2, 7, [700, 1300], static=True)
+    _decode("f16", 128, 4, 7, [900] * 6, graph=True, ready=True)
+    _decode("bf16", 64, 8, 2, [3000, 40, 1, 2000, 700], mode="auto", dynamic=True, graph=True, ready=True)
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1e-33, 2.0])
+def test_decode_at_any_logit_scale(scale):
+    _decode("f16", 64, 2, 3, [300, 700], scale=scale)
+    _decode("bf16", 128, 1, 12, [5, 40], "v1", [1, 1], scale=scale)
 
 
 def test_a_scale_of_one_by_default():
     _decode("f16", 128, 2, 4, [100, 200], ks=1.0, vs=1.0)
+
+
+def test_blocks_beyond_four_gigabytes():
+    """Append, decode, weights and compaction of pages whose places pass 32 bits."""
+    blocks, heads, size, n = 520000, 8, 128, 40
+    gen = torch.Generator().manual_seed(8)
+    kc, vc = (torch.zeros((blocks, heads, 9 * size), dtype=torch.uint8, device=DEV) for _ in range(2))
+    assert kc.numel() > 1 << 32
+    far, near = np.array([blocks - 1, blocks - 7, blocks - 3]), np.array([1, 5, 2])
+    rows = [torch.randn((n, heads, size), generator=gen).half().to(DEV) for _ in range(2)]
+    q = torch.randn((1, heads, size), generator=gen).half().to(DEV)
+    kept = torch.arange(0, n, 2, dtype=torch.int32, device=DEV).expand(1, heads, -1).contiguous()
+    results = []
+    for pages in (far, near):
+        slots = pages[np.arange(n) // 16] * 16 + np.arange(n) % 16
+        pa.pa_append_kv(*rows, kc, vc, _int(slots), layout="nhd", kv_dtype="e2m1", k_scale=0.0019, v_scale=0.0019)
+        out, ws = torch.empty_like(q), pa.alloc_workspace(1, heads, size, n, DEV)
+        kw = dict(num_kv_heads=heads, scale=size ** -0.5, max_seq_len=n, layout="nhd", kv_dtype="e2m1", k_scale=0.0019)
+        table, lens = _int(pages[None]), _int([n])
+        pa.pa_decode(out, q, kc, vc, table, lens, mode="v2", v_scale=0.0019, **kw, **ws)
+        scores = torch.zeros((blocks, heads, 16), device=DEV)
+        pa.pa_add_weights(scores, q, kc, table, lens, ws["exp_sums"], ws["max_logits"], **kw)
+        seen = scores[torch.from_numpy(pages).to(DEV)].clone()
+        pa.pa_compact_kv(kc, vc, table, kept, _int([n // 2]), scores=scores, layout="nhd", kv_dtype="e2m1")
+        at = torch.from_numpy(pages).to(DEV)
+        results.append((out, seen, kc[at].clone(), vc[at].clone(), scores[at].clone()))
+        assert abs(float(seen.sum()) - heads) < 1e-3  # a whole softmax for every head
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("mode,group", [("v1", 4), ("v2", 4), ("v2", 12)])

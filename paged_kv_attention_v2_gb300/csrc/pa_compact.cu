@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kBS = PA_BLOCK_SIZE;
 constexpr int kThreads = 256;
+constexpr unsigned kSingle = 1u << 16;  // above the bytes that __byte_perm reads
 constexpr int kAhead = 4;         // chunks whose places are in shared memory (see move_chain)
 
 // One array of the cache, in atoms: a token's are token * token_step into its page, a fixed step of the layout apart.
@@ -53,16 +54,23 @@ struct CompactParams {
 };
 
 struct Places {
-    int64_t src[kAhead][kThreads], dst[kAhead][kThreads];  // byte offsets of the tokens' first atoms; src < 0: stays
+    alignas(16) int64_t src[kAhead][kThreads];  // byte offsets of the tokens' first atoms; src < 0: stays
+    alignas(16) int64_t dst[kAhead][kThreads];
 };
 
 // Moves a chain: LANES * NA atoms of type V of every token, from the first one of `page` (block 0's) on.  LANES
 // neighbouring threads have successive atoms of a token, each of them NA of those, LANES apart, of each of NT
 // tokens of a chunk.  STEP: bytes between successive atoms.
-template <typename V, int NA, int LANES, int NT, int STEP>
+// With an element type S, an atom is two tokens' elements side by side (split values of 16 and 8 bits): a thread loads
+// the one or two atoms that hold the pair it stores, and stores them at once.  An atom read that way may hold a
+// neighbour that went or belongs to another pair of this chunk; a chunk's loads still come before its stores, and a
+// chunk begins at an even token, so none is read that an earlier chunk's store may be writing.
+template <typename V, int NA, int LANES, int NT, int STEP, typename S = void>
 __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& arr, uint8_t* page, int unit, int n, Places& at) {
-    constexpr int kChunk = kThreads / LANES * NT;  // tokens at once
+    constexpr bool kPairs = !std::is_void<S>::value;
+    constexpr int kChunk = kThreads / LANES * NT * (kPairs ? 2 : 1);  // tokens at once
     static_assert(kChunk <= kThreads, "a thread to plan each token");
+    static_assert(!kPairs || kChunk % 32 == 0, "whole warps plan pairs");
     const int tid = threadIdx.x, seq = unit / p.num_kv_heads;
     const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
     const int32_t* kept = p.kept + (int64_t)unit * p.max_budget;
@@ -88,7 +96,7 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
         if (i < n) {
             if (t.k < i || t.k <= t.before || t.k >= p.max_blocks_per_seq * kBS) {
                 if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_SLOT);
-            } else if (t.k > i) {
+            } else if (kPairs || t.k > i) {
                 const int from = table[t.k / kBS], to = table[i / kBS];
                 if ((unsigned)from >= (unsigned)p.num_blocks || (unsigned)to >= (unsigned)p.num_blocks) {
                     if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
@@ -98,14 +106,58 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
                 }
             }
         }
+        if constexpr (kPairs) {
+            // The even token's thread has the pair: its atoms (the second -1 where one holds both), the place and
+            // the bytes of the result; kSingle where the other token of the pair is not moved.
+            constexpr int E = (int)sizeof(V) / 2;
+            const int64_t src1 = __shfl_down_sync(~0u, src, 1), dst1 = __shfl_down_sync(~0u, dst, 1);
+            if (tid % 2 != 0) return;
+            int64_t a = -1, b = -1, to = dst;
+            unsigned bytes = 0;
+            if (src >= 0 && src1 >= 0) {
+                if (src != dst || src1 != dst1) {
+                    a = src & -(int64_t)sizeof(V);
+                    b = src1 & -(int64_t)sizeof(V);
+                    unsigned lo = src & E, hi = src1 & E;
+                    if (b == a) b = -1;
+                    else hi += 4;
+                    bytes = E == 2 ? (lo | (lo + 1) << 4 | hi << 8 | (hi + 1) << 12) : (lo | hi << 4);
+                }
+            } else if (src >= 0 || src1 >= 0) {
+                const int64_t from = src >= 0 ? src : src1;
+                to = src >= 0 ? dst : dst1;
+                if (from != to) {
+                    a = from & -(int64_t)sizeof(V);
+                    const unsigned lo = from & E;
+                    bytes = kSingle | lo | (lo + 1) << 4;
+                }
+            }
+            *reinterpret_cast<longlong2*>(&at.src[j % kAhead][tid]) = make_longlong2(a, b);
+            *reinterpret_cast<longlong2*>(&at.dst[j % kAhead][tid]) = make_longlong2(to, (int64_t)bytes);
+            return;
+        }
         at.src[j % kAhead][tid] = src;
         at.dst[j % kAhead][tid] = dst;
     };
     const int lane_token = tid / LANES, lane_atom = tid % LANES * STEP;
-    V cur[NT][NA], next[NT][NA];
-    auto load = [&](int j, V(&x)[NT][NA]) {
+    constexpr int kRegs = kPairs ? 2 * NA : NA;
+    V cur[NT][kRegs], next[NT][kRegs];
+    auto load = [&](int j, V(&x)[NT][kRegs]) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+            if constexpr (kPairs) {
+                const longlong2 s = *reinterpret_cast<const longlong2*>(&at.src[j % kAhead][2 * (lane_token + t * (kThreads / LANES))]);
+                const uint8_t *a = page + s.x + lane_atom, *b = page + s.y + lane_atom;
+                if (s.x >= 0) {
+#pragma unroll
+                    for (int k = 0; k < NA; ++k) x[t][k] = *reinterpret_cast<const V*>(a + k * LANES * STEP);
+                }
+                if (s.y >= 0) {
+#pragma unroll
+                    for (int k = 0; k < NA; ++k) x[t][NA + k] = *reinterpret_cast<const V*>(b + k * LANES * STEP);
+                }
+                continue;
+            }
             const int64_t s = at.src[j % kAhead][lane_token + t * (kThreads / LANES)];
             const uint8_t* from = page + s + lane_atom;
             if (s >= 0) {
@@ -114,9 +166,24 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
             }
         }
     };
-    auto store = [&](int j, const V(&x)[NT][NA]) {
+    auto store = [&](int j, const V(&x)[NT][kRegs]) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+            if constexpr (kPairs) {
+                const int i = 2 * (lane_token + t * (kThreads / LANES));
+                const longlong2 d = *reinterpret_cast<const longlong2*>(&at.dst[j % kAhead][i]);
+                uint8_t* to = page + d.x + lane_atom;
+                const unsigned bytes = (unsigned)d.y;
+                if (at.src[j % kAhead][i] >= 0) {
+#pragma unroll
+                    for (int k = 0; k < NA; ++k) {
+                        const unsigned v = __byte_perm(x[t][k], x[t][NA + k], bytes);
+                        if (bytes & kSingle) *reinterpret_cast<S*>(to + k * LANES * STEP) = (S)v;
+                        else *reinterpret_cast<V*>(to + k * LANES * STEP) = (V)v;
+                    }
+                }
+                continue;
+            }
             const int i = lane_token + t * (kThreads / LANES);
             uint8_t* to = page + at.dst[j % kAhead][i] + lane_atom;
             if (at.src[j % kAhead][i] >= 0) {
@@ -142,7 +209,7 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < NA; ++k) cur[t][k] = next[t][k];
+            for (int k = 0; k < kRegs; ++k) cur[t][k] = next[t][k];
     }
 }
 
@@ -171,8 +238,8 @@ __global__ void __launch_bounds__(kThreads) pa_compact_kernel(const CompactParam
     case kRow16: move_chain<uint4, 1, 16, 4, 16>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
     case kPiece: move_chain<uint4, 4, 1, 1, 256>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
     case kWide: move_chain<uint32_t, 8, 2, 2, 64>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
-    case kHalf: move_chain<uint16_t, 8, 2, 2, 32>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
-    case kByte: move_chain<uint8_t, 4, 4, 4, 16>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kHalf: move_chain<uint32_t, 4, 4, 2, 32, uint16_t>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
+    case kByte: move_chain<uint16_t, 4, 4, 2, 16, uint8_t>(p, arr, page + part * arr.chain_bytes, unit, n, at); break;
     case kWord8: move_chain<uint2, 1, 1, 1, 8>(p, arr, page, unit, n, at); break;
     default: move_chain<uint32_t, 1, 1, 1, 4>(p, arr, page, unit, n, at); break;
     }

@@ -16,7 +16,7 @@
 // fp16 38 us; a ring of asynchronous copies in shared memory 41 to 46.)  Four lanes then
 // share a token's sum; no atomics, so results do not depend on the run.
 // Measured: 32 x 4096 fp16, groups of seven, 24.6 us (139 MB: 20.4 at the copy rate; bound by
-// memory), 4 x 100000 over 4-bit keys 38.5 (18.9; by issue slots).
+// memory), 4 x 100000 over 4-bit keys 31.5 (18.9; by issue slots).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     pdl_launch_dependents();
     pdl_wait_primary();
     const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
-    // the first two pages' ids, with the lengths: which of them there are is seen below
-    int page = tile * p.tile_pages + warp;
-    int blk = page < p.max_blocks_per_seq ? table[page] : -1;
-    int blk_next = page + kWeightWarps < p.max_blocks_per_seq ? table[page + kWeightWarps] : -1;
+    // the ids of this warp's pages (the i-th is first + kWeightWarps i), a lane each, with the lengths: which of them
+    // there are is seen below
+    const int first = tile * p.tile_pages + warp, mine = first + kWeightWarps * lane;
+    int ids = mine < p.max_blocks_per_seq ? table[mine] : -1;
     int len = p.seq_lens[seq];
     if (len < 0 || len > p.max_seq_len) {
         if (threadIdx.x == 0 && tile == 0 && kvh == 0) weights_report(p, PA_DEVERR_SEQ_LEN);
@@ -271,26 +271,24 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     const uint8_t* lane_scales = static_cast<const uint8_t*>(p.key_cache) + kvh * Page::kPageBytes + Page::scale_offset(r, cq);
     float* lane_score = p.scores + kvh * BS + r + 8 * (cq & 1);
     auto score_of = [&](int blk) { return lane_score + (uint64_t)(uint32_t)blk * (uint32_t)(p.num_kv_heads * BS); };
-    auto check = [&](int page, int blk) {
-        if (page >= page1) return -1;
-        if ((unsigned)blk >= (unsigned)p.num_blocks) {
-            if (lane == 0) weights_report(p, PA_DEVERR_BLOCK_ID);
-            return -1;
-        }
-        return blk;
-    };
-    // A page's keys and this lane's old score: lanes with cq 0 and 1 own tokens r and r + 8.
+    const int mine_n = (page1 - first + kWeightWarps - 1) / kWeightWarps;  // (up to 32; none: at most 0)
+    if (lane < mine_n && (unsigned)ids >= (unsigned)p.num_blocks) weights_report(p, PA_DEVERR_BLOCK_ID);
+    if (lane >= mine_n || (unsigned)ids >= (unsigned)p.num_blocks) ids = -1;
+    auto id = [&](int i) { return i < mine_n ? __shfl_sync(0xffffffffu, ids, i) : -1; };  // (out of range: -1)
+    const int seen = GE > 0 ? seen0 : 0x7fffffff;
+    // A page's keys and this lane's old score: lanes with cq 0 and 1 own tokens r and r + 8.  A page that is not
+    // there, or that no row sees, is block 0 instead, read and not used (loads in branches, and each page's id read and
+    // looked at in its turn: 34.0 us against 32.0, 4 x 100000 e2m1).
     auto load = [&](int page, int blk, Page& k, float& old) {
-        if (blk < 0) return;
-        const uint64_t off = (uint64_t)(uint32_t)blk * p.block_bytes;
-        if ((page + 1) * BS > seen0 && GE > 0) k.load(lane_keys + off, lane_scales + off, p);
-        if (cq < 2 && p.decay != 0.f) old = *score_of(blk);
+        const uint32_t b = (page + 1) * BS > seen ? max(blk, 0) : 0;
+        const uint64_t off = (uint64_t)b * p.block_bytes;
+        k.load(lane_keys + off, lane_scales + off, p);
+        old = *score_of(max(blk, 0));
     };
     Page cur, next;
     float old_cur = 0.f, old_next = 0.f;
-    blk = check(page, blk);
-    blk_next = check(page + kWeightWarps, blk_next);
-    load(page, blk, cur, old_cur);
+    int blk = id(0), blk_next = -1;
+    load(first, blk, cur, old_cur);
 
     uint32_t q[NT][Page::kQWords], top = 0;
 #pragma unroll
@@ -339,7 +337,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
         for (int e = 0; e < 2; ++e) {
             const int v = nt * 8 + 2 * cq + e;
             there[nt][e] = v < GE;
-            lev[nt][e] = level[v] * kLog2;
+            lev[nt][e] = v < GE ? level[v] * kLog2 : INFINITY;
             slope[nt][e] = p.alibi && v < GE ? p.alibi[kvh * G + v % G] : 0.f;
         }
     // tokens [all0, all1) are seen by every row
@@ -348,67 +346,72 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     const bool special = p.softcap > 0.f || p.alibi;
     const float to_log2 = special ? kLog2 : p.scale * kLog2;  // (scale and exponent in one step)
 
-    for (; page < page1; page += kWeightWarps) {
-        load(page + kWeightWarps, blk_next, next, old_next);
-        const int after = page + 2 * kWeightWarps, blk_after = after < page1 ? table[after] : -1;
-        if (blk >= 0) {
-            const int tok = page * BS;
-            float w = 0.f;
-            if (tok + BS > seen0 && GE > 0) {
-                float z[NT][4], sum[2] = {0.f, 0.f};
-                cur.products(q, z);
-                if (special) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            z[nt][e] *= p.scale;
-                            if (p.softcap > 0.f) z[nt][e] = p.softcap * tanhf(z[nt][e] * p.inv_softcap);
-                            if (p.alibi) z[nt][e] = fmaf(slope[nt][e & 1], (float)(tok + r + 8 * (e >> 1) - (len - 1)), z[nt][e]);
-                        }
-                }
+    // pages [in0, in1): every token is seen by every row and is older than this call's, so nothing is masked
+    const int in0 = max((all0 + BS - 1) / BS, (seen0 + BS - 1) / BS), in1 = GE > 0 ? min(all1, len - qn) / BS : 0;
+    auto work = [&](int page, int blk, const Page& keys, float old) {
+        if (blk < 0) return;
+        const int tok = page * BS;
+        const bool edge = page < in0 || page >= in1;
+        float w = 0.f;
+        if (!edge || (tok + BS > seen0 && GE > 0)) {
+            float z[NT][4], sum[2] = {0.f, 0.f};
+            keys.products(q, z);
+            if (special) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[nt][e] = there[nt][e & 1] ? exp2_ftz(fmaf(z[nt][e], to_log2, -lev[nt][e & 1])) : 0.f;
-                if (tok < all0 || tok + BS > all1) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int t = tok + r + 8 * (e >> 1), pos = len - qn + (nt * 8 + 2 * cq + (e & 1)) / G;
-                            if (t > pos || (p.window_left >= 0 && t < pos - p.window_left)) z[nt][e] = 0.f;
-                        }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sum[0] += z[nt][0] + z[nt][1];
-                    sum[1] += z[nt][2] + z[nt][3];
-                }
-                // lane cq 0 gets the first one's sum over the four lanes, cq 1 the second one's
-                const float give = cq & 1 ? sum[0] : sum[1], keep = cq & 1 ? sum[1] : sum[0];
-                w = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-                w += __shfl_xor_sync(0xffffffffu, w, 2);
+                    for (int e = 0; e < 4; ++e) {
+                        z[nt][e] *= p.scale;
+                        if (p.softcap > 0.f) z[nt][e] = p.softcap * tanhf(z[nt][e] * p.inv_softcap);
+                        if (p.alibi) z[nt][e] = fmaf(slope[nt][e & 1], (float)(tok + r + 8 * (e >> 1) - (len - 1)), z[nt][e]);
+                    }
             }
-            const int t = tok + r + 8 * cq;
-            if (cq < 2 && t < len) {
-                // this call's tokens have no score yet
-                const float v = p.decay == 0.f || t >= len - qn ? w : fmaf(p.decay, old_cur, w);
-                *score_of(blk) = v;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    // (4-bit keys are finite or NaN for every row: rows that are not there need only their level)
+                    z[nt][e] = Page::kFp4 || there[nt][e & 1] ? exp2_ftz(fmaf(z[nt][e], to_log2, -lev[nt][e & 1])) : 0.f;
+            if (edge) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = tok + r + 8 * (e >> 1), pos = len - qn + (nt * 8 + 2 * cq + (e & 1)) / G;
+                        if (t > pos || (p.window_left >= 0 && t < pos - p.window_left)) z[nt][e] = 0.f;
+                    }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                sum[0] += z[nt][0] + z[nt][1];
+                sum[1] += z[nt][2] + z[nt][3];
+            }
+            // lane cq 0 gets the first one's sum over the four lanes, cq 1 the second one's
+            const float give = cq & 1 ? sum[0] : sum[1], keep = cq & 1 ? sum[1] : sum[0];
+            w = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+            w += __shfl_xor_sync(0xffffffffu, w, 2);
         }
+        const int t = tok + r + 8 * cq;
+        if (cq < 2 && (!edge || t < len)) {
+            // this call's tokens have no score yet
+            *score_of(blk) = p.decay == 0.f || (edge && t >= len - qn) ? w : fmaf(p.decay, old, w);
+        }
+    };
+    for (int i = 0; i < mine_n; ++i) {
+        const int page = first + kWeightWarps * i;
+        blk_next = id(i + 1);
+        load(page + kWeightWarps, blk_next, next, old_next);
+        work(page, blk, cur, old_cur);
         cur = next;
         old_cur = old_next;
         blk = blk_next;
-        blk_next = check(after, blk_after);
     }
 }
 
 // Tiles: as many as fit on the GPU at once, or whole rounds of that where they would have more than kTilePages
 // pages (a tile's first page comes some three dependent loads after its CTA starts, and its
 // rows' statistics are read again, so few long ones), each a whole number of rounds of a CTA's warps.
-constexpr int kTilePages = 256;  // (4 x 100000 e2m1: 128 38.6 us, 256 35.0)
+constexpr int kTilePages = 32 * kWeightWarps;  // (their ids a lane each; 4 x 100000 e2m1: 128 pages 38.6 us, 256 35.0 at the time)
 
 template <typename T, int HEAD, int KV, int NT>
 bool launch_weights_rows(WeightParams& p, int sms, void* stream) {

@@ -11,7 +11,7 @@
 // One cluster of 1, 2, 4 or 8 CTAs works on a (sequence, kv head), each on a part of the tokens whose
 // keys it keeps in shared memory; the CTAs read each other's histograms there.  Little is read
 // (four bytes a token) and what bounds the call is the chain of dependent steps, so few steps
-// and short ones are what counts (GPU time, 4 kv heads: 32 x 4096 7.2 us, 4 x 100000 18.9).
+// and short ones are what counts (GPU time, 4 kv heads: 32 x 4096 6.5 us, 4 x 100000 16.7).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -29,6 +29,7 @@ constexpr int kBS = PA_BLOCK_SIZE;
 constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kQuads = 4;       // 16-byte loads of a thread in flight
+constexpr uint32_t kStays = 0xffffffffu;  // the key of a token that stays whatever its score: above every score's
 constexpr int kCached = 40960;  // keys that a CTA keeps (160 KB); longer parts are read again at every step
 
 struct SelectParams {
@@ -49,7 +50,8 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Sum of v over the threads before this one, and over all of them.
+// Sum of v over the threads before this one, and over all of them.  (Two calls in a row take different `warps`, so
+// one barrier is enough: no thread writes to one that another still reads.)
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warps, uint32_t& total) {
     static_assert(kThreads == 1024, "a lane for each warp");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -67,7 +69,6 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warps, uint
     const uint32_t w = warp_scan(warps[lane]);
     total = __shfl_sync(0xffffffffu, w, 31);
     const uint32_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-    __syncthreads();
     return (warp > 0 ? before : 0) + x - v;
 }
 
@@ -75,9 +76,9 @@ template <bool CACHED, int RANKS>
 __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams p) {
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ __align__(16) uint32_t hist[3][kBins];
-    __shared__ uint32_t warps[kThreads / 32];
-    __shared__ uint32_t found[2];   // digit of the threshold, how many above it
-    __shared__ uint32_t counts[2];  // this CTA's tokens that stay for sure, and those at the threshold
+    __shared__ uint32_t warps[2][kThreads / 32];
+    __shared__ uint32_t found[3][2];  // digit of the threshold, how many above it
+    __shared__ uint2 counts;          // this CTA's tokens that stay for sure, and those at the threshold
     cg::cluster_group cluster = cg::this_cluster();
     constexpr int ranks = RANKS;
     const int tid = threadIdx.x, rank = RANKS == 1 ? 0 : cluster.block_rank();
@@ -120,7 +121,6 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
         }
         return key_of(p.scores[((int64_t)blk * p.num_kv_heads + head) * kBS + t % kBS]);
     };
-    auto key_at = [&](int i) { return CACHED ? keys[i] : read(t0 + i); };
     __syncthreads();  // histograms zeroed
     if (CACHED && left > 0) {
         // the keys, four of a page at a time: the loads of a thread do not wait for each other
@@ -147,13 +147,16 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
             for (int k = 0; k < kQuads; ++k) {
                 const int i = i0 + k * kThreads + tid;
                 if (i >= quads) continue;
-                const uint32_t y[4] = {key_of(x[k].x), key_of(x[k].y), key_of(x[k].z), key_of(x[k].w)};
-                *reinterpret_cast<uint4*>(keys + 4 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+                uint32_t y[4] = {key_of(x[k].x), key_of(x[k].y), key_of(x[k].z), key_of(x[k].w)};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = t0 + 4 * i + e;
-                    if (t >= lo && t < hi) atomicAdd(&hist[0][y[e] >> 21], 1u);
+                    if (t >= lo && t < hi)
+                        atomicAdd(&hist[0][y[e] >> 21], 1u);
+                    else
+                        y[e] = kStays;
                 }
+                *reinterpret_cast<uint4*>(keys + 4 * i) = make_uint4(y[0], y[1], y[2], y[3]);
             }
         }
     }
@@ -165,12 +168,23 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const uint32_t known = pass == 0 ? 0 : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
             const uint32_t digits = pass == 2 ? 0x3ffu : 0x7ffu;
-            if (!CACHED || pass > 0) {
-#pragma unroll 4
-                for (int i = max(lo - t0, 0) + tid; i < min(mine, hi - t0); i += kThreads) {
-                    const uint32_t k = key_at(i);
-                    if ((k & known) == prefix) atomicAdd(&hist[pass][k >> shift & digits], 1u);
+            auto add = [&](uint32_t k) {
+                if ((k & known) == prefix) atomicAdd(&hist[pass][k >> shift & digits], 1u);
+            };
+            if constexpr (CACHED) {
+                if (pass > 0) {  // (kStays: no score has its first digit)
+#pragma unroll 2
+                    for (int i = tid; i < (mine + 3) / 4; i += kThreads) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(keys + 4 * i);
+                        add(v.x);
+                        add(v.y);
+                        add(v.z);
+                        add(v.w);
+                    }
                 }
+            } else {
+#pragma unroll 4
+                for (int i = max(lo - t0, 0) + tid; i < min(mine, hi - t0); i += kThreads) add(read(t0 + i));
             }
             sync_all();
             // every CTA adds up all histograms: two bins a thread, the highest first
@@ -184,19 +198,18 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
                 c[0] += h.y;
                 c[1] += h.x;
             }
-            uint32_t above = block_scan(c[0] + c[1], warps, total);
+            uint32_t above = block_scan(c[0] + c[1], warps[0], total);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (above < left && left <= above + c[i]) {
-                    found[0] = (uint32_t)(bin0 + 1 - i);
-                    found[1] = above;
+                    found[pass][0] = (uint32_t)(bin0 + 1 - i);
+                    found[pass][1] = above;
                 }
                 above += c[i];
             }
             __syncthreads();
-            prefix |= found[0] << shift;
-            left -= found[1];
-            __syncthreads();
+            prefix |= found[pass][0] << shift;
+            left -= found[pass][1];
         }
     }
     // Each thread takes `run` successive tokens of every round of the CTA's: bits of those that stay whatever the
@@ -209,35 +222,42 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
     auto look = [&](int round, uint32_t& sure, uint32_t& ties) {
         const int a = (round * kThreads + tid) * run, count = min(run, mine - a);
         sure = ties = 0;
-        for (int i = 0; i < count; i += 4) {
-            uint32_t k[4] = {0, 0, 0, 0};
-            if (CACHED && any) {
+        if (count <= 0) return;
+        if (CACHED && any) {
+            for (int i = run - 4; i >= 0; i -= 4) {
+                if (i >= count) continue;
                 const uint4 v = *reinterpret_cast<const uint4*>(keys + a + i);
-                k[0] = v.x;
-                k[1] = v.y;
-                k[2] = v.z;
-                k[3] = v.w;
-            }
+                const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+                sure <<= 4;
+                ties <<= 4;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = t0 + a + i + e;
-                if (i + e >= count) continue;
-                if (t < lo || t >= hi) {
-                    sure |= 1u << (i + e);
-                } else if (any) {
-                    if (!CACHED) k[e] = read(t);
-                    sure |= (uint32_t)(k[e] > prefix) << (i + e);
-                    ties |= (uint32_t)(k[e] == prefix) << (i + e);
+                for (int e = 0; e < 4; ++e) {
+                    if (k[e] > prefix) sure |= 1u << e;
+                    if (k[e] == prefix) ties |= 1u << e;
                 }
+            }
+            sure &= (1u << count) - 1;  // (behind the end: kStays)
+            return;
+        }
+        for (int i = 0; i < count; ++i) {
+            const int t = t0 + a + i;
+            if (t < lo || t >= hi) {
+                sure |= 1u << i;
+            } else if (any) {
+                const uint32_t k = read(t);
+                sure |= (uint32_t)(k > prefix) << i;
+                ties |= (uint32_t)(k == prefix) << i;
             }
         }
     };
     // Both counts in one scan: 28 tokens of 1024 threads are less than 2^16.
     static_assert(28 * kThreads < 65536, "two counts to a word");
     uint32_t sure = 0, ties = 0, before = 0, all = 0;
+    int turn = 0;
     auto count = [&](int round) {
         look(round, sure, ties);
-        before = block_scan(__popc(ties) << 16 | __popc(sure), warps, all);
+        turn ^= 1;
+        before = block_scan(__popc(ties) << 16 | __popc(sure), warps[turn], all);
     };
     uint32_t place = 0, at_threshold = 0;  // tokens that stay, and ties, of the CTAs before this one, then of this one's rounds
     auto taken = [&](uint32_t n) { return at_threshold < left ? min(n, left - at_threshold) : 0u; };  // of the next n ties
@@ -248,16 +268,16 @@ __global__ void __launch_bounds__(kThreads) pa_select_kernel(const SelectParams 
             all_sure += all & 0xffffu;
             all_ties += all >> 16;
         }
-        if (tid == 0) {
-            counts[0] = all_sure;
-            counts[1] = all_ties;
-        }
+        if (tid == 0) counts = make_uint2(all_sure, all_ties);
         cluster.sync();
-        for (int r = 0; r < rank; ++r) {
-            const uint32_t* c = cluster.map_shared_rank(counts, r);
-            const uint32_t s = c[0], e = c[1];
-            place += s + taken(e);
-            at_threshold += e;
+        uint2 c[RANKS];
+#pragma unroll
+        for (int r = 0; r < RANKS; ++r) c[r] = *cluster.map_shared_rank(&counts, r);
+#pragma unroll
+        for (int r = 0; r < RANKS; ++r) {
+            if (r >= rank) continue;
+            place += c[r].x + taken(c[r].y);
+            at_threshold += c[r].y;
         }
     }
     for (int round = 0; round < rounds; ++round) {

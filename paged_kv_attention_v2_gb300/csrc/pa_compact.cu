@@ -7,13 +7,13 @@
 // come before its stores: a CTA loads a chunk of 256 tokens into registers, waits at a barrier
 // and stores it, with the next chunk's loads already on their way.  No CTA waits for another:
 // what makes enough chains of few long sequences is that the pieces of a head do not depend on
-// each other: 64 bytes of a token's row (NHD), four of the 16-byte pieces of split keys, or 16 head
+// each other: 256 bytes of a token's row (NHD), four of the 16-byte pieces of split keys, or 16 head
 // dims of split values each make a chain of their own.
 // Which way lanes run follows the layout: along a token's row, or along the tokens where a page holds
 // [piece][token]; there successive tokens that stay are neighbours in the page, and a load takes
 // few sectors.  Measured: 32 x 16384 to 2048, 8 heads of 128, bf16 NHD 94 us (542 MB: 80 at the
-// copy rate); 32 x 4096 to 4032, 4 heads, fp16 split 108 (77), where the values' two-byte loads
-// are what takes longer (keys alone 46, values alone 66).
+// copy rate); 32 x 4096 to 4032, 4 heads, fp16 split 101 (77; with the values token by token, two
+// bytes to a load, 107).
 #include <cuda_runtime.h>
 
 #include <type_traits>

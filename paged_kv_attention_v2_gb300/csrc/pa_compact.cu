@@ -99,7 +99,7 @@ __device__ __forceinline__ void move_chain(const CompactParams& p, const Array& 
             } else if (kPairs || t.k > i) {
                 const int from = table[t.k / kBS], to = table[i / kBS];
                 if ((unsigned)from >= (unsigned)p.num_blocks || (unsigned)to >= (unsigned)p.num_blocks) {
-                    if (p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
+                    if (t.k > i && p.dev_error) atomicOr(p.dev_error, PA_DEVERR_BLOCK_ID);
                 } else {
                     src = from * arr.block_bytes + t.k % kBS * arr.token_step;
                     dst = to * arr.block_bytes + i % kBS * arr.token_step;

@@ -351,3 +351,59 @@ def test_compact_reports_what_it_does_not_move():
     err.zero_()
     pa.pa_compact_kv(k, k.clone(), _int([[0, 1, 2]]), _int([[[0, 1]]]), _int([9]), layout="nhd", dev_error=err)
     assert int(err) == pa.PA_DEVERR_SEQ_LEN
+
+
+@pytest.mark.parametrize("dtype,layout", [("f32", "split"), ("f16", "split"), ("e4m3", "split"), ("bf16", "nhd"), ("e5m2", "nhd"), ("e2m1", "nhd")])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_compact_moves_the_others(dtype, layout, seed):
+    """Entries that are refused, and pages that are not there, among ones that move: only those places stay as they were."""
+    rng = np.random.default_rng(seed)
+    n, heads, size, blocks = 1100, 2, 64, 100
+    pages = -(-n // 16)
+    table = rng.permutation(blocks)[:pages]
+    kept = np.stack([np.sort(rng.permutation(n)[:n - 14 - 300 * seed]) if seed else np.concatenate([np.arange(5), np.arange(5, n - 9) + 9])
+                     for _ in range(heads)])
+    count = kept.shape[1]
+    bad = rng.random(kept.shape) < 0.1
+    kept = np.where(bad, np.where(rng.random(kept.shape) < 0.5, np.arange(count) - 1, 16 * pages + 5), kept)
+    away = rng.permutation(pages)[:3]
+    table[away] = (blocks, -1, blocks + 70)
+    elem = {"f32": 4, "f16": 2, "bf16": 2}.get(dtype, 1)
+    kv = dtype if elem == 1 else None
+    shapes = (((blocks, heads, 9 * size),) * 2 if dtype == "e2m1" else cache_shapes(blocks, heads, size, heads, size, layout, elem))
+    bits = {1: np.uint8, 2: np.int16, 4: np.int32}[elem]
+    caches = [rng.integers(np.iinfo(bits).min, np.iinfo(bits).max, s, dtype=bits, endpoint=True) for s in shapes]
+    ok = np.zeros(kept.shape, dtype=bool)
+    for h in range(heads):
+        for i in range(count):
+            k = kept[h, i]
+            if k >= i and k > (kept[h, i - 1] if i else -1) and k < 16 * pages:
+                ok[h, i] = k == i or (0 <= table[k // 16] < blocks and 0 <= table[i // 16] < blocks)
+
+    def move(x, w, token):  # token(x, block, head, t): that token's elements of a cache, in place
+        for h in range(heads):
+            for i in np.flatnonzero(ok[h]):
+                if kept[h, i] != i:
+                    token(w, table[i // 16], h, i % 16)[...] = token(x, table[kept[h, i] // 16], h, kept[h, i] % 16)
+        return w
+    rows = lambda x, b, h, t: x[b, h, t]  # noqa: E731
+    if dtype == "e2m1":
+        places = [lambda x, b, h, t: x[b, h, :8 * size].reshape(16, size // 2)[t], lambda x, b, h, t: x[b, h, 8 * size:].reshape(16, size // 16)[t]]
+        want = [x.copy() for x in caches]
+        for place in places:
+            for x, w in zip(caches, want):
+                move(x, w, place)
+    elif layout == "nhd":
+        want = [move(x, x.copy(), rows) for x in caches]
+    else:
+        want = [move(caches[0], caches[0].copy(), lambda x, b, h, t: x[b, h, :, t]),
+                move(caches[1], caches[1].copy(), lambda x, b, h, t: x[b, h, :, t])]
+    gpu = [torch.from_numpy(c.copy()).to(DEV) for c in caches]
+    view = [g if dtype == "e2m1" else g.view(TORCH[dtype]) for g in gpu]
+    err = _int([0])
+    pa.pa_compact_kv(*view, _int(table[None]), _int(kept[None]), _int([count]), layout=layout, kv_dtype=kv, dev_error=err)
+    torch.cuda.synchronize()
+    assert int(err) == pa.PA_DEVERR_SLOT | pa.PA_DEVERR_BLOCK_ID
+    for g, w in zip(gpu, want):
+        same = g.cpu().numpy() == w
+        assert same.all(), np.argwhere(~same)[:4]

@@ -287,3 +287,20 @@ def test_a_query_beyond_fp16_is_clamped_and_reported():
                      dev_error=err, **ws)
         assert int(err) == (8 if flagged else 0), value  # PA_DEVERR_QUERY_RANGE
         assert torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,size,ctas", [(28, 4, 128, 3), (64, 4, 128, 2), (8, 2, 64, 3)])
+def test_plan(dtype, heads, kv_heads, size, ctas):
+    """pa_plan tells of a 4-bit call what it launches."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for lens, merged in (([4096] * 32, False), ([1500, 1100], True)):
+        q = torch.zeros((len(lens), heads, size), dtype=TORCH[dtype], device=DEV)
+        k = torch.zeros((4, kv_heads, 9 * size), dtype=torch.uint8, device=DEV)
+        ws = pa.alloc_workspace(len(lens), heads, size, max(lens), DEV, num_kv_heads=kv_heads)
+        g = pa.plan_for(q, q, k, k, torch.zeros((len(lens), 256), dtype=torch.int32, device=DEV),
+                        torch.zeros(len(lens), dtype=torch.int32, device=DEV), num_kv_heads=kv_heads, scale=0.1, max_seq_len=max(lens),
+                        layout="nhd", mode="v2", kv_dtype="e2m1", **ws)
+        tiles = kv_heads * len(lens) * -(-max(lens) // 512)
+        assert (g["mode"], g["ctas_per_sm"], g["merge_in_kernel"], g["kernels"]) == ("v2", ctas, merged, 1 if merged else 2)
+        assert 1 <= g["grid"] <= min(tiles, ctas * sms)

@@ -150,7 +150,7 @@ pa_status pa_append_kv(const pa_append_args* args, void* stream);
  * last query_start[s+1] - query_start[s] of the sequence (without query_start the last one),
  * are set to their weights and not added to, so a slot's former score does not matter; decay 0
  * sets every token (the scores of a prompt, by its last tokens).  Tokens outside the window
- * only fade.  Sums are fp32, in an order that does not depend on the run.  Places behind a
+ * only fade (with decay 1 pages before every row's window are not looked at).  Sums are fp32, in an order that does not depend on the run.  Places behind a
  * sequence's end keep their scores; a page whose block id is out of range is skipped
  * (PA_DEVERR_BLOCK_ID).  Each page belongs to one sequence: two that share one would both write
  * its scores.  num_kv_heads pages of keys of one block are less than 2^31 bytes.

@@ -261,10 +261,12 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
         if (qn != n && threadIdx.x == 0 && tile == 0 && kvh == 0) weights_report(p, PA_DEVERR_SEQ_LEN);
     }
     const int pages = (len + BS - 1) / BS, page0 = tile * p.tile_pages, page1 = min(page0 + p.tile_pages, pages);
-    if (page0 >= page1) return;
     const int G = p.group, GE = qn * G;
     // keys that some row sees: [seen0, len)
     const int seen0 = p.window_left >= 0 ? max(0, len - qn - p.window_left) : 0;
+    // pages before that keep their scores where nothing fades
+    const int from = p.decay == 1.f ? seen0 / BS : 0;
+    if (max(page0, from) >= page1) return;
 
     // this lane's places in block 0; a block further, block_bytes further
     const uint8_t* lane_keys = static_cast<const uint8_t*>(p.key_cache) + kvh * Page::kPageBytes + Page::offset(p, r, cq);
@@ -272,23 +274,25 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     float* lane_score = p.scores + kvh * BS + r + 8 * (cq & 1);
     auto score_of = [&](int blk) { return lane_score + (uint64_t)(uint32_t)blk * (uint32_t)(p.num_kv_heads * BS); };
     const int mine_n = (page1 - first + kWeightWarps - 1) / kWeightWarps;  // (up to 32; none: at most 0)
-    if (lane < mine_n && (unsigned)ids >= (unsigned)p.num_blocks) weights_report(p, PA_DEVERR_BLOCK_ID);
+    const int i0 = max(0, (from - first + kWeightWarps - 1) / kWeightWarps);
+    if (lane >= i0 && lane < mine_n && (unsigned)ids >= (unsigned)p.num_blocks) weights_report(p, PA_DEVERR_BLOCK_ID);
     if (lane >= mine_n || (unsigned)ids >= (unsigned)p.num_blocks) ids = -1;
     auto id = [&](int i) { return i < mine_n ? __shfl_sync(0xffffffffu, ids, i) : -1; };  // (out of range: -1)
     const int seen = GE > 0 ? seen0 : 0x7fffffff;
-    // A page's keys and this lane's old score: lanes with cq 0 and 1 own tokens r and r + 8.  A page that is not
-    // there, or that no row sees, is block 0 instead, read and not used (loads in branches, and each page's id read and
-    // looked at in its turn: 34.0 us against 32.0, 4 x 100000 e2m1).
+    // A page's keys and this lane's old score: lanes with cq 0 and 1 own tokens r and r + 8.  Of a page that is not
+    // there, or that no row sees, 4-bit keys are block 0's, read and not used (loads in a branch, and each page's id
+    // read and looked at in its turn: 34.0 us against 32.0, 4 x 100000); where a page is more bytes a branch is
+    // cheaper (the same in fp16 with a window of 4096, all scores fading: 39 us against 57).
     auto load = [&](int page, int blk, Page& k, float& old) {
-        const uint32_t b = (page + 1) * BS > seen ? max(blk, 0) : 0;
-        const uint64_t off = (uint64_t)b * p.block_bytes;
-        k.load(lane_keys + off, lane_scales + off, p);
+        const bool need = blk >= 0 && (page + 1) * BS > seen;
+        const uint64_t off = need ? (uint64_t)(uint32_t)blk * p.block_bytes : 0;
+        if (Page::kFp4 || need) k.load(lane_keys + off, lane_scales + off, p);
         old = *score_of(max(blk, 0));
     };
     Page cur, next;
     float old_cur = 0.f, old_next = 0.f;
-    int blk = id(0), blk_next = -1;
-    load(first, blk, cur, old_cur);
+    int blk = id(i0), blk_next = -1;
+    load(first + kWeightWarps * i0, blk, cur, old_cur);
 
     uint32_t q[NT][Page::kQWords], top = 0;
 #pragma unroll
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
             *score_of(blk) = p.decay == 0.f || (edge && t >= len - qn) ? w : fmaf(p.decay, old, w);
         }
     };
-    for (int i = 0; i < mine_n; ++i) {
+    for (int i = i0; i < mine_n; ++i) {
         const int page = first + kWeightWarps * i;
         blk_next = id(i + 1);
         load(page + kWeightWarps, blk_next, next, old_next);

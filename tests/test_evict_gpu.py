@@ -182,6 +182,28 @@ def test_weights_skip_pages_out_of_range():
     assert (s[0] == 5).all() and (s[2] == 5).all() and (s[1] > 5).all()
 
 
+@pytest.mark.parametrize("kv", [None, "e2m1"])
+def test_weights_do_not_look_at_pages_before_the_window_unless_they_fade(kv):
+    """300 tokens, the last 21 within the window: pages 0 to 16 have no token in it."""
+    q = torch.randn(1, 1, 64, device=DEV).half()
+    k = torch.zeros(20, 1, 9 * 64, dtype=torch.uint8, device=DEV) if kv else torch.zeros(20, 1, 16, 64, device=DEV).half()
+    one = torch.ones(1, 1, 1, device=DEV)
+    table = np.arange(20)
+    table[3] = 99
+    for decay, bit in ((1.0, 0), (0.5, pa.PA_DEVERR_BLOCK_ID)):
+        scores = torch.full((20, 1, 16), 5.0, device=DEV)
+        scores[6, 0, 2] = float("nan")
+        err = _int([0])
+        pa.pa_add_weights(scores, q, k, _int(table[None]), _int([300]), one, torch.zeros_like(one), num_kv_heads=1, scale=0.1, max_seq_len=320,
+                          layout="nhd", kv_dtype=kv, window_left=20, decay=decay, dev_error=err)
+        assert int(err) == bit
+        s = scores.cpu().flatten()
+        assert (s[300:] == 5).all() and s[299] == 1 and torch.isnan(s[98])  # zero keys: logits 0, weights exp(0) / 1
+        assert (s[279:299] == 5 * decay + 1).all() and (s[48:64] == 5).all()
+        rest = torch.cat([s[:48], s[64:98], s[99:279]])
+        assert (rest == 5 * decay).all()
+
+
 # ------------------------------------------------------------------ selection
 
 def _select(lens, heads, budgets, sink, recent, scores=None, seed=0, graph=False):

@@ -146,7 +146,8 @@ pa_status pa_append_kv(const pa_append_args* args, void* stream);
  *                          the sequence's query tokens of softmax(z)(t),
  * with the logits z of pa_decode (scale, softcap, alibi_slopes, sliding_window,
  * query_start as there).  exp_sums and max_logits are the statistics that pa_decode left in
- * PA_MODE_V2 for the same arguments (v1 leaves none), in the same shapes.  The tokens of this step, the
+ * PA_MODE_V2 for the same arguments, in the same shapes (v1, which PA_MODE_AUTO may run, leaves the
+ * workspace as it was: what an earlier call left there would be taken).  The tokens of this step, the
  * last query_start[s+1] - query_start[s] of the sequence (without query_start the last one),
  * are set to their weights and not added to, so a slot's former score does not matter; decay 0
  * sets every token (the scores of a prompt, by its last tokens).  Tokens outside the window
@@ -154,6 +155,10 @@ pa_status pa_append_kv(const pa_append_args* args, void* stream);
  * sequence's end keep their scores; a page whose block id is out of range is skipped
  * (PA_DEVERR_BLOCK_ID).  Each page belongs to one sequence: two that share one would both write
  * its scores.  num_kv_heads pages of keys of one block are less than 2^31 bytes.
+ *
+ * With alibi_slopes set relative_max in both calls.  Without it max_logits hold slope * position, and what
+ * their rounding to fp32 has lost is a factor on all weights of a row: off by up to 2^-23 * slope *
+ * seq_len (slope 0.8: 1e-4 at 1000 tokens, 1e-2 at 100000).
  */
 typedef struct pa_weights_args {
     float* scores;               /* [num_blocks][num_kv_heads][16], updated in place */
@@ -180,6 +185,7 @@ typedef struct pa_weights_args {
     int32_t kv_dtype;            /* pa_kv_dtype */
     float scale, softcap, k_scale;
     float decay;                 /* >= 0; 1: plain sums */
+    int32_t relative_max;        /* as the decode had it */
 } pa_weights_args;
 
 /* num_seqs == 0 or max_seq_len == 0 is a no-op. */

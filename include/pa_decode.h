@@ -230,6 +230,15 @@ typedef struct pa_decode_args {
      * touched only after that wait.  0 (a zero-initialised struct): every
      * input is read after the wait. */
     int32_t metadata_ready;
+    /* 1, with alibi_slopes: a v2 call leaves max_logits relative to the sequence's
+     * last token, max z_t - alibi_slopes[h] * (seq_lens[s] - 1).  At an absolute
+     * position a maximum is slope * position large and its rounding to fp32 loses
+     * up to 2^-23 * slope * seq_len, for which exp_sums (relative to the maximum
+     * before that rounding) do not make up; relative to the last token the
+     * maxima of the partitions that count are small (slopes >= 0).  For
+     * pa_add_weights, which takes either (its relative_max).  out, tmp_out and
+     * exp_sums are the same.  0 (a zero-initialised struct): absolute positions. */
+    int32_t relative_max;
 } pa_decode_args;
 
 /* Largest partition count per sequence for which the merge runs inside the

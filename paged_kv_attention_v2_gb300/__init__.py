@@ -121,7 +121,7 @@ def _pack(out, query, key_cache, value_cache, block_tables, seq_lens, num_kv_hea
           block_size=PA_BLOCK_SIZE, alibi_slopes=None, softcap=0.0, layout="split", mode="auto", exp_sums=None,
           max_logits=None, tmp_out=None, dev_error=None, event_begin=None, event_end=None, partition_counters=None,
           window_left=-1, kv_dtype=None, k_scale=1.0, v_scale=1.0, query_start=None, max_query_len=None,
-          seq_lens_host=None, tile_counters=None, metadata_ready=False):
+          seq_lens_host=None, tile_counters=None, metadata_ready=False, relative_max=False):
     """The packed argument struct, and the host lengths that its pointer needs alive."""
     num_rows, num_heads, head_size = query.shape
     num_seqs = seq_lens.shape[0]
@@ -165,7 +165,7 @@ def _pack(out, query, key_cache, value_cache, block_tables, seq_lens, num_kv_hea
         int(window_left) + 1 if window_left >= 0 else 0, _KV[kv_dtype], k_scale, v_scale, _ptr(query_start),
         num_rows if several else 0, int(max_query_len) if several else 0,
         0 if host_lens is None else host_lens.__array_interface__["data"][0], _ptr(tile_counters),
-        1 if metadata_ready else 0), host_lens
+        1 if metadata_ready else 0, 1 if relative_max else 0), host_lens
 
 
 def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: int,
@@ -176,7 +176,7 @@ def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num
               window_left: int = -1, kv_dtype: str | None = None, k_scale: float = 1.0,
               v_scale: float = 1.0, query_start=None,
               max_query_len: int | None = None, seq_lens_host=None,
-              tile_counters=None, metadata_ready: bool = False) -> _abi.PaDecodeArgs:
+              tile_counters=None, metadata_ready: bool = False, relative_max: bool = False) -> _abi.PaDecodeArgs:
     """Build the C argument struct.  The library validates sizes and types it can
     see; this also checks what only the tensors know: the caches' element size
     and element count against kv_dtype, head_size and num_kv_heads.
@@ -195,12 +195,13 @@ def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num
     zeroed once, e.g. from alloc_workspace(..., tile_counters=True)) turns on
     the dynamic tile schedule.  metadata_ready promises that no earlier kernel
     in the stream writes block_tables, seq_lens or query_start (the kernel may
-    read them before it waits for that kernel)."""
+    read them before it waits for that kernel).  relative_max, with alibi_slopes,
+    leaves max_logits relative to each sequence's last token (for pa_add_weights)."""
     packed, host_lens = _pack(
         out, query, key_cache, value_cache, block_tables, seq_lens, num_kv_heads, scale, max_seq_len, block_size,
         alibi_slopes, softcap, layout, mode, exp_sums, max_logits, tmp_out, dev_error, event_begin, event_end,
         partition_counters, window_left, kv_dtype, k_scale, v_scale, query_start, max_query_len, seq_lens_host,
-        tile_counters, metadata_ready)
+        tile_counters, metadata_ready, relative_max)
     a = _abi.PaDecodeArgs.from_buffer_copy(packed)
     a._keep_host_lens = host_lens  # the pointer inside stays valid as long as the struct lives
     return a

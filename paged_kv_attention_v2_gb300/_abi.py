@@ -85,6 +85,7 @@ class PaDecodeArgs(ctypes.Structure):
         ("seq_lens_host", ctypes.c_void_p),
         ("tile_counters", ctypes.c_void_p),
         ("metadata_ready", ctypes.c_int32),
+        ("relative_max", ctypes.c_int32),
     ]
 
 
@@ -193,6 +194,7 @@ class PaWeightsArgs(ctypes.Structure):
         ("softcap", ctypes.c_float),
         ("k_scale", ctypes.c_float),
         ("decay", ctypes.c_float),
+        ("relative_max", ctypes.c_int32),
     ]
 
 

@@ -423,6 +423,7 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
     p.block_tables = a->block_tables;
     p.seq_lens = a->seq_lens;
     p.alibi = a->alibi_slopes;
+    p.stat_alibi = a->relative_max ? nullptr : a->alibi_slopes;
     p.out = a->out;
     p.exp_sums = a->exp_sums;
     p.max_logits = a->max_logits;

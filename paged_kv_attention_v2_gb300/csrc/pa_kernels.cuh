@@ -86,6 +86,7 @@ struct Params {
     const int32_t* block_tables;
     const int32_t* seq_lens;
     const float* alibi;
+    const float* stat_alibi;  // alibi, or null: max_logits are left relative to the last token
     void* out;
     float* exp_sums;
     float* max_logits;
@@ -3010,8 +3011,8 @@ __global__ void __launch_bounds__(WARPS * 32) pa_reduce_kernel(const Params p) {
         }
         // statistics: sequence frame -> absolute ALiBi positions (every read of
         // max_logits above happened before the barrier)
-        if (p.alibi) {
-            const float shift = p.alibi[h] * (float)(len - 1);
+        if (p.stat_alibi) {
+            const float shift = p.stat_alibi[h] * (float)(len - 1);
             for (int q = p0 + tid; q < P; q += NT) ml[q] += shift;
         }
     }
@@ -3155,10 +3156,10 @@ __device__ __forceinline__ void merge_stats_row(const Params& p, int64_t srow, i
     // statistics: sequence frame -> absolute ALiBi positions; unused partitions
     // padded (every read of this row's statistics is above, in this warp)
     __syncwarp();
-    const float shift = p.alibi ? p.alibi[h] * (float)(len - 1) : 0.f;
+    const float shift = p.stat_alibi ? p.stat_alibi[h] * (float)(len - 1) : 0.f;
     for (int q = lane; q < p.max_parts; q += 32) {
         if (q >= p0 && q < P) {
-            if (p.alibi) ml[q] += shift;
+            if (p.stat_alibi) ml[q] += shift;
         } else {
             ml[q] = -INFINITY;
             es[q] = 0.f;
@@ -3309,11 +3310,11 @@ __device__ __forceinline__ void diff_merge_row(const Params& p, int64_t row, int
     // statistics: sequence frame -> absolute ALiBi positions; unused partitions
     // padded (every read of this row's statistics is above, in this warp)
     __syncwarp();
-    const float shift = p.alibi ? p.alibi[h] * (float)(len - 1) : 0.f;
+    const float shift = p.stat_alibi ? p.stat_alibi[h] * (float)(len - 1) : 0.f;
     for (int q = lane; q < 2 * p.max_parts; q += 32) {
         const int map = q >= p.max_parts, at = q - map * p.max_parts;
         if (at >= p0 && at < P) {
-            if (p.alibi) ml[map][at] += shift;
+            if (p.stat_alibi) ml[map][at] += shift;
         } else {
             ml[map][at] = -INFINITY;
             es[map][at] = 0.f;
@@ -3489,10 +3490,10 @@ __global__ void __launch_bounds__(WARPS * 32) pa_diff_reduce_kernel(const Params
     }
     // statistics: sequence frame -> absolute ALiBi positions, unused partitions
     // padded (every read of them above happened before the barrier)
-    const float shift = p.alibi ? p.alibi[h] * (float)(len - 1) : 0.f;
+    const float shift = p.stat_alibi ? p.stat_alibi[h] * (float)(len - 1) : 0.f;
     for (int q = tid; q < p.max_parts; q += HALF) {
         if (q >= p0 && q < P) {
-            if (p.alibi) ml[q] += shift;
+            if (p.stat_alibi) ml[q] += shift;
         } else {
             ml[q] = -INFINITY;
             es[q] = 0.f;

@@ -52,6 +52,7 @@ extern "C" pa_status pa_add_weights(const pa_weights_args* a, void* stream) {
     p.exp_sums = a->exp_sums;
     p.max_logits = a->max_logits;
     p.alibi = a->alibi_slopes;
+    p.relative_max = a->relative_max != 0;
     p.dev_error = a->dev_error;
     p.num_seqs = a->num_seqs;
     p.num_heads = a->num_heads;

@@ -43,6 +43,7 @@ struct WeightParams {
     const float* exp_sums;
     const float* max_logits;
     const float* alibi;
+    bool relative_max;  // the maxima leave slope x (length - 1) out
     int32_t* dev_error;
     int num_seqs, num_heads, num_kv_heads, group, num_blocks, max_blocks_per_seq, max_seq_len, max_parts;
     int max_q_len, num_q_rows, window_left, tile_pages, tiles;  // tiles of the longest sequence
@@ -327,8 +328,8 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
             M = top_m;
         }
         if (lane == 0) {
-            // the maxima hold slope x position: taken off in one rounding, as the logits below leave it out
-            if (p.alibi && v < GE) M = fmaf(-p.alibi[kvh * G + v % G], (float)(len - 1), M);
+            // maxima at absolute positions hold slope x position: taken off in one rounding, as the logits below leave it out
+            if (p.alibi && !p.relative_max && v < GE) M = fmaf(-p.alibi[kvh * G + v % G], (float)(len - 1), M);
             level[v] = M == -INFINITY ? INFINITY : M + logf(S);  // a row that sees no key: weights zero
         }
     }

@@ -105,7 +105,7 @@ def _pack_diff(out, query, key_cache, value_cache, block_tables, seq_lens, lambd
         window_left + 1 if window_left >= 0 else 0, _KV[kv_dtype], k_scale, v_scale,
         _ints("query_start", query_start, device, n + 1), tokens, most,
         0 if host is None else host.__array_interface__["data"][0], _ints("tile_counters", tile_counters, device, 2),
-        1 if metadata_ready else 0,
+        1 if metadata_ready else 0, 0,
         lam, stride, _floats("norm_weight", norm_weight, device, 2 * size), norm_eps, out_scale, 1 if norm else 0), host
 
 

@@ -3,7 +3,7 @@
     pa_decode(out, query, key_cache, value_cache, block_tables, seq_lens, mode="v2", **ws, ...)
     pa_add_weights(scores, query, key_cache, block_tables, seq_lens, ws["exp_sums"], ws["max_logits"], ...)
 
-after each step, and when a sequence has outgrown its budget
+after each step (with ALiBi both with relative_max=True), and when a sequence has outgrown its budget
 
     pa_select_tokens(kept, keep_lens, scores, block_tables, seq_lens, budgets, max_seq_len=..., sink=4, recent=64)
     pa_compact_kv(key_cache, value_cache, block_tables, kept, keep_lens, scores=scores)
@@ -34,7 +34,7 @@ def _check_cache(name: str, cache, types, numel: int, device: int, kv_dtype) -> 
 
 def _pack_weights(scores, query, key_cache, block_tables, seq_lens, exp_sums, max_logits, num_kv_heads, scale, max_seq_len,
                   decay, alibi_slopes, softcap, layout, window_left, kv_dtype, k_scale, query_start, max_query_len,
-                  dev_error) -> bytes:
+                  dev_error, relative_max) -> bytes:
     device, dtype = query.get_device(), query.dtype
     rows, heads, size = query.shape
     n = seq_lens.shape[0]
@@ -61,35 +61,40 @@ def _pack_weights(scores, query, key_cache, block_tables, seq_lens, exp_sums, ma
         0 if alibi_slopes is None else _floats("alibi_slopes", alibi_slopes, device, heads),
         _ints("query_start", query_start, device, n + 1), _ints("dev_error", dev_error, device, 1), n, heads, num_kv_heads,
         size, blocks, _PAGE, max_seq_len, block_tables.shape[1], tokens, most, window_left + 1 if window_left >= 0 else 0,
-        _DTYPE[dtype], _LAYOUT[layout], _KV[kv_dtype], scale, softcap, k_scale, decay)
+        _DTYPE[dtype], _LAYOUT[layout], _KV[kv_dtype], scale, softcap, k_scale, decay,
+        1 if relative_max else 0)
 
 
 def make_weights_args(scores, query, key_cache, block_tables, seq_lens, exp_sums, max_logits, *, num_kv_heads: int,
                       scale: float, max_seq_len: int, decay: float = 1.0, alibi_slopes=None, softcap: float = 0.0,
                       layout: str = "split", window_left: int = -1, kv_dtype: str | None = None, k_scale: float = 1.0,
-                      query_start=None, max_query_len: int | None = None, dev_error=None) -> _abi.PaWeightsArgs:
+                      query_start=None, max_query_len: int | None = None, dev_error=None,
+                      relative_max: bool = False) -> _abi.PaWeightsArgs:
     """Build the C argument struct of pa_add_weights (arguments as there)."""
     return _abi.PaWeightsArgs.from_buffer_copy(
         _pack_weights(scores, query, key_cache, block_tables, seq_lens, exp_sums, max_logits, num_kv_heads, scale,
                       max_seq_len, decay, alibi_slopes, softcap, layout, window_left, kv_dtype, k_scale, query_start,
-                      max_query_len, dev_error))
+                      max_query_len, dev_error, relative_max))
 
 
 def pa_add_weights(scores, query, key_cache, block_tables, seq_lens, exp_sums, max_logits, *, num_kv_heads: int,
                    scale: float, max_seq_len: int, decay: float = 1.0, alibi_slopes=None, softcap: float = 0.0,
                    layout: str = "split", window_left: int = -1, kv_dtype: str | None = None, k_scale: float = 1.0,
-                   query_start=None, max_query_len: int | None = None, dev_error=None, stream=None) -> None:
+                   query_start=None, max_query_len: int | None = None, dev_error=None, relative_max: bool = False,
+                   stream=None) -> None:
     """Add the attention weights of a decode to the score of every token it attended to.
 
     scores [num_blocks, num_kv_heads, 16] fp32, updated in place (decay times the old score
     plus the weights of the kv head's query heads; the step's own tokens, and with decay 0
     every token, are set); exp_sums and max_logits [rows, num_heads, partitions] as pa_decode
-    left them with mode="v2" for the same query, cache and options.  Everything else as
-    pa_decode; include/pa_cache.h has the formula.
+    left them with mode="v2" for the same query, cache and options (mode="auto" may run v1,
+    which leaves them as they were: the weights would then be an earlier call's).  With
+    alibi_slopes give relative_max=True to both calls: without it the weights are off by
+    up to 2^-23 * slope * length.  Everything else as pa_decode; include/pa_cache.h has the formula.
     """
     args = _pack_weights(scores, query, key_cache, block_tables, seq_lens, exp_sums, max_logits, num_kv_heads, scale,
                          max_seq_len, decay, alibi_slopes, softcap, layout, window_left, kv_dtype, k_scale, query_start,
-                         max_query_len, dev_error)
+                         max_query_len, dev_error, relative_max)
     _call("pa_add_weights", args, stream, query.get_device())
 
 

@@ -13,10 +13,11 @@ the library is missing.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import _abi
 from ._abi import (PA_BLOCK_SIZE, PA_DEVERR_BLOCK_ID, PA_DEVERR_POOL, PA_DEVERR_SEQ_LEN, PA_DEVERR_SLOT,
-                   PA_DEVERR_TIMEOUT, PA_PARTITION_SIZE, LibraryMissing)
+                   PA_DEVERR_TIMEOUT, PA_PARTITION_SIZE, LibraryMissing, sliding_window)
 
 __all__ = ["pa_decode", "pa_decode_static_workspace", "alloc_workspace", "max_num_partitions", "choose_mode",
            "plan", "plan_for", "status_str",
@@ -155,17 +156,23 @@ def _pack(out, query, key_cache, value_cache, block_tables, seq_lens, num_kv_hea
         if host_lens.shape != (num_seqs,):
             raise ValueError("seq_lens_host must hold num_seqs lengths")
     several = query_start is not None
-    return _DECODE.pack(
-        out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
-        seq_lens.data_ptr(), num_seqs, num_heads, num_kv_heads, head_size, num_blocks, block_size, max_seq_len,
-        block_tables.shape[1] if block_tables.dim() == 2 else 0, scale, softcap, _ptr(alibi_slopes),
-        _DTYPES[query.dtype], _LAYOUTS[layout], _MODES[mode], _ptr(exp_sums), _ptr(max_logits), _ptr(tmp_out),
-        _ptr(dev_error), 0 if event_begin is None else event_begin.cuda_event,
-        0 if event_end is None else event_end.cuda_event, _ptr(partition_counters),
-        int(window_left) + 1 if window_left >= 0 else 0, _KV[kv_dtype], k_scale, v_scale, _ptr(query_start),
-        num_rows if several else 0, int(max_query_len) if several else 0,
-        0 if host_lens is None else host_lens.__array_interface__["data"][0], _ptr(tile_counters),
-        1 if metadata_ready else 0, 1 if relative_max else 0), host_lens
+    try:
+        packed = _DECODE.pack(
+            out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+            seq_lens.data_ptr(), num_seqs, num_heads, num_kv_heads, head_size, num_blocks, block_size, max_seq_len,
+            block_tables.shape[1] if block_tables.dim() == 2 else 0, scale, softcap, _ptr(alibi_slopes),
+            _DTYPES[query.dtype], _LAYOUTS[layout], _MODES[mode], _ptr(exp_sums), _ptr(max_logits), _ptr(tmp_out),
+            _ptr(dev_error), 0 if event_begin is None else event_begin.cuda_event,
+            0 if event_end is None else event_end.cuda_event, _ptr(partition_counters),
+            sliding_window(window_left), _KV[kv_dtype], k_scale, v_scale, _ptr(query_start),
+            num_rows if several else 0, int(max_query_len) if several else 0,
+            0 if host_lens is None else host_lens.__array_interface__["data"][0], _ptr(tile_counters),
+            1 if metadata_ready else 0, 1 if relative_max else 0)
+    except struct.error as e:  # something that is no number, or a size beyond 32 bits
+        if str(e).startswith("required argument"):
+            raise TypeError(str(e)) from None
+        raise PaDecodeError(_abi.PA_ERR_INVALID_ARG) from None
+    return packed, host_lens
 
 
 def make_args(out, query, key_cache, value_cache, block_tables, seq_lens, *, num_kv_heads: int,

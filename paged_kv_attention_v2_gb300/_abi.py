@@ -244,6 +244,12 @@ class PaCompactArgs(ctypes.Structure):
     ]
 
 
+def sliding_window(window_left: int) -> int:
+    """The structs' sliding_window of a window_left: 0 (off) for negative ones, and for ones
+    that reach over any length."""
+    return int(window_left) + 1 if 0 <= window_left < 2 ** 31 - 1 else 0
+
+
 _CODES = {ctypes.c_void_p: "P", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f"}
 
 

@@ -60,7 +60,7 @@ def _pack_weights(scores, query, key_cache, block_tables, seq_lens, exp_sums, ma
         _floats("exp_sums", exp_sums, device, stats), _floats("max_logits", max_logits, device, stats),
         0 if alibi_slopes is None else _floats("alibi_slopes", alibi_slopes, device, heads),
         _ints("query_start", query_start, device, n + 1), _ints("dev_error", dev_error, device, 1), n, heads, num_kv_heads,
-        size, blocks, _PAGE, max_seq_len, block_tables.shape[1], tokens, most, window_left + 1 if window_left >= 0 else 0,
+        size, blocks, _PAGE, max_seq_len, block_tables.shape[1], tokens, most, _abi.sliding_window(window_left),
         _DTYPE[dtype], _LAYOUT[layout], _KV[kv_dtype], scale, softcap, k_scale, decay,
         1 if relative_max else 0)
 

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -443,7 +444,8 @@ pa_status prepare(const pa_decode_args* a, void* stream, Prepared& pr, const pa_
     p.softcap = a->softcap > 0.f ? a->softcap : 0.f;
     p.inv_softcap = a->softcap > 0.f ? 1.f / a->softcap : 0.f;
     p.counters = a->partition_counters;
-    p.window_left = a->sliding_window > 0 ? a->sliding_window - 1 : -1;
+    // (a window over any length is one of max_seq_len; a position, -16 at least, minus the window stays in 32 bits)
+    p.window_left = a->sliding_window > 0 ? std::min(a->sliding_window - 1, std::min(a->max_seq_len, INT32_MAX - 16)) : -1;
     p.query_start = a->query_start;
     p.max_q_len = max_q;
     p.num_q_rows = multi ? a->num_query_tokens : a->num_seqs;

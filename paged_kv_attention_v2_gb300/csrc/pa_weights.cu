@@ -1,5 +1,6 @@
 // pa_weights.cu -- pa_add_weights (pa_weights.cuh): argument checks, tiles, launch; the
 // fp32 kernels.
+#include <algorithm>
 #include <cmath>
 
 #include "pa_weights.cuh"
@@ -64,7 +65,8 @@ extern "C" pa_status pa_add_weights(const pa_weights_args* a, void* stream) {
     p.max_parts = pa_max_num_partitions(a->max_seq_len);
     p.max_q_len = most;
     p.num_q_rows = multi ? a->num_query_tokens : a->num_seqs;
-    p.window_left = a->sliding_window > 0 ? a->sliding_window - 1 : -1;
+    // (a window over any length is one of max_seq_len: positions minus the window stay in 32 bits)
+    p.window_left = a->sliding_window > 0 ? std::min(a->sliding_window - 1, a->max_seq_len) : -1;
     p.scale = a->scale * (kv != PA_KV_SAME && a->k_scale > 0.f ? a->k_scale : 1.f);
     p.softcap = a->softcap > 0.f ? a->softcap : 0.f;
     p.inv_softcap = a->softcap > 0.f ? 1.f / a->softcap : 0.f;

@@ -95,6 +95,9 @@ typedef enum pa_kv_dtype {
  * head_size / 16 e4m3 scales, one for every 16 successive elements:
  *     K(t)[i] = k_scale * scale(t, i / 16) * code(t, i),   V likewise with v_scale.
  * A scale that is NaN makes its 16 elements NaN.
+ *
+ * fp8 and 4-bit caches multiply in fp16: the elements of a bf16 query become fp16 numbers, beyond 65504
+ * that number (PA_DEVERR_QUERY_RANGE), below 2^-14 rounded to multiples of 2^-24.
  */
 typedef enum pa_layout { PA_LAYOUT_SPLIT = 0, PA_LAYOUT_NHD = 1 } pa_layout;
 

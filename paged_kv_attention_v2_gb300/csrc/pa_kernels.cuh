@@ -1912,12 +1912,16 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
     }
 }
 
-// Consumer for 4-bit caches.  Bound by issue slots: a page is 1152 bytes each of K and V (head
-// size 128) and 390 instructions of a warp with its share of the tile's ends, of which 64 turn
-// codes into fp16 and 64 multiply by scales (4 x 100000, groups of seven, bf16: 64 us, 34 at
-// the copy rate; the pages streamed and not worked on 41).  Tensor-core inputs are fp16 for both query types, as in the
-// fp8 consumer, with code x block scale in fp16 (exact) and k_scale, v_scale folded
-// into the logit scale and the epilogue.
+// Consumer for 4-bit caches.  Bound by its instructions and their latencies: a page is 1152 bytes each
+// of K and V (head size 128) and 390 instructions of a warp with its share of the tile's ends, of
+// which 64 turn codes into fp16 and 64 multiply by scales, issued in 0.56 of the cycles by three
+// warps to a scheduler, each a chain of loads, conversions, MMAs and exponentials (4 x 100000, groups
+// of seven, bf16: 64 us, 34 at the copy rate; the pages streamed and not worked on 41).  Tensor-core
+// inputs are fp16 for both query types, as in the fp8 consumer, with code x block scale in fp16
+// (exact) and k_scale, v_scale folded into the logit scale and the epilogue.  The softmax weights go to
+// P.V as one fp16 term, as there (their sum is fp32, unrounded): half a step of 2^-11 of each weight,
+// which stays below the step of a 16-bit output (fp16, 32 x 4096: 2.7e-4 from 64 bits at most, where
+// rounding the output alone is 2.1e-4); a second term would be 32 more MMAs a page.
 //
 // A page is read as it lies in memory, without a transposition: the reduction index of an
 // MMA and the rows of its result may be in any order, and here they follow the page.

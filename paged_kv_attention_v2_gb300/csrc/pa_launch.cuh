@@ -91,7 +91,7 @@ cudaError_t launch_main(const Params& p_in, const LaunchArgs& la, bool* fused) {
     // CTA is free, so no CTA waits on a fixed share.
     if (!p_in.tile_ctr) {
         const int64_t rounds = (la.tiles_upper + grid - 1) / grid, cut = (la.tiles_upper + rounds - 1) / rounds;
-        // 4-bit caches: bound by the SMs' issue slots, not by a CTA's stream.  The CTAs of an SM share those, so
+        // 4-bit caches: bound by the instructions of an SM's warps, not by a CTA's stream.  Its CTAs share those, so
         // what counts is the tiles of the busiest SM; a cut that leaves some SMs a CTA more than others
         // can raise them (1024 tiles: 342 CTAs x 3, nine on some SMs; 456 CTAs: seven).
         const int64_t sms = la.sm_count;

@@ -78,7 +78,7 @@ extern "C" pa_status pa_add_weights(const pa_weights_args* a, void* stream) {
     const int elem = kv != PA_KV_SAME ? 1 : (a->dtype == PA_DTYPE_F32 ? 4 : 2);
     p.token_step = a->layout == PA_LAYOUT_NHD ? a->head_size * elem : 16;
     p.piece_step = a->layout == PA_LAYOUT_NHD ? 16 : 16 * PA_BLOCK_SIZE;
-    // (grid: at least 2048 tokens a tile, checked for any tile size)
+    // (grid: the CTAs that fit on the GPU once, or for larger batches at most 1 + max_seq_len / 2048 tiles, twice that with rounding, a head)
     if ((int64_t)a->num_seqs * a->num_kv_heads > 0x7fffffffLL / (1 + (a->max_seq_len >> 11)) / 2) return PA_ERR_UNSUPPORTED;
     const int kvk = kv == PA_KV_SAME ? pa::kWSame : kv == PA_KV_FP8_E4M3 ? pa::kWE4M3 : kv == PA_KV_FP8_E5M2 ? pa::kWE5M2 : pa::kWE2M1;
     const bool ok = a->dtype == PA_DTYPE_F32   ? pa::launch_weights_f32(p, a->head_size, sms, stream)

@@ -16,7 +16,9 @@
 // fp16 38 us; a ring of asynchronous copies in shared memory 41 to 46.)  Four lanes then
 // share a token's sum; no atomics, so results do not depend on the run.
 // Measured: 32 x 4096 fp16, groups of seven, 24.6 us (139 MB: 20.4 at the copy rate; bound by
-// memory), 4 x 100000 over 4-bit keys 31.5 (18.9; by issue slots).
+// memory), 4 x 100000 over 4-bit keys 31.5 (18.9; issued in 0.62 of the cycles, 216 instructions of
+// a warp per page).  Tiles are cut for max_seq_len: with a window few of them have work (4 x 100000
+// fp16, window of 4096: 23 us, its bytes 2.5), and of a ragged batch the longest sequence's have most.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) pa_weights_kernel(const Wei
     // A page's keys and this lane's old score: lanes with cq 0 and 1 own tokens r and r + 8.  Of a page that is not
     // there, or that no row sees, 4-bit keys are block 0's, read and not used (loads in a branch, and each page's id
     // read and looked at in its turn: 34.0 us against 32.0, 4 x 100000); where a page is more bytes a branch is
-    // cheaper (the same in fp16 with a window of 4096, all scores fading: 39 us against 57).
+    // cheaper (the same in fp16 with a window of 4096, all scores fading: 37 us, against 57 at the time).
     auto load = [&](int page, int blk, Page& k, float& old) {
         const bool need = blk >= 0 && (page + 1) * BS > seen;
         const uint64_t off = need ? (uint64_t)(uint32_t)blk * p.block_bytes : 0;

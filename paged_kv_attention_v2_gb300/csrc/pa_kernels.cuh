@@ -1919,9 +1919,9 @@ __device__ void consumer_mma_fp8(const Params& p, const Smem& sm, int warp, int 
 // of seven, bf16: 64 us, 34 at the copy rate; the pages streamed and not worked on 41).  Tensor-core
 // inputs are fp16 for both query types, as in the fp8 consumer, with code x block scale in fp16
 // (exact) and k_scale, v_scale folded into the logit scale and the epilogue.  The softmax weights go to
-// P.V as one fp16 term, as there (their sum is fp32, unrounded): half a step of 2^-11 of each weight,
-// which stays below the step of a 16-bit output (fp16, 32 x 4096: 2.7e-4 from 64 bits at most, where
-// rounding the output alone is 2.1e-4); a second term would be 32 more MMAs a page.
+// P.V as one fp16 term, as there (their sum is fp32, unrounded): each weight is off by at most 2^-11 of
+// itself, independently of the others, so that an output's rounding outweighs it (fp16, 32 x 4096, root
+// mean square against 64 bits: 2.8e-4 of the outputs', and 2.1e-4 from rounding the output alone).
 //
 // A page is read as it lies in memory, without a transposition: the reduction index of an
 // MMA and the rows of its result may be in any order, and here they follow the page.

@@ -3,6 +3,7 @@ absolute position (slope x position) has few bits left: relative_max keeps them.
 softmax in 64 bits."""
 from __future__ import annotations
 
+import ctypes
 import math
 
 import numpy as np
@@ -160,3 +161,34 @@ def test_without_slopes_the_flag_changes_nothing():
     a = _run("bf16", "e2m1", "nhd", 64, 1, [5000, 40], [0.0] * 4, relative=False)
     b = _run("bf16", "e2m1", "nhd", 64, 1, [5000, 40], [0.0] * 4)
     assert torch.equal(a[0], b[0]) and torch.equal(a[2]["max_logits"], b[2]["max_logits"])
+
+
+@pytest.mark.parametrize("n,tokens,counters", [(3, 40001, False), (2, 3000, True), (40, 1500, False)])
+def test_differential_statistics_follow_the_flag(n, tokens, counters):
+    """pa_diff_decode leaves its statistics by the same field: the outputs and sums are the same, the maxima those
+    without the shift."""
+    from paged_kv_attention_v2_gb300 import _abi, diff
+    gen = torch.Generator().manual_seed(tokens)
+    heads, size, pages = 4, 64, -(-tokens // 16)
+    q = torch.randn((n, heads, 2, size), generator=gen).half().to(DEV)
+    k = torch.randn((pages, 2 * heads, 16, size), generator=gen).half().to(DEV)
+    v = torch.randn((pages, heads, 16, 2 * size), generator=gen).half().to(DEV)
+    table, lens = _int(np.tile(np.arange(pages), (n, 1))), _int([tokens] * n)
+    slope, lam = torch.tensor(STEEP[:heads], device=DEV), torch.rand(heads, generator=gen).to(DEV)
+    results = []
+    for flag in (0, 1):
+        ws = pa.alloc_diff_workspace(n, heads, size, tokens, DEV, num_seqs=n if counters else None, num_kv_heads=heads if counters else None)
+        out, err = torch.empty((n, heads, 2 * size), dtype=q.dtype, device=DEV), _int([0])
+        a = diff.make_diff_args(out, q, k, v, table, lens, lambdas=lam, num_kv_heads=heads, scale=size ** -0.5, max_seq_len=tokens,
+                                alibi_slopes=slope, layout="nhd", mode="v2", dev_error=err, **ws)
+        a.decode.relative_max = flag
+        plan = diff.diff_plan(a)
+        assert _abi.load().pa_diff_decode(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == _abi.PA_OK
+        torch.cuda.synchronize()
+        assert int(err) == 0 and plan["mode"] == "v2"
+        parts = -(-tokens // plan["partition_tokens"])
+        results.append((out, *(ws[x].flatten()[:n * heads * 2 * parts].view(n, heads, 2, parts) for x in ("exp_sums", "max_logits"))))
+    (oa, ea, ma), (ob, eb, mb) = results
+    assert torch.equal(oa, ob) and torch.equal(ea, eb) and bool(torch.isfinite(mb).all())
+    shift = slope.double()[None, :, None, None] * (tokens - 1)
+    assert bool(((ma.double() - mb.double() - shift).abs() <= 2.0 ** -23 * (shift + mb.double().abs() + 8)).all())
